@@ -627,6 +627,277 @@ int attn_bwd(const void* q, const void* k, const void* v, const void* out, const
   return EXATTN_OK;
 }
 
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kMaxTokens = 0x7FFFFFFF;
+
+// Sections and base of attn_rope_axes and the 4-bit append, as the kernels'
+// table: fixed-point frequency and axis of each pair.
+int rope_table(const int* sections, int num_axes, int d, float base, int per_axis, exattn::RopeAxesTable* out) {
+  if (sections == nullptr || num_axes < 1 || num_axes > exattn::kRopeMaxAxes) return EXATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(base) || !(base > 1.f)) return EXATTN_ERR_INVALID_ARG;
+  int sum = 0;
+  for (int a = 0; a < num_axes; ++a) {
+    if (sections[a] < 0 || sections[a] > d / 2) return EXATTN_ERR_INVALID_ARG;
+    sum += sections[a];
+  }
+  if (sum != d / 2) return EXATTN_ERR_INVALID_ARG;
+  const double log2_base = std::log2(static_cast<double>(base));
+  int i = 0;
+  for (int a = 0; a < num_axes; ++a)
+    for (int j = 0; j < sections[a]; ++j, ++i) {
+      const double power = per_axis ? static_cast<double>(j) / sections[a] : 2.0 * i / d;
+      // theta / (2 pi) * 2^64, below 2^62, rounded to an integer
+      out->u[i] = static_cast<unsigned long long>(
+          std::nearbyint(std::exp2(-power * log2_base) * (18446744073709551616.0 / 6.283185307179586476925)));
+      out->axis[i] = static_cast<unsigned char>(a);
+    }
+  return EXATTN_OK;
+}
+
+// A [batch, heads, tokens, d] bf16 tensor by its element strides: every
+// stride that is used has to keep rows on 16-byte boundaries.  An output's rows
+// must also lie apart: each dimension's stride is at least what the
+// dimensions of smaller stride span.
+int head_view(const void* ptr, int64_t batch, int64_t head, int64_t token, int64_t B, int64_t H, int64_t N, int d,
+              bool output, exattn::HeadView* out) {
+  int64_t stride[3] = {batch, head, token}, size[3] = {B, H, N};
+  for (int x = 0; x < 3; ++x) {
+    if (size[x] <= 1) stride[x] = 0;  // never used
+    if (stride[x] < 0 || stride[x] > (int64_t{1} << 40)) return EXATTN_ERR_INVALID_ARG;
+    if (stride[x] % 8 != 0) return EXATTN_ERR_ALIGNMENT;
+  }
+  out->ptr = ptr;
+  out->batch = stride[0] / 8;
+  out->head = stride[1] / 8;
+  out->token = stride[2] / 8;
+  if (!output) return EXATTN_OK;
+  int64_t span = d;
+  for (int pass = 0; pass < 3; ++pass) {  // dimensions by ascending stride
+    int low = -1;
+    for (int x = 0; x < 3; ++x)
+      if (size[x] > 1 && (low < 0 || stride[x] < stride[low])) low = x;
+    if (low < 0) break;
+    if (stride[low] < span) return EXATTN_ERR_INVALID_ARG;
+    span += (size[low] - 1) * stride[low];
+    size[low] = 1;
+  }
+  return EXATTN_OK;
+}
+
+bool same_view(const exattn::HeadView& a, const exattn::HeadView& b) {
+  return a.batch == b.batch && a.head == b.head && a.token == b.token;
+}
+
+// Sizes that the 4-bit cache calls share.
+int fp4_sizes(int Hkv, int d, int num_blocks, int num_seqs, int max_blocks_per_seq) {
+  if (Hkv < 1 || num_blocks < 1 || num_seqs < 1 || max_blocks_per_seq < 1) return EXATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return EXATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(max_blocks_per_seq) * exattn::kDecodeBlockSize > (1 << 30)) return EXATTN_ERR_UNSUPPORTED;
+  return EXATTN_OK;
+}
+
+int status_word(unsigned int** status) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev;
+  return device_state(&dev, status);
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions,
+                   const int64_t* strides, const int* sections, int num_axes, int B, int Hq, int Hkv, int N, int d,
+                   float base, int per_axis, int inverse, void* stream) {
+  if (B < 0 || N < 0 || Hq < 0 || Hkv < 0 || strides == nullptr) return EXATTN_ERR_INVALID_ARG;
+  if (d < 16 || d > exattn::kRopeMaxDim || d % 16 != 0) return EXATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(B) * N > kMaxTokens || Hq > 65535 || Hkv > 65535) return EXATTN_ERR_UNSUPPORTED;
+  exattn::RopeAxesTable table;
+  int rc = rope_table(sections, num_axes, d, base, per_axis, &table);
+  if (rc != EXATTN_OK) return rc;
+  if (B == 0 || N == 0 || Hq + Hkv == 0) return EXATTN_OK;
+  if (positions == nullptr || (Hq > 0 && (q == nullptr || q_out == nullptr)) ||
+      (Hkv > 0 && (k == nullptr || k_out == nullptr)) || (Hq > 0 && Hkv > 0 && q_out == k_out))
+    return EXATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || !aligned4(positions))
+    return EXATTN_ERR_ALIGNMENT;
+  exattn::RopeAxesArgs a;
+  const int64_t* s = strides;
+  if ((rc = head_view(q, s[0], s[1], s[2], B, Hq, N, d, false, &a.q)) != EXATTN_OK ||
+      (rc = head_view(k, s[3], s[4], s[5], B, Hkv, N, d, false, &a.k)) != EXATTN_OK ||
+      (rc = head_view(q_out, s[6], s[7], s[8], B, Hq, N, d, true, &a.q_out)) != EXATTN_OK ||
+      (rc = head_view(k_out, s[9], s[10], s[11], B, Hkv, N, d, true, &a.k_out)) != EXATTN_OK)
+    return rc;
+  // in place means the same rows
+  if ((Hq > 0 && q == q_out && !same_view(a.q, a.q_out)) || (Hkv > 0 && k == k_out && !same_view(a.k, a.k_out)))
+    return EXATTN_ERR_INVALID_ARG;
+  a.positions = positions;
+  a.pos_axis = s[12];
+  a.pos_batch = s[13];
+  a.pos_token = s[14];
+  if (a.pos_axis < 0 || a.pos_batch < 0 || a.pos_token < 0) return EXATTN_ERR_INVALID_ARG;
+  a.B = static_cast<unsigned int>(B);
+  a.N = static_cast<unsigned int>(N);
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.inverse = inverse ? 1 : 0;
+  return exattn::launch_rope_axes(a, table, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXATTN_OK
+                                                                                              : EXATTN_ERR_CUDA;
+}
+
+size_t attn_fp4_cache_bytes(int num_blocks, int Hkv, int d) {
+  if (num_blocks < 1 || Hkv < 1 || (d != 64 && d != 128)) return 0;
+  return static_cast<size_t>(num_blocks) * Hkv * 18 * d;
+}
+
+int attn_rope_cache_write_fp4(const void* q, const void* k, const void* v, void* q_out, const int32_t* seq_ids,
+                              const int32_t* slots, const int32_t* positions, const int32_t* block_table,
+                              void* kv_cache, const int64_t* strides, const int* sections, int num_axes,
+                              int num_tokens, int Hq, int Hkv, int d, int num_seqs, int num_blocks,
+                              int max_blocks_per_seq, float base, int per_axis, float k_scale, float v_scale,
+                              void* stream) {
+  if (num_tokens < 0 || Hq < 0 || strides == nullptr) return EXATTN_ERR_INVALID_ARG;
+  int rc = fp4_sizes(Hkv, d, num_blocks, num_seqs, max_blocks_per_seq);
+  if (rc != EXATTN_OK) return rc;
+  if (Hq > 65535 || Hkv > 65535) return EXATTN_ERR_UNSUPPORTED;
+  if (!good_scale(k_scale) || !good_scale(v_scale)) return EXATTN_ERR_INVALID_ARG;
+  exattn::RopeAxesTable table;
+  if ((rc = rope_table(sections, num_axes, d, base, per_axis, &table)) != EXATTN_OK) return rc;
+  if (num_tokens == 0) return EXATTN_OK;
+  if ((Hq > 0 && (q == nullptr || q_out == nullptr)) || k == nullptr || v == nullptr || seq_ids == nullptr ||
+      slots == nullptr || positions == nullptr || block_table == nullptr || kv_cache == nullptr)
+    return EXATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) || !aligned16(kv_cache) ||
+      !aligned4(seq_ids) || !aligned4(slots) || !aligned4(positions) || !aligned4(block_table))
+    return EXATTN_ERR_ALIGNMENT;
+  exattn::RopeFp4Args a;
+  const int64_t* s = strides;
+  if ((rc = head_view(q, 0, s[1], s[0], 1, Hq, num_tokens, d, false, &a.q)) != EXATTN_OK ||
+      (rc = head_view(k, 0, s[3], s[2], 1, Hkv, num_tokens, d, false, &a.k)) != EXATTN_OK ||
+      (rc = head_view(v, 0, s[5], s[4], 1, Hkv, num_tokens, d, false, &a.v)) != EXATTN_OK ||
+      (rc = head_view(q_out, 0, s[7], s[6], 1, Hq, num_tokens, d, true, &a.q_out)) != EXATTN_OK)
+    return rc;
+  if (Hq > 0 && q == q_out && !same_view(a.q, a.q_out)) return EXATTN_ERR_INVALID_ARG;
+  a.positions = positions;
+  a.pos_axis = s[8];
+  if (a.pos_axis < 0) return EXATTN_ERR_INVALID_ARG;
+  if ((rc = status_word(&a.at.status)) != EXATTN_OK) return rc;
+  a.kv_cache = kv_cache;
+  a.at.seq_ids = seq_ids;
+  a.at.slots = slots;
+  a.at.block_table = block_table;
+  a.at.num_tokens = num_tokens;
+  a.at.num_seqs = num_seqs;
+  a.at.num_blocks = num_blocks;
+  a.at.max_blocks_per_seq = max_blocks_per_seq;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return exattn::launch_rope_cache_write_fp4(a, table, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? EXATTN_OK
+             : EXATTN_ERR_CUDA;
+}
+
+int attn_cache_read_fp4(const void* kv_cache, const int32_t* seq_ids, const int32_t* slots,
+                        const int32_t* block_table, void* k_out, void* v_out, const int64_t* strides, int num_tokens,
+                        int Hkv, int d, int num_seqs, int num_blocks, int max_blocks_per_seq, float k_scale,
+                        float v_scale, void* stream) {
+  if (num_tokens < 0 || strides == nullptr) return EXATTN_ERR_INVALID_ARG;
+  int rc = fp4_sizes(Hkv, d, num_blocks, num_seqs, max_blocks_per_seq);
+  if (rc != EXATTN_OK) return rc;
+  if (Hkv > 65535) return EXATTN_ERR_UNSUPPORTED;
+  if (!good_scale(k_scale) || !good_scale(v_scale)) return EXATTN_ERR_INVALID_ARG;
+  if (num_tokens == 0) return EXATTN_OK;
+  if (kv_cache == nullptr || seq_ids == nullptr || slots == nullptr || block_table == nullptr || k_out == nullptr ||
+      v_out == nullptr || k_out == v_out)
+    return EXATTN_ERR_INVALID_ARG;
+  if (!aligned16(kv_cache) || !aligned16(k_out) || !aligned16(v_out) || !aligned4(seq_ids) || !aligned4(slots) ||
+      !aligned4(block_table))
+    return EXATTN_ERR_ALIGNMENT;
+  exattn::ReadFp4Args a;
+  if ((rc = head_view(k_out, 0, strides[1], strides[0], 1, Hkv, num_tokens, d, true, &a.k_out)) != EXATTN_OK ||
+      (rc = head_view(v_out, 0, strides[3], strides[2], 1, Hkv, num_tokens, d, true, &a.v_out)) != EXATTN_OK)
+    return rc;
+  if ((rc = status_word(&a.at.status)) != EXATTN_OK) return rc;
+  a.kv_cache = kv_cache;
+  a.at.seq_ids = seq_ids;
+  a.at.slots = slots;
+  a.at.block_table = block_table;
+  a.at.num_tokens = num_tokens;
+  a.at.num_seqs = num_seqs;
+  a.at.num_blocks = num_blocks;
+  a.at.max_blocks_per_seq = max_blocks_per_seq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return exattn::launch_cache_read_fp4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXATTN_OK
+                                                                                            : EXATTN_ERR_CUDA;
+}
+
+size_t attn_decode_fp4_workspace_bytes(int num_seqs, int Hq, int Hkv, int d, int max_blocks_per_seq) {
+  if (num_seqs < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128) || max_blocks_per_seq < 1) return 0;
+  const size_t splits =
+      static_cast<size_t>(exattn::fp4_decode_splits(num_seqs, Hkv, Hq / Hkv, max_blocks_per_seq));
+  if (splits == 1) return 0;
+  const size_t rows = static_cast<size_t>(num_seqs) * Hq * splits;
+  return rows * d * sizeof(float) + ((rows * sizeof(float) + 15) & ~static_cast<size_t>(15));
+}
+
+int attn_decode_paged_fp4(const void* q, const void* kv_cache, const int32_t* block_table, const int32_t* ctx_lens,
+                          void* out, float* lse, int num_seqs, int Hq, int Hkv, int d, int num_blocks,
+                          int max_blocks_per_seq, float scale, float k_scale, float v_scale, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  if (num_seqs < 0 || Hq < 1) return EXATTN_ERR_INVALID_ARG;
+  int rc = fp4_sizes(Hkv, d, num_blocks, 1, max_blocks_per_seq);
+  if (rc != EXATTN_OK) return rc;
+  if (Hq % Hkv != 0 || !good_scale(scale) || !good_scale(k_scale) || !good_scale(v_scale))
+    return EXATTN_ERR_INVALID_ARG;
+  const int group = Hq / Hkv;
+  const int rows = exattn::fp4_decode_rows(group);
+  if (num_seqs > 65535 || Hq > 65535 || static_cast<int64_t>(Hkv) * ((group + rows - 1) / rows) > 65535)
+    return EXATTN_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return EXATTN_OK;
+  if (q == nullptr || kv_cache == nullptr || block_table == nullptr || ctx_lens == nullptr || out == nullptr)
+    return EXATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(out) || !aligned4(block_table) || !aligned4(ctx_lens) ||
+      !aligned4(lse))
+    return EXATTN_ERR_ALIGNMENT;
+  const size_t need = attn_decode_fp4_workspace_bytes(num_seqs, Hq, Hkv, d, max_blocks_per_seq);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EXATTN_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return EXATTN_ERR_ALIGNMENT;
+  exattn::DecodeFp4Args a;
+  exattn::DeviceGuard g;
+  if ((rc = status_word(&g.status)) != EXATTN_OK) return rc;
+  g.wait_ns = wait_budget_ns();
+  a.q = q;
+  a.kv_cache = kv_cache;
+  a.block_table = block_table;
+  a.ctx_lens = ctx_lens;
+  a.out = out;
+  a.lse = lse;
+  a.splits = exattn::fp4_decode_splits(num_seqs, Hkv, group, max_blocks_per_seq);
+  a.ws_o = static_cast<float*>(workspace);
+  a.ws_lse = a.ws_o + (need > 0 ? static_cast<size_t>(num_seqs) * Hq * a.splits * d : 0);
+  a.num_seqs = num_seqs;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.num_blocks = num_blocks;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.scale = scale;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return exattn::launch_decode_fp4(a, g, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXATTN_OK
+                                                                                           : EXATTN_ERR_CUDA;
+}
+
 int attn_get_device_status(void* stream, int* status_out) {
   if (status_out == nullptr) return EXATTN_ERR_INVALID_ARG;
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return EXATTN_ERR_CUDA;

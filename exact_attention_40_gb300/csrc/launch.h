@@ -116,6 +116,95 @@ struct RopeArgs {
 
 cudaError_t launch_rope_cache_write(const RopeArgs& a, cudaStream_t stream);
 
+// Positions of several axes: strides (in elements) of [axes][batch][token], or
+// of [axes][token] with batch stride 0.
+struct RopeAxesTable {
+  unsigned long long u[kRopeMaxDim / 2];  // theta_i / (2 pi), in units of 2^-64 turn
+  unsigned char axis[kRopeMaxDim / 2];    // position axis of pair i
+};
+
+constexpr int kRopeMaxAxes = 4;
+
+// A [batch, heads, tokens, d] bf16 tensor by its strides, in 16-byte vectors.
+struct HeadView {
+  const void* ptr;
+  long long batch, head, token;
+};
+
+struct RopeAxesArgs {
+  HeadView q, k, q_out, k_out;
+  const int32_t* positions;
+  long long pos_axis, pos_batch, pos_token;
+  unsigned int B, N;  // B * N < 2^31
+  int Hq, Hkv, d, inverse;
+};
+
+cudaError_t launch_rope_axes(const RopeAxesArgs& a, const RopeAxesTable& table, cudaStream_t stream);
+
+// Where the tokens of the 4-bit cache calls lie.
+struct Fp4Slots {
+  const int32_t* seq_ids;      // [num_tokens]
+  const int32_t* slots;        // [num_tokens]: token index within its sequence
+  const int32_t* block_table;  // [num_seqs, max_blocks_per_seq]
+  unsigned int* status;        // device status word
+  long long num_tokens;
+  int num_seqs, num_blocks, max_blocks_per_seq;
+};
+
+struct RopeFp4Args {
+  HeadView q, k, v, q_out;  // batch stride unused
+  const int32_t* positions;
+  long long pos_axis;       // stride between axes, in elements
+  void* kv_cache;           // [num_blocks, Hkv, 18 d]
+  Fp4Slots at;
+  int Hq, Hkv, d;
+  float k_scale, v_scale;
+};
+
+cudaError_t launch_rope_cache_write_fp4(const RopeFp4Args& a, const RopeAxesTable& table, cudaStream_t stream);
+
+struct ReadFp4Args {
+  const void* kv_cache;
+  HeadView k_out, v_out;  // batch stride unused
+  Fp4Slots at;
+  int Hkv, d;
+  float k_scale, v_scale;
+};
+
+cudaError_t launch_cache_read_fp4(const ReadFp4Args& a, cudaStream_t stream);
+
+// Query heads a CTA of the 4-bit decode takes: 8 columns of an mma, or 16 for
+// the larger groups.
+inline int fp4_decode_rows(int group) { return group <= 8 ? 8 : 16; }
+
+constexpr int kFp4MinSplitBlocks = 8;  // blocks a split takes at least: two per warp
+
+// Splits of a sequence: enough CTAs for three waves of four per SM, but none
+// of fewer than kFp4MinSplitBlocks blocks.  By the call's sizes alone, so that
+// the workspace can be sized on any host.
+inline int fp4_decode_splits(int num_seqs, int Hkv, int group, int max_blocks_per_seq) {
+  const int rows = fp4_decode_rows(group);
+  const long long base = static_cast<long long>(num_seqs) * Hkv * ((group + rows - 1) / rows);
+  const long long want = (152ll * 12 + base - 1) / base;
+  const long long most = (static_cast<long long>(max_blocks_per_seq) + kFp4MinSplitBlocks - 1) / kFp4MinSplitBlocks;
+  return static_cast<int>(want < most ? want : most);
+}
+
+struct DecodeFp4Args {
+  const void* q;
+  const void* kv_cache;
+  const int32_t* block_table;
+  const int32_t* ctx_lens;
+  void* out;
+  float* lse;
+  float* ws_o;    // [num_seqs, Hq, splits, d]
+  float* ws_lse;  // [num_seqs, Hq, splits]
+  int num_seqs, Hq, Hkv, d, num_blocks, max_blocks_per_seq, splits;
+  float scale, k_scale, v_scale;
+};
+
+cudaError_t launch_decode_fp4(const DecodeFp4Args& a, const DeviceGuard& g, cudaStream_t stream);
+
 struct BwdArgs {
   // tensor maps (3-D views (d, rows, planes), 64-column boxes, 128-byte
   // swizzle) of q, dout (planes B*Hq) and k, v (planes B*Hkv), with 64-row

@@ -66,6 +66,18 @@ lib.attn_bwd_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, _I]
 lib.attn_bwd_workspace_bytes.restype = _SZ
 lib.attn_bwd.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P]
 lib.attn_bwd.restype = _I
+lib.attn_rope_axes.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P]
+lib.attn_rope_axes.restype = _I
+lib.attn_fp4_cache_bytes.argtypes = [_I, _I, _I]
+lib.attn_fp4_cache_bytes.restype = _SZ
+lib.attn_rope_cache_write_fp4.argtypes = [_P] * 9 + [_P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _F, _F, _P]
+lib.attn_rope_cache_write_fp4.restype = _I
+lib.attn_cache_read_fp4.argtypes = [_P] * 6 + [_P, _I, _I, _I, _I, _I, _I, _F, _F, _P]
+lib.attn_cache_read_fp4.restype = _I
+lib.attn_decode_fp4_workspace_bytes.argtypes = [_I, _I, _I, _I, _I]
+lib.attn_decode_fp4_workspace_bytes.restype = _SZ
+lib.attn_decode_paged_fp4.argtypes = [_P] * 6 + [_I] * 6 + [_F, _F, _F, _P, _SZ, _P]
+lib.attn_decode_paged_fp4.restype = _I
 lib.attn_shutdown.argtypes = []
 lib.attn_shutdown.restype = None
 
@@ -359,6 +371,247 @@ def attn_bwd(q, k, v, out, dout, lse, causal: bool = False, scale: float | None 
     if rc != EXATTN_OK:
         raise ExattnError("attn_bwd", rc)
     return dq, dk, dv
+
+
+_I64x15, _I64x9, _I64x4 = ctypes.c_int64 * 15, ctypes.c_int64 * 9, ctypes.c_int64 * 4
+
+
+def _check_rows(name, t, ndim, device):
+    """A bf16 tensor of head vectors: any strides, the vectors contiguous."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device != device or not t.is_cuda:
+        raise ValueError("%s must live on %s" % (name, device if device.type == "cuda" else "a CUDA device"))
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    if t.dim() != ndim:
+        raise ValueError("%s must have %d dimensions, got %d" % (name, ndim, t.dim()))
+    if t.stride(-1) != 1:
+        raise ValueError("the last dimension of %s must be contiguous" % name)
+
+
+def _check_ints(name, t, shape, device):
+    """A contiguous int32 tensor; shape entries of None are not checked."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != torch.int32:
+        raise TypeError("%s must be torch.int32, got %s" % (name, t.dtype))
+    if t.device != device:
+        raise ValueError("%s must live on %s" % (name, device))
+    if t.dim() != len(shape) or any(a is not None and a != b for a, b in zip(shape, t.shape)):
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _check_cache_fp4(t, device):
+    """(num_blocks, Hkv, d) of a 4-bit cache."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("kv_cache must be a torch.Tensor")
+    if t.dtype != torch.uint8:
+        raise TypeError("kv_cache must be torch.uint8, got %s" % t.dtype)
+    if t.device != device or not t.is_cuda:
+        raise ValueError("kv_cache must live on the tensors' CUDA device")
+    if t.dim() != 3 or t.shape[2] % 18 != 0 or not t.is_contiguous():
+        raise ValueError("kv_cache must be contiguous [num_blocks, Hkv, 18 d], got %s" % (tuple(t.shape),))
+    return t.shape[0], t.shape[1], t.shape[2] // 18
+
+
+def _sections(sections):
+    n = len(sections)
+    return (ctypes.c_int * n)(*sections), n
+
+
+def attn_rope_axes(q, k, positions, sections, base: float = 500000.0, per_axis: bool = False,
+                   inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary positions of several axes.  q [B,Hq,N,d], k [B,Hkv,N,d] bf16, any
+    strides with d contiguous; positions int32 [axes,B,N] or [axes,N] (for every
+    batch), any strides; sections: pairs of each axis, summing to d/2.
+    per_axis: each axis has a spectrum of its own instead of a part of one.
+    inverse: the gradient (the reverse rotation).  q_out, k_out may be q and k.
+
+    Returns (q_out, k_out), contiguous [B,H,N,d] where they were not given."""
+    import torch
+    _check_rows("q", q, 4, q.device)
+    _check_rows("k", k, 4, q.device)
+    B, Hq, N, d = q.shape
+    Bk, Hkv, Nk, dk = k.shape
+    if Bk != B or Nk != N or dk != d:
+        raise ValueError("shape mismatch: q %s k %s" % (tuple(q.shape), tuple(k.shape)))
+    secs, axes = _sections(sections)
+    if positions.dtype != torch.int32 or positions.device != q.device:
+        raise TypeError("positions must be torch.int32 on the tensors' device")
+    if positions.dim() == 2 and positions.shape == (axes, N):
+        pa, pt = positions.stride()
+        pb = 0
+    elif positions.shape == (axes, B, N):
+        pa, pb, pt = positions.stride()
+    else:
+        raise ValueError("positions must be [%d, %d, %d] or [%d, %d], got %s"
+                         % (axes, B, N, axes, N, tuple(positions.shape)))
+    if q_out is None:
+        q_out = torch.empty((B, Hq, N, d), device=q.device, dtype=torch.bfloat16)
+    elif q_out is not q:
+        _check_rows("q_out", q_out, 4, q.device)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+    if k_out is None:
+        k_out = torch.empty((B, Hkv, N, d), device=q.device, dtype=torch.bfloat16)
+    elif k_out is not k:
+        _check_rows("k_out", k_out, 4, q.device)
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must have the shape of k")
+    strides = _I64x15(*q.stride()[:3], *k.stride()[:3], *q_out.stride()[:3], *k_out.stride()[:3], pa, pb, pt)
+    with _on_device(q):
+        rc = lib.attn_rope_axes(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), positions.data_ptr(),
+                                strides, secs, axes, B, Hq, Hkv, N, d, base, int(per_axis), int(inverse),
+                                _stream_handle(stream))
+    if rc != EXATTN_OK:
+        raise ExattnError("attn_rope_axes", rc)
+    return q_out, k_out
+
+
+def attn_fp4_cache(num_blocks: int, Hkv: int, d: int, device="cuda"):
+    """An empty (zeroed) 4-bit paged cache: uint8 [num_blocks, Hkv, 18 d]."""
+    import torch
+    if lib.attn_fp4_cache_bytes(num_blocks, Hkv, d) == 0:
+        raise ValueError("no 4-bit cache of %d blocks, %d heads of %d" % (num_blocks, Hkv, d))
+    return torch.zeros((num_blocks, Hkv, 18 * d), device=device, dtype=torch.uint8)
+
+
+def attn_rope_cache_write_fp4(q, k, v, seq_ids, slots, positions, block_table, kv_cache, sections,
+                              base: float = 500000.0, per_axis: bool = False, k_scale: float = 1.0,
+                              v_scale: float = 1.0, q_out=None, stream=None):
+    """Rotates new tokens' queries and keys by their positions and stores the
+    rotated keys and the values into the 4-bit cache.  q [T,Hq,d], k, v [T,Hkv,d]
+    bf16, any strides with d contiguous; seq_ids, slots int32 [T]: sequence and
+    index in it; positions int32 [axes,T]; block_table int32 [S,max_blocks];
+    sections, base, per_axis as attn_rope_axes.  q_out may be q.
+
+    Returns q_out, the rotated queries (contiguous where not given)."""
+    import torch
+    device = kv_cache.device
+    nb, Hkv, d = _check_cache_fp4(kv_cache, device)
+    _check_rows("q", q, 3, device)
+    _check_rows("k", k, 3, device)
+    _check_rows("v", v, 3, device)
+    T, Hq, dq = q.shape
+    if dq != d or k.shape != (T, Hkv, d) or v.shape != (T, Hkv, d):
+        raise ValueError("shape mismatch: q %s k %s v %s kv_cache %s"
+                         % (tuple(q.shape), tuple(k.shape), tuple(v.shape), tuple(kv_cache.shape)))
+    secs, axes = _sections(sections)
+    _check_ints("seq_ids", seq_ids, (T,), device)
+    _check_ints("slots", slots, (T,), device)
+    _check_ints("positions", positions, (axes, T), device)
+    _check_ints("block_table", block_table, (None, None), device)
+    S, max_blocks = block_table.shape
+    if q_out is None:
+        q_out = torch.empty((T, Hq, d), device=device, dtype=torch.bfloat16)
+    elif q_out is not q:
+        _check_rows("q_out", q_out, 3, device)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+    strides = _I64x9(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *q_out.stride()[:2], T)
+    with _on_device(kv_cache):
+        rc = lib.attn_rope_cache_write_fp4(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), seq_ids.data_ptr(), slots.data_ptr(),
+            positions.data_ptr(), block_table.data_ptr(), kv_cache.data_ptr(), strides, secs, axes, T, Hq, Hkv, d, S,
+            nb, max_blocks, base, int(per_axis), k_scale, v_scale, _stream_handle(stream))
+    if rc != EXATTN_OK:
+        raise ExattnError("attn_rope_cache_write_fp4", rc)
+    return q_out
+
+
+def attn_cache_read_fp4(kv_cache, seq_ids, slots, block_table, k_scale: float = 1.0, v_scale: float = 1.0,
+                        k_out=None, v_out=None, stream=None):
+    """Tokens of the 4-bit cache as bf16: token i is place slots[i] of sequence
+    seq_ids[i].  k_out, v_out [T,Hkv,d], any strides with d contiguous (a
+    [Hkv,N,d] tensor's transpose takes one sequence for attn_fwd).
+
+    Returns (k_out, v_out), contiguous where not given."""
+    import torch
+    device = kv_cache.device
+    nb, Hkv, d = _check_cache_fp4(kv_cache, device)
+    _check_ints("seq_ids", seq_ids, (None,), device)
+    T = seq_ids.shape[0]
+    _check_ints("slots", slots, (T,), device)
+    _check_ints("block_table", block_table, (None, None), device)
+    S, max_blocks = block_table.shape
+    if k_out is None:
+        k_out = torch.empty((T, Hkv, d), device=device, dtype=torch.bfloat16)
+    else:
+        _check_rows("k_out", k_out, 3, device)
+    if v_out is None:
+        v_out = torch.empty((T, Hkv, d), device=device, dtype=torch.bfloat16)
+    else:
+        _check_rows("v_out", v_out, 3, device)
+    if k_out.shape != (T, Hkv, d) or v_out.shape != (T, Hkv, d):
+        raise ValueError("k_out and v_out must be %s" % ((T, Hkv, d),))
+    strides = _I64x4(*k_out.stride()[:2], *v_out.stride()[:2])
+    with _on_device(kv_cache):
+        rc = lib.attn_cache_read_fp4(kv_cache.data_ptr(), seq_ids.data_ptr(), slots.data_ptr(),
+                                     block_table.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), strides, T, Hkv, d,
+                                     S, nb, max_blocks, k_scale, v_scale, _stream_handle(stream))
+    if rc != EXATTN_OK:
+        raise ExattnError("attn_cache_read_fp4", rc)
+    return k_out, v_out
+
+
+def attn_decode_fp4_workspace_bytes(num_seqs, Hq, Hkv, d, max_blocks_per_seq) -> int:
+    return int(lib.attn_decode_fp4_workspace_bytes(num_seqs, Hq, Hkv, d, max_blocks_per_seq))
+
+
+def attn_decode_paged_fp4(q, kv_cache, block_table, ctx_lens, scale: float | None = None, k_scale: float = 1.0,
+                          v_scale: float = 1.0, out=None, lse=None, workspace=None, return_lse: bool = True,
+                          stream=None):
+    """One-token decode over the 4-bit cache.  q [S,Hq,d] bf16; kv_cache uint8
+    [num_blocks,Hkv,18 d]; block_table int32 [S,max_blocks]; ctx_lens int32 [S].
+
+    Returns (out [S,Hq,d] bf16, lse [S,Hq] fp32 or None)."""
+    import torch
+    device = kv_cache.device
+    nb, Hkv, d = _check_cache_fp4(kv_cache, device)
+    _check_tensor("q", q, torch.bfloat16, 3)
+    S, Hq, dq = q.shape
+    if q.device != device or dq != d:
+        raise ValueError("q %s on %s does not fit kv_cache %s on %s"
+                         % (tuple(q.shape), q.device, tuple(kv_cache.shape), device))
+    _check_ints("block_table", block_table, (S, None), device)
+    _check_ints("ctx_lens", ctx_lens, (S,), device)
+    max_blocks = block_table.shape[1]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_tensor("out", out, torch.bfloat16, 3)
+        if out.shape != q.shape or out.device != device:
+            raise ValueError("out must be like q")
+    if lse is None:
+        if return_lse:
+            lse = torch.empty((S, Hq), device=device, dtype=torch.float32)
+    else:
+        _check_tensor("lse", lse, torch.float32, 2)
+        if lse.shape != (S, Hq) or lse.device != device:
+            raise ValueError("lse must be [%d, %d] on the tensors' device" % (S, Hq))
+    if workspace is None:
+        need = lib.attn_decode_fp4_workspace_bytes(S, Hq, Hkv, d, max_blocks)
+        if need:
+            workspace = torch.empty(need, device=device, dtype=torch.uint8)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the tensors' device")
+    with _on_device(kv_cache):
+        rc = lib.attn_decode_paged_fp4(
+            q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(),
+            lse.data_ptr() if lse is not None else None, S, Hq, Hkv, d, nb, max_blocks, scale, k_scale, v_scale,
+            workspace.data_ptr() if workspace is not None else None,
+            workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream_handle(stream))
+    if rc != EXATTN_OK:
+        raise ExattnError("attn_decode_paged_fp4", rc)
+    return out, lse
 
 
 def attn_get_device_status(stream=None) -> int:

@@ -285,6 +285,123 @@ int attn_rope_cache_write(void* q, const void* k, const void* v, const int32_t* 
                           int num_blocks, int max_blocks_per_seq, float base, void* stream);
 
 /*
+ * Rotary positions of several axes (time, height, width): queries and keys in
+ * the layout of attn_fwd, or any other that strides describe.  Pairs (i, i +
+ * d/2) of every head vector of token n turn by
+ *   positions[axis(i)][b][n] * theta_i
+ *   y_i = x_i cos - x_(i+d/2) sin,  y_(i+d/2) = x_(i+d/2) cos + x_i sin.
+ * The first sections[0] pairs follow axis 0, the next sections[1] axis 1, ...;
+ * the sections sum to d/2 (one section: ordinary rotary positions).  Pair i is
+ * pair j of its section:
+ *   per_axis == 0: theta_i = base^(-2i/d)              (one spectrum for all)
+ *   per_axis != 0: theta_i = base^(-j/sections[axis])  (each axis its own)
+ * inverse != 0 turns the other way, which is the gradient: with the same
+ * positions it takes the gradients of the outputs to those of the inputs.
+ * Angles are reduced modulo a turn exactly (64-bit fixed point, any int32
+ * position), the rotation is in fp32, one rounding to bf16.
+ *   q, q_out [B, Hq, N, d], k, k_out [B, Hkv, N, d] bf16 by their strides, d
+ *            contiguous; q_out may be q and k_out k (with the same strides, in
+ *            place), no other overlap.  Hq or Hkv may be 0 (its pointers NULL).
+ *   positions int32 by its strides
+ *   strides  host array of 15, in elements: q (batch, head, token), k, q_out,
+ *            k_out, positions (axis, batch, token).  Those of dimensions of
+ *            size 1 are not used.  The tensors' are multiples of 8
+ *            (EXATTN_ERR_ALIGNMENT); an output's rows must not overlap
+ *            (EXATTN_ERR_INVALID_ARG).  Inputs may be broadcast (stride 0).
+ * d a multiple of 16 in [16, 256]; 1 <= num_axes <= 4; base finite and > 1;
+ * B * N < 2^31; B == 0 or N == 0 launches nothing.  Tensors 16-byte aligned,
+ * positions 4-byte.  One launch on `stream`, asynchronous, deterministic.
+ */
+int attn_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions,
+                   const int64_t* strides, const int* sections, int num_axes, int B, int Hq, int Hkv, int N, int d,
+                   float base, int per_axis, int inverse, void* stream);
+
+/*
+ * The 4-bit paged cache.  A value is code * scale * g: code an e2m1 number (0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6, signed), scale an e4m3 number shared by 16
+ * neighbouring columns of a head vector, g the tensor's fp32 scale (k_scale or
+ * v_scale, finite and > 0).  4.5 bits a value, 3.6 times less than bf16.
+ *   kv_cache [num_blocks, Hkv, 18 d] bytes, 16-byte aligned: one block of 16
+ *   tokens of one KV head is one span,
+ *     key codes    [16][d/2]   byte c: column 2c (low four bits) and 2c + 1
+ *     value codes  [16][d/2]
+ *     key scales   [16][d/16]
+ *     value scales [16][d/16]
+ * attn_fp4_cache_bytes: its size (0 for invalid arguments).  d is 64 or 128 for
+ * every call on it.
+ */
+size_t attn_fp4_cache_bytes(int num_blocks, int Hkv, int d);
+
+/*
+ * Append to the 4-bit cache: rotates the new tokens' queries and keys (as
+ * attn_rope_axes, positions by axis, frequencies by sections, base, per_axis)
+ * and stores the rotated keys and the values.  Per group of 16 columns x, in
+ * fp32:
+ *   scale = e4m3(min(max|x| / (6 g), 448)),  code = e2m1(x / (scale g)),
+ * rounded to nearest, ties to even, e2m1 saturating at 6.  The keys are the
+ * fp32 results of the rotation, not rounded to bf16 before.  A group that holds
+ * a NaN or an infinity gets a NaN scale: all of it reads back as NaN.
+ *   q, q_out  [num_tokens, Hq, d] bf16 by strides; q_out may be q.  Hq may be 0.
+ *   k, v      [num_tokens, Hkv, d] bf16 by strides
+ *   seq_ids, slots int32 [num_tokens]: sequence, and the token's index in it
+ *             (with one axis usually its position too)
+ *   positions int32 [num_axes][num_tokens]
+ *   block_table int32 [num_seqs, max_blocks_per_seq] (as attn_decode_paged)
+ *   strides   host array of 9, in elements: q (token, head), k, v, q_out, axis
+ *             of positions; rules as attn_rope_axes
+ * Token t goes to place slots[t] % 16 of physical block
+ * block_table[seq_ids[t]][slots[t] / 16]; nothing else of the cache is
+ * written.  Two tokens with one place leave a mixture of both there.  A token
+ * whose sequence, slot or table entry lies outside the table or the cache is
+ * rotated in q_out but stores nothing, and sets EXATTN_DEVICE_BOUNDS_BIT.
+ * num_tokens >= 0 (0 launches nothing).  One launch on `stream`, asynchronous,
+ * deterministic.
+ */
+int attn_rope_cache_write_fp4(const void* q, const void* k, const void* v, void* q_out, const int32_t* seq_ids,
+                              const int32_t* slots, const int32_t* positions, const int32_t* block_table,
+                              void* kv_cache, const int64_t* strides, const int* sections, int num_axes,
+                              int num_tokens, int Hq, int Hkv, int d, int num_seqs, int num_blocks,
+                              int max_blocks_per_seq, float base, int per_axis, float k_scale, float v_scale,
+                              void* stream);
+
+/*
+ * Reads tokens of the 4-bit cache back as bf16 (code * scale, exact, times g,
+ * rounded once): the keys and values attn_fwd needs to prefill a further chunk
+ * over a cached prefix.
+ *   seq_ids, slots, block_table, sizes, scales as attn_rope_cache_write_fp4
+ *   k_out, v_out [num_tokens, Hkv, d] bf16 by strides (so that a [Hkv, N, d]
+ *             tensor can take a sequence); apart from each other
+ *   strides   host array of 4, in elements: k_out (token, head), v_out
+ * A token outside the table or the cache reads as zeros and sets
+ * EXATTN_DEVICE_BOUNDS_BIT.  num_tokens >= 0 (0 launches nothing).  One launch
+ * on `stream`, asynchronous, deterministic.
+ */
+int attn_cache_read_fp4(const void* kv_cache, const int32_t* seq_ids, const int32_t* slots,
+                        const int32_t* block_table, void* k_out, void* v_out, const int64_t* strides, int num_tokens,
+                        int Hkv, int d, int num_seqs, int num_blocks, int max_blocks_per_seq, float k_scale,
+                        float v_scale, void* stream);
+
+/*
+ * One-token decode over the 4-bit cache: attn_decode_paged on the keys and
+ * values that the cache stands for.  q, out [num_seqs, Hq, d] bf16, lse
+ * [num_seqs, Hq] fp32 or NULL, block_table, ctx_lens and their checks on the
+ * device as attn_decode_paged; keys and values enter exactly, the weights are
+ * rounded to fp16.  ctx_len 0 gives out = 0, lse = -inf.
+ *   workspace: attn_decode_fp4_workspace_bytes(...) bytes, 16-byte aligned, its
+ *   contents clobbered; NULL where that is 0.  Calls whose executions overlap
+ *   need one each.
+ * One or two launches on `stream` (the second merges the splits of a sequence,
+ * a programmatic dependent launch), asynchronous, deterministic; it can be
+ * captured into a CUDA graph.  A bounded wait that runs out sets
+ * EXATTN_DEVICE_TIMEOUT_BIT.
+ */
+size_t attn_decode_fp4_workspace_bytes(int num_seqs, int Hq, int Hkv, int d, int max_blocks_per_seq);
+int attn_decode_paged_fp4(const void* q, const void* kv_cache, const int32_t* block_table, const int32_t* ctx_lens,
+                          void* out, float* lse, int num_seqs, int Hq, int Hkv, int d, int num_blocks,
+                          int max_blocks_per_seq, float scale, float k_scale, float v_scale, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the status word of the
  * current device and stores it in *status_out: 0, or an OR of
  * EXATTN_DEVICE_*_BIT (the bits are small, so the value is never negative).
