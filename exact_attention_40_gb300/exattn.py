@@ -15,8 +15,10 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libexattn.so")
@@ -373,56 +375,85 @@ def attn_bwd(q, k, v, out, dout, lse, causal: bool = False, scale: float | None 
     return dq, dk, dv
 
 
-_I64x15, _I64x9, _I64x4 = ctypes.c_int64 * 15, ctypes.c_int64 * 9, ctypes.c_int64 * 4
+_pack15, _pack9, _pack4 = struct.Struct("15q").pack, struct.Struct("9q").pack, struct.Struct("4q").pack
 
 
-def _check_rows(name, t, ndim, device):
+def _launch(fn, device, stream, *args):
+    """fn(*args, stream handle) with `device` current; the stream defaults to
+    that device's current one.  (The raw-handle query takes 0.1 us where a Stream
+    object takes 3, which is a good part of a small call.)"""
+    import torch
+    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == device.index:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, handle)
+    if rc != EXATTN_OK:
+        raise ExattnError(fn.__name__, rc)
+
+
+def _check_rows(name, t, shape, device):
     """A bf16 tensor of head vectors: any strides, the vectors contiguous."""
     import torch
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.bfloat16 and t.device == device \
+            and t.shape == shape and t.stride()[-1] == 1:
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device != device or not t.is_cuda:
-        raise ValueError("%s must live on %s" % (name, device if device.type == "cuda" else "a CUDA device"))
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
-    if t.dim() != ndim:
-        raise ValueError("%s must have %d dimensions, got %d" % (name, ndim, t.dim()))
-    if t.stride(-1) != 1:
-        raise ValueError("the last dimension of %s must be contiguous" % name)
+    if not t.is_cuda or t.device != device:
+        raise ValueError("%s must live on the call's CUDA device, is on %s" % (name, t.device))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    raise ValueError("the last dimension of %s must be contiguous" % name)
 
 
 def _check_ints(name, t, shape, device):
-    """A contiguous int32 tensor; shape entries of None are not checked."""
+    """A contiguous int32 tensor."""
     import torch
+    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == device and t.shape == shape \
+            and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError("%s must be torch.int32, got %s" % (name, t.dtype))
     if t.device != device:
         raise ValueError("%s must live on %s" % (name, device))
-    if t.dim() != len(shape) or any(a is not None and a != b for a, b in zip(shape, t.shape)):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    raise ValueError("%s must be contiguous" % name)
 
 
-def _check_cache_fp4(t, device):
-    """(num_blocks, Hkv, d) of a 4-bit cache."""
+def _dims(name, t, ndim):
+    """The shape of a tensor of ndim dimensions."""
     import torch
     if not isinstance(t, torch.Tensor):
-        raise TypeError("kv_cache must be a torch.Tensor")
-    if t.dtype != torch.uint8:
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dim() != ndim:
+        raise ValueError("%s must have %d dimensions, got %d" % (name, ndim, t.dim()))
+    return t.shape
+
+
+def _check_cache_fp4(t):
+    """(num_blocks, Hkv, d) of a 4-bit cache."""
+    import torch
+    nb, Hkv, span = _dims("kv_cache", t, 3)
+    if t.dtype is not torch.uint8:
         raise TypeError("kv_cache must be torch.uint8, got %s" % t.dtype)
-    if t.device != device or not t.is_cuda:
-        raise ValueError("kv_cache must live on the tensors' CUDA device")
-    if t.dim() != 3 or t.shape[2] % 18 != 0 or not t.is_contiguous():
+    if not t.is_cuda:
+        raise ValueError("kv_cache must live on a CUDA device")
+    if span % 18 != 0 or not t.is_contiguous():
         raise ValueError("kv_cache must be contiguous [num_blocks, Hkv, 18 d], got %s" % (tuple(t.shape),))
-    return t.shape[0], t.shape[1], t.shape[2] // 18
+    return nb, Hkv, span // 18
 
 
+@functools.lru_cache(maxsize=256)
 def _sections(sections):
-    n = len(sections)
-    return (ctypes.c_int * n)(*sections), n
+    """The C array of a tuple of section sizes."""
+    return (ctypes.c_int * len(sections))(*sections)
 
 
 def attn_rope_axes(q, k, positions, sections, base: float = 500000.0, per_axis: bool = False,
@@ -435,42 +466,36 @@ def attn_rope_axes(q, k, positions, sections, base: float = 500000.0, per_axis: 
 
     Returns (q_out, k_out), contiguous [B,H,N,d] where they were not given."""
     import torch
-    _check_rows("q", q, 4, q.device)
-    _check_rows("k", k, 4, q.device)
-    B, Hq, N, d = q.shape
-    Bk, Hkv, Nk, dk = k.shape
-    if Bk != B or Nk != N or dk != d:
-        raise ValueError("shape mismatch: q %s k %s" % (tuple(q.shape), tuple(k.shape)))
-    secs, axes = _sections(sections)
-    if positions.dtype != torch.int32 or positions.device != q.device:
+    q_shape = B, Hq, N, d = _dims("q", q, 4)
+    k_shape = _dims("k", k, 4)
+    Hkv = k_shape[1]
+    device = q.device
+    _check_rows("q", q, q_shape, device)
+    _check_rows("k", k, (B, Hkv, N, d), device)
+    sections = tuple(sections)
+    axes = len(sections)
+    shape = _dims("positions", positions, positions.dim())
+    if positions.dtype is not torch.int32 or positions.device != device:
         raise TypeError("positions must be torch.int32 on the tensors' device")
-    if positions.dim() == 2 and positions.shape == (axes, N):
+    if shape == (axes, B, N):
+        pa, pb, pt = positions.stride()
+    elif shape == (axes, N):
         pa, pt = positions.stride()
         pb = 0
-    elif positions.shape == (axes, B, N):
-        pa, pb, pt = positions.stride()
     else:
-        raise ValueError("positions must be [%d, %d, %d] or [%d, %d], got %s"
-                         % (axes, B, N, axes, N, tuple(positions.shape)))
+        raise ValueError("positions must be [%d, %d, %d] or [%d, %d], got %s" % (axes, B, N, axes, N, tuple(shape)))
     if q_out is None:
-        q_out = torch.empty((B, Hq, N, d), device=q.device, dtype=torch.bfloat16)
+        q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=device)
     elif q_out is not q:
-        _check_rows("q_out", q_out, 4, q.device)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have the shape of q")
+        _check_rows("q_out", q_out, q_shape, device)
     if k_out is None:
-        k_out = torch.empty((B, Hkv, N, d), device=q.device, dtype=torch.bfloat16)
+        k_out = torch.empty(k_shape, dtype=torch.bfloat16, device=device)
     elif k_out is not k:
-        _check_rows("k_out", k_out, 4, q.device)
-        if k_out.shape != k.shape:
-            raise ValueError("k_out must have the shape of k")
-    strides = _I64x15(*q.stride()[:3], *k.stride()[:3], *q_out.stride()[:3], *k_out.stride()[:3], pa, pb, pt)
-    with _on_device(q):
-        rc = lib.attn_rope_axes(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), positions.data_ptr(),
-                                strides, secs, axes, B, Hq, Hkv, N, d, base, int(per_axis), int(inverse),
-                                _stream_handle(stream))
-    if rc != EXATTN_OK:
-        raise ExattnError("attn_rope_axes", rc)
+        _check_rows("k_out", k_out, k_shape, device)
+    strides = _pack15(*q.stride()[:3], *k.stride()[:3], *q_out.stride()[:3], *k_out.stride()[:3], pa, pb, pt)
+    _launch(lib.attn_rope_axes, device, stream, q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+            positions.data_ptr(), strides, _sections(sections), axes, B, Hq, Hkv, N, d, base, bool(per_axis),
+            bool(inverse))
     return q_out, k_out
 
 
@@ -493,35 +518,28 @@ def attn_rope_cache_write_fp4(q, k, v, seq_ids, slots, positions, block_table, k
 
     Returns q_out, the rotated queries (contiguous where not given)."""
     import torch
+    nb, Hkv, d = _check_cache_fp4(kv_cache)
     device = kv_cache.device
-    nb, Hkv, d = _check_cache_fp4(kv_cache, device)
-    _check_rows("q", q, 3, device)
-    _check_rows("k", k, 3, device)
-    _check_rows("v", v, 3, device)
-    T, Hq, dq = q.shape
-    if dq != d or k.shape != (T, Hkv, d) or v.shape != (T, Hkv, d):
-        raise ValueError("shape mismatch: q %s k %s v %s kv_cache %s"
-                         % (tuple(q.shape), tuple(k.shape), tuple(v.shape), tuple(kv_cache.shape)))
-    secs, axes = _sections(sections)
+    T, Hq, _ = _dims("q", q, 3)
+    _check_rows("q", q, (T, Hq, d), device)
+    _check_rows("k", k, (T, Hkv, d), device)
+    _check_rows("v", v, (T, Hkv, d), device)
+    sections = tuple(sections)
+    axes = len(sections)
+    S, max_blocks = _dims("block_table", block_table, 2)
     _check_ints("seq_ids", seq_ids, (T,), device)
     _check_ints("slots", slots, (T,), device)
     _check_ints("positions", positions, (axes, T), device)
-    _check_ints("block_table", block_table, (None, None), device)
-    S, max_blocks = block_table.shape
+    _check_ints("block_table", block_table, (S, max_blocks), device)
     if q_out is None:
-        q_out = torch.empty((T, Hq, d), device=device, dtype=torch.bfloat16)
+        q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=device)
     elif q_out is not q:
-        _check_rows("q_out", q_out, 3, device)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have the shape of q")
-    strides = _I64x9(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *q_out.stride()[:2], T)
-    with _on_device(kv_cache):
-        rc = lib.attn_rope_cache_write_fp4(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), seq_ids.data_ptr(), slots.data_ptr(),
-            positions.data_ptr(), block_table.data_ptr(), kv_cache.data_ptr(), strides, secs, axes, T, Hq, Hkv, d, S,
-            nb, max_blocks, base, int(per_axis), k_scale, v_scale, _stream_handle(stream))
-    if rc != EXATTN_OK:
-        raise ExattnError("attn_rope_cache_write_fp4", rc)
+        _check_rows("q_out", q_out, (T, Hq, d), device)
+    strides = _pack9(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *q_out.stride()[:2], T)
+    _launch(lib.attn_rope_cache_write_fp4, device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
+            seq_ids.data_ptr(), slots.data_ptr(), positions.data_ptr(), block_table.data_ptr(), kv_cache.data_ptr(),
+            strides, _sections(sections), axes, T, Hq, Hkv, d, S, nb, max_blocks, base, bool(per_axis), k_scale,
+            v_scale)
     return q_out
 
 
@@ -533,30 +551,24 @@ def attn_cache_read_fp4(kv_cache, seq_ids, slots, block_table, k_scale: float = 
 
     Returns (k_out, v_out), contiguous where not given."""
     import torch
+    nb, Hkv, d = _check_cache_fp4(kv_cache)
     device = kv_cache.device
-    nb, Hkv, d = _check_cache_fp4(kv_cache, device)
-    _check_ints("seq_ids", seq_ids, (None,), device)
-    T = seq_ids.shape[0]
+    T, = _dims("seq_ids", seq_ids, 1)
+    S, max_blocks = _dims("block_table", block_table, 2)
+    _check_ints("seq_ids", seq_ids, (T,), device)
     _check_ints("slots", slots, (T,), device)
-    _check_ints("block_table", block_table, (None, None), device)
-    S, max_blocks = block_table.shape
+    _check_ints("block_table", block_table, (S, max_blocks), device)
     if k_out is None:
-        k_out = torch.empty((T, Hkv, d), device=device, dtype=torch.bfloat16)
+        k_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=device)
     else:
-        _check_rows("k_out", k_out, 3, device)
+        _check_rows("k_out", k_out, (T, Hkv, d), device)
     if v_out is None:
-        v_out = torch.empty((T, Hkv, d), device=device, dtype=torch.bfloat16)
+        v_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=device)
     else:
-        _check_rows("v_out", v_out, 3, device)
-    if k_out.shape != (T, Hkv, d) or v_out.shape != (T, Hkv, d):
-        raise ValueError("k_out and v_out must be %s" % ((T, Hkv, d),))
-    strides = _I64x4(*k_out.stride()[:2], *v_out.stride()[:2])
-    with _on_device(kv_cache):
-        rc = lib.attn_cache_read_fp4(kv_cache.data_ptr(), seq_ids.data_ptr(), slots.data_ptr(),
-                                     block_table.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), strides, T, Hkv, d,
-                                     S, nb, max_blocks, k_scale, v_scale, _stream_handle(stream))
-    if rc != EXATTN_OK:
-        raise ExattnError("attn_cache_read_fp4", rc)
+        _check_rows("v_out", v_out, (T, Hkv, d), device)
+    _launch(lib.attn_cache_read_fp4, device, stream, kv_cache.data_ptr(), seq_ids.data_ptr(), slots.data_ptr(),
+            block_table.data_ptr(), k_out.data_ptr(), v_out.data_ptr(),
+            _pack4(*k_out.stride()[:2], *v_out.stride()[:2]), T, Hkv, d, S, nb, max_blocks, k_scale, v_scale)
     return k_out, v_out
 
 
@@ -572,45 +584,41 @@ def attn_decode_paged_fp4(q, kv_cache, block_table, ctx_lens, scale: float | Non
 
     Returns (out [S,Hq,d] bf16, lse [S,Hq] fp32 or None)."""
     import torch
+    nb, Hkv, d = _check_cache_fp4(kv_cache)
     device = kv_cache.device
-    nb, Hkv, d = _check_cache_fp4(kv_cache, device)
-    _check_tensor("q", q, torch.bfloat16, 3)
-    S, Hq, dq = q.shape
-    if q.device != device or dq != d:
-        raise ValueError("q %s on %s does not fit kv_cache %s on %s"
-                         % (tuple(q.shape), q.device, tuple(kv_cache.shape), device))
-    _check_ints("block_table", block_table, (S, None), device)
+    S, Hq, _ = _dims("q", q, 3)
+    _check_rows("q", q, (S, Hq, d), device)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    _, max_blocks = _dims("block_table", block_table, 2)
+    _check_ints("block_table", block_table, (S, max_blocks), device)
     _check_ints("ctx_lens", ctx_lens, (S,), device)
-    max_blocks = block_table.shape[1]
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _check_tensor("out", out, torch.bfloat16, 3)
-        if out.shape != q.shape or out.device != device:
-            raise ValueError("out must be like q")
+        _check_rows("out", out, (S, Hq, d), device)
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
     if lse is None:
         if return_lse:
-            lse = torch.empty((S, Hq), device=device, dtype=torch.float32)
+            lse = torch.empty((S, Hq), dtype=torch.float32, device=device)
     else:
         _check_tensor("lse", lse, torch.float32, 2)
         if lse.shape != (S, Hq) or lse.device != device:
             raise ValueError("lse must be [%d, %d] on the tensors' device" % (S, Hq))
+    ws_bytes = 0
     if workspace is None:
-        need = lib.attn_decode_fp4_workspace_bytes(S, Hq, Hkv, d, max_blocks)
-        if need:
-            workspace = torch.empty(need, device=device, dtype=torch.uint8)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous on the tensors' device")
-    with _on_device(kv_cache):
-        rc = lib.attn_decode_paged_fp4(
-            q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(),
-            lse.data_ptr() if lse is not None else None, S, Hq, Hkv, d, nb, max_blocks, scale, k_scale, v_scale,
-            workspace.data_ptr() if workspace is not None else None,
-            workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream_handle(stream))
-    if rc != EXATTN_OK:
-        raise ExattnError("attn_decode_paged_fp4", rc)
+        ws_bytes = lib.attn_decode_fp4_workspace_bytes(S, Hq, Hkv, d, max_blocks)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    else:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous on the tensors' device")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _launch(lib.attn_decode_paged_fp4, device, stream, q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
+            ctx_lens.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), S, Hq, Hkv, d, nb,
+            max_blocks, 1.0 / math.sqrt(d) if scale is None else scale, k_scale, v_scale,
+            None if workspace is None else workspace.data_ptr(), ws_bytes)
     return out, lse
 
 
