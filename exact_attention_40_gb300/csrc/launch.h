@@ -177,16 +177,21 @@ cudaError_t launch_cache_read_fp4(const ReadFp4Args& a, cudaStream_t stream);
 // the larger groups.
 inline int fp4_decode_rows(int group) { return group <= 8 ? 8 : 16; }
 
-constexpr int kFp4MinSplitBlocks = 8;  // blocks a split takes at least: two per warp
+constexpr int kFp4MinSplitBlocks = 8;      // blocks a split takes at least: a pair per warp
+constexpr int kFp4MaxSplits = 152 * 4;     // four CTAs for each SM
 
 // Splits of a sequence: enough CTAs for three waves of four per SM, but none
 // of fewer than kFp4MinSplitBlocks blocks.  By the call's sizes alone, so that
 // the workspace can be sized on any host.
+#include <cstdlib>
 inline int fp4_decode_splits(int num_seqs, int Hkv, int group, int max_blocks_per_seq) {
+  static const int want_ctas = getenv("FP4_WANT") ? atoi(getenv("FP4_WANT")) : 152*4;
+  static const int min_blk = getenv("FP4_MIN") ? atoi(getenv("FP4_MIN")) : 8;
   const int rows = fp4_decode_rows(group);
   const long long base = static_cast<long long>(num_seqs) * Hkv * ((group + rows - 1) / rows);
-  const long long want = (152ll * 12 + base - 1) / base;
-  const long long most = (static_cast<long long>(max_blocks_per_seq) + kFp4MinSplitBlocks - 1) / kFp4MinSplitBlocks;
+  long long want = (want_ctas + base - 1) / base;
+  if (want > kFp4MaxSplits) want = kFp4MaxSplits;
+  const long long most = (static_cast<long long>(max_blocks_per_seq) + min_blk - 1) / min_blk;
   return static_cast<int>(want < most ? want : most);
 }
 

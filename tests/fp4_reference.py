@@ -97,13 +97,13 @@ def random_cache(seed, nb, Hkv, d, k_scale=1.0, v_scale=1.0, gain=1.0):
 
 
 def decode(q, cache, table, lens, d, scale, k_scale, v_scale):
-    """out [S,Hq,d], lse [S,Hq], largest |score| and weighted mean of |v| per row,
-    fp64; blocks with a table entry out of range are left out."""
+    """out [S,Hq,d], lse [S,Hq], largest |score| [S,Hq], weighted mean and largest
+    of |v| [S,Hq,d], fp64; blocks with a table entry out of range are left out."""
     S, Hq = q.shape[:2]
     nb, Hkv = cache.shape[:2]
     q = synth.bf16_bits_to_f32(q).astype(np.float64)
     out, lse = np.zeros((S, Hq, d)), np.full((S, Hq), -np.inf)
-    big, mean = np.zeros((S, Hq)), np.zeros((S, Hq, d))
+    big, mean, most = np.zeros((S, Hq)), np.zeros((S, Hq, d)), np.zeros((S, Hq, d))
     G = Hq // Hkv
     for s in range(S):
         n = int(lens[s])
@@ -121,9 +121,10 @@ def decode(q, cache, table, lens, d, scale, k_scale, v_scale):
             p = np.exp(x - m)
             out[s, h] = p @ v[h // G] / p.sum()
             mean[s, h] = p @ np.abs(v[h // G]) / p.sum()
+            most[s, h] = np.abs(v[h // G]).max(0)
             lse[s, h] = m + np.log(p.sum())
             big[s, h] = np.abs(x).max()
-    return out, lse, big, mean
+    return out, lse, big, mean, most
 
 
 def cos_sin(positions, sections, base, per_axis):
