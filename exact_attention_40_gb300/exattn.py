@@ -2,6 +2,9 @@
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels behind the C ABI.  PyTorch supplies device memory and the stream.
+The calls of the 4-bit cache and of multi-axis rotary positions, which a
+serving step makes with a few tokens, marshal theirs in a compiled module
+(csrc/binding.cpp) instead of ctypes.
 Importing this module loads the library and raises if it has not been
 built (``python -m exact_attention_40_gb300.build``) -- there is no
 fallback path.
@@ -15,10 +18,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import functools
 import math
 import os
-import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libexattn.so")
@@ -375,85 +376,16 @@ def attn_bwd(q, k, v, out, dout, lse, causal: bool = False, scale: float | None 
     return dq, dk, dv
 
 
-_pack15, _pack9, _pack4 = struct.Struct("15q").pack, struct.Struct("9q").pack, struct.Struct("4q").pack
+_native = None  # _binding, the compiled half, once a call needs it
 
 
-def _launch(fn, device, stream, *args):
-    """fn(*args, stream handle) with `device` current; the stream defaults to
-    that device's current one.  (The raw-handle query takes 0.1 us where a Stream
-    object takes 3, which is a good part of a small call.)"""
-    import torch
-    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == device.index:
-        rc = fn(*args, handle)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, handle)
-    if rc != EXATTN_OK:
-        raise ExattnError(fn.__name__, rc)
-
-
-def _check_rows(name, t, shape, device):
-    """A bf16 tensor of head vectors: any strides, the vectors contiguous."""
-    import torch
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.bfloat16 and t.device == device \
-            and t.shape == shape and t.stride()[-1] == 1:
-        return
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype is not torch.bfloat16:
-        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
-    if not t.is_cuda or t.device != device:
-        raise ValueError("%s must live on the call's CUDA device, is on %s" % (name, t.device))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    raise ValueError("the last dimension of %s must be contiguous" % name)
-
-
-def _check_ints(name, t, shape, device):
-    """A contiguous int32 tensor."""
-    import torch
-    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == device and t.shape == shape \
-            and t.is_contiguous():
-        return
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype is not torch.int32:
-        raise TypeError("%s must be torch.int32, got %s" % (name, t.dtype))
-    if t.device != device:
-        raise ValueError("%s must live on %s" % (name, device))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-    raise ValueError("%s must be contiguous" % name)
-
-
-def _dims(name, t, ndim):
-    """The shape of a tensor of ndim dimensions."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dim() != ndim:
-        raise ValueError("%s must have %d dimensions, got %d" % (name, ndim, t.dim()))
-    return t.shape
-
-
-def _check_cache_fp4(t):
-    """(num_blocks, Hkv, d) of a 4-bit cache."""
-    import torch
-    nb, Hkv, span = _dims("kv_cache", t, 3)
-    if t.dtype is not torch.uint8:
-        raise TypeError("kv_cache must be torch.uint8, got %s" % t.dtype)
-    if not t.is_cuda:
-        raise ValueError("kv_cache must live on a CUDA device")
-    if span % 18 != 0 or not t.is_contiguous():
-        raise ValueError("kv_cache must be contiguous [num_blocks, Hkv, 18 d], got %s" % (tuple(t.shape),))
-    return nb, Hkv, span // 18
-
-
-@functools.lru_cache(maxsize=256)
-def _sections(sections):
-    """The C array of a tuple of section sizes."""
-    return (ctypes.c_int * len(sections))(*sections)
+def _load_native():
+    global _native
+    import torch  # noqa: F401  (its libraries have to be in the process first)
+    from . import _binding
+    _binding.set_error(ExattnError)
+    _native = _binding
+    return _binding
 
 
 def attn_rope_axes(q, k, positions, sections, base: float = 500000.0, per_axis: bool = False,
@@ -465,38 +397,8 @@ def attn_rope_axes(q, k, positions, sections, base: float = 500000.0, per_axis: 
     inverse: the gradient (the reverse rotation).  q_out, k_out may be q and k.
 
     Returns (q_out, k_out), contiguous [B,H,N,d] where they were not given."""
-    import torch
-    q_shape = B, Hq, N, d = _dims("q", q, 4)
-    k_shape = _dims("k", k, 4)
-    Hkv = k_shape[1]
-    device = q.device
-    _check_rows("q", q, q_shape, device)
-    _check_rows("k", k, (B, Hkv, N, d), device)
-    sections = tuple(sections)
-    axes = len(sections)
-    shape = _dims("positions", positions, positions.dim())
-    if positions.dtype is not torch.int32 or positions.device != device:
-        raise TypeError("positions must be torch.int32 on the tensors' device")
-    if shape == (axes, B, N):
-        pa, pb, pt = positions.stride()
-    elif shape == (axes, N):
-        pa, pt = positions.stride()
-        pb = 0
-    else:
-        raise ValueError("positions must be [%d, %d, %d] or [%d, %d], got %s" % (axes, B, N, axes, N, tuple(shape)))
-    if q_out is None:
-        q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=device)
-    elif q_out is not q:
-        _check_rows("q_out", q_out, q_shape, device)
-    if k_out is None:
-        k_out = torch.empty(k_shape, dtype=torch.bfloat16, device=device)
-    elif k_out is not k:
-        _check_rows("k_out", k_out, k_shape, device)
-    strides = _pack15(*q.stride()[:3], *k.stride()[:3], *q_out.stride()[:3], *k_out.stride()[:3], pa, pb, pt)
-    _launch(lib.attn_rope_axes, device, stream, q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-            positions.data_ptr(), strides, _sections(sections), axes, B, Hq, Hkv, N, d, base, bool(per_axis),
-            bool(inverse))
-    return q_out, k_out
+    return (_native or _load_native()).rope_axes(q, k, positions, sections, base, per_axis, inverse, q_out, k_out,
+                                                 stream)
 
 
 def attn_fp4_cache(num_blocks: int, Hkv: int, d: int, device="cuda"):
@@ -517,30 +419,8 @@ def attn_rope_cache_write_fp4(q, k, v, seq_ids, slots, positions, block_table, k
     sections, base, per_axis as attn_rope_axes.  q_out may be q.
 
     Returns q_out, the rotated queries (contiguous where not given)."""
-    import torch
-    nb, Hkv, d = _check_cache_fp4(kv_cache)
-    device = kv_cache.device
-    T, Hq, _ = _dims("q", q, 3)
-    _check_rows("q", q, (T, Hq, d), device)
-    _check_rows("k", k, (T, Hkv, d), device)
-    _check_rows("v", v, (T, Hkv, d), device)
-    sections = tuple(sections)
-    axes = len(sections)
-    S, max_blocks = _dims("block_table", block_table, 2)
-    _check_ints("seq_ids", seq_ids, (T,), device)
-    _check_ints("slots", slots, (T,), device)
-    _check_ints("positions", positions, (axes, T), device)
-    _check_ints("block_table", block_table, (S, max_blocks), device)
-    if q_out is None:
-        q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=device)
-    elif q_out is not q:
-        _check_rows("q_out", q_out, (T, Hq, d), device)
-    strides = _pack9(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *q_out.stride()[:2], T)
-    _launch(lib.attn_rope_cache_write_fp4, device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
-            seq_ids.data_ptr(), slots.data_ptr(), positions.data_ptr(), block_table.data_ptr(), kv_cache.data_ptr(),
-            strides, _sections(sections), axes, T, Hq, Hkv, d, S, nb, max_blocks, base, bool(per_axis), k_scale,
-            v_scale)
-    return q_out
+    return (_native or _load_native()).rope_cache_write_fp4(q, k, v, seq_ids, slots, positions, block_table, kv_cache,
+                                                            sections, base, per_axis, k_scale, v_scale, q_out, stream)
 
 
 def attn_cache_read_fp4(kv_cache, seq_ids, slots, block_table, k_scale: float = 1.0, v_scale: float = 1.0,
@@ -550,26 +430,8 @@ def attn_cache_read_fp4(kv_cache, seq_ids, slots, block_table, k_scale: float = 
     [Hkv,N,d] tensor's transpose takes one sequence for attn_fwd).
 
     Returns (k_out, v_out), contiguous where not given."""
-    import torch
-    nb, Hkv, d = _check_cache_fp4(kv_cache)
-    device = kv_cache.device
-    T, = _dims("seq_ids", seq_ids, 1)
-    S, max_blocks = _dims("block_table", block_table, 2)
-    _check_ints("seq_ids", seq_ids, (T,), device)
-    _check_ints("slots", slots, (T,), device)
-    _check_ints("block_table", block_table, (S, max_blocks), device)
-    if k_out is None:
-        k_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=device)
-    else:
-        _check_rows("k_out", k_out, (T, Hkv, d), device)
-    if v_out is None:
-        v_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=device)
-    else:
-        _check_rows("v_out", v_out, (T, Hkv, d), device)
-    _launch(lib.attn_cache_read_fp4, device, stream, kv_cache.data_ptr(), seq_ids.data_ptr(), slots.data_ptr(),
-            block_table.data_ptr(), k_out.data_ptr(), v_out.data_ptr(),
-            _pack4(*k_out.stride()[:2], *v_out.stride()[:2]), T, Hkv, d, S, nb, max_blocks, k_scale, v_scale)
-    return k_out, v_out
+    return (_native or _load_native()).cache_read_fp4(kv_cache, seq_ids, slots, block_table, k_scale, v_scale, k_out,
+                                                      v_out, stream)
 
 
 def attn_decode_fp4_workspace_bytes(num_seqs, Hq, Hkv, d, max_blocks_per_seq) -> int:
@@ -583,43 +445,8 @@ def attn_decode_paged_fp4(q, kv_cache, block_table, ctx_lens, scale: float | Non
     [num_blocks,Hkv,18 d]; block_table int32 [S,max_blocks]; ctx_lens int32 [S].
 
     Returns (out [S,Hq,d] bf16, lse [S,Hq] fp32 or None)."""
-    import torch
-    nb, Hkv, d = _check_cache_fp4(kv_cache)
-    device = kv_cache.device
-    S, Hq, _ = _dims("q", q, 3)
-    _check_rows("q", q, (S, Hq, d), device)
-    if not q.is_contiguous():
-        raise ValueError("q must be contiguous")
-    _, max_blocks = _dims("block_table", block_table, 2)
-    _check_ints("block_table", block_table, (S, max_blocks), device)
-    _check_ints("ctx_lens", ctx_lens, (S,), device)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _check_rows("out", out, (S, Hq, d), device)
-        if not out.is_contiguous():
-            raise ValueError("out must be contiguous")
-    if lse is None:
-        if return_lse:
-            lse = torch.empty((S, Hq), dtype=torch.float32, device=device)
-    else:
-        _check_tensor("lse", lse, torch.float32, 2)
-        if lse.shape != (S, Hq) or lse.device != device:
-            raise ValueError("lse must be [%d, %d] on the tensors' device" % (S, Hq))
-    ws_bytes = 0
-    if workspace is None:
-        ws_bytes = lib.attn_decode_fp4_workspace_bytes(S, Hq, Hkv, d, max_blocks)
-        if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
-    else:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous on the tensors' device")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _launch(lib.attn_decode_paged_fp4, device, stream, q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
-            ctx_lens.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), S, Hq, Hkv, d, nb,
-            max_blocks, 1.0 / math.sqrt(d) if scale is None else scale, k_scale, v_scale,
-            None if workspace is None else workspace.data_ptr(), ws_bytes)
-    return out, lse
+    return (_native or _load_native()).decode_paged_fp4(q, kv_cache, block_table, ctx_lens, scale, k_scale, v_scale, out,
+                                                        lse, workspace, return_lse, stream)
 
 
 def attn_get_device_status(stream=None) -> int:

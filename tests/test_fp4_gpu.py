@@ -562,6 +562,26 @@ def test_threads_and_streams(env):
             assert torch.equal(x, y)
 
 
+def test_workspace_of_a_call_on_another_stream_is_not_reused_while_it_runs(env):
+    """The call allocates its workspace, uses it on the given stream and drops it;
+    what the current stream allocates next must not land there."""
+    torch, ex, dev = env
+    q, cache, table, lens = decode_case(560, [20000, 3], 8, 1, 128)
+    args = [to_dev(x, dev) for x in (q, cache, table, lens)]
+    want, want_lse = ex.attn_decode_paged_fp4(*args)
+    n = ex.attn_decode_fp4_workspace_bytes(2, 8, 1, 128, table.shape[1])
+    assert n > 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        out, lse = ex.attn_decode_paged_fp4(*args, stream=side)
+        for _ in range(3):
+            torch.full((n,), 0xFF, device=dev, dtype=torch.uint8)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 def test_append_captured_and_replayed(env):
     torch, ex, dev = env
     d, Hkv = 128, 2
