@@ -102,24 +102,4 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Scale of a group with largest magnitude `amax` (NaN when it holds one):
-// e4m3(amax / (6 g)), NaN when the group holds a NaN or an infinity, so that
-// the whole group reads back as NaN.  *divisor: what its values are divided
-// by before they are rounded to e2m1 (0: all of them round to 0).
-__device__ __forceinline__ uint32_t fp4_group_scale(float amax, float g, float* divisor) {
-  const uint32_t s8 = amax <= 3.4028234663852886e38f ? f32_to_e4m3(__fdiv_rn(amax, __fmul_rn(6.f, g))) : 0x7Fu;
-  *divisor = __fmul_rn(f16_lo(e4m3x2_to_f16(s8)), g);
-  return s8;
-}
-
-// Codes of eight values of a group.  The division is the correctly rounded
-// one: values of a few bits often lie exactly between two codes, and a
-// product with the reciprocal would not see that.
-__device__ __forceinline__ uint32_t fp4_encode8(const float (&x)[8], float divisor) {
-  float y[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = divisor == 0.f ? 0.f : __fdiv_rn(x[e], divisor);
-  return f32x8_to_e2m1(y);
-}
-
 }  // namespace exattn

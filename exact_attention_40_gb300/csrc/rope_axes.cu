@@ -11,8 +11,8 @@
 // its threads then walk the heads.  Thread (token, j) of d/16 threads a token
 // owns the 8 pairs 8 j .. 8 j + 7 of every head it visits (two 16-byte loads,
 // two 16-byte stores), so its cosines and sines stay in registers; `lanes`
-// such sets of threads share the heads.  Tiles shrink, and lanes grow, until
-// there are two CTAs an SM.
+// such sets of threads share the heads.  The first heads are loaded before the
+// angles are formed, so the two latencies overlap.
 #include <cuda_bf16.h>
 
 #include "fp4.cuh"
@@ -24,7 +24,6 @@ namespace exattn {
 namespace {
 
 constexpr int kTileThreads = 256;
-constexpr int kUnroll = 4;  // heads whose loads are in flight together
 
 // How a CTA's threads cover tokens and heads.
 struct Tile {
@@ -48,69 +47,113 @@ __device__ __forceinline__ void tile_angles(float2* cs, const RopeAxesTable& tab
   }
 }
 
-__device__ __forceinline__ void load_cs(const float2* cs, float (&c)[8], float (&s)[8], float sign) {
+// A thread's 8 cosines and sines as packed pairs.
+struct Turn8 {
+  uint64_t c[4], s[4];
+  __device__ __forceinline__ void load(const float2* cs, float sign) {
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    const float4 x = *reinterpret_cast<const float4*>(cs + e);
-    c[e] = x.x;
-    s[e] = sign * x.y;
-    c[e + 1] = x.z;
-    s[e + 1] = sign * x.w;
+    for (int e = 0; e < 4; ++e) {
+      const float4 x = *reinterpret_cast<const float4*>(cs + 2 * e);
+      c[e] = f2_pack(x.x, x.z);
+      s[e] = f2_pack(sign * x.y, sign * x.w);
+    }
+  }
+  // The turned pairs (a, b) of the vectors (lo, hi), two values in a register pair.
+  // Products are rounded before they are added (the one fused operation
+  // multiplies by -1), so that the fp32 result, and with it every 4-bit code, is
+  // the one that the definition's plain fp32 operations give.
+  __device__ __forceinline__ void turn(const uint4 lo, const uint4 hi, uint64_t (&ya)[4], uint64_t (&yb)[4]) const {
+    const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
+    const uint64_t minus_one = f2_pack(-1.f, -1.f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t a = f2_pack(__uint_as_float(l[e] << 16), __uint_as_float(l[e] & 0xFFFF0000u));
+      const uint64_t b = f2_pack(__uint_as_float(h[e] << 16), __uint_as_float(h[e] & 0xFFFF0000u));
+      ya[e] = f2_fma(f2_mul(b, s[e]), minus_one, f2_mul(a, c[e]));
+      yb[e] = f2_add(f2_mul(b, c[e]), f2_mul(a, s[e]));
+    }
+  }
+};
+
+__device__ __forceinline__ uint4 pack_pairs(const uint64_t (&y)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float a, b;
+    f2_unpack(y[e], a, b);
+    w[e] = pack_bf16x2(a, b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Two 16-byte vectors of one head.
+struct Vecs {
+  uint4 lo, hi;
+  __device__ __forceinline__ void load(const uint4* src, int apart) {
+    lo = src[0];
+    hi = src[apart];
+  }
+};
+
+// Heads first, first + step, ... below count of one view, two at a time: body(head,
+// vectors).  `have`: the first two are already in x.
+template <typename Body>
+__device__ __forceinline__ void walk_heads(const uint4* src, long long head, int first, int count, int step,
+                                           int apart, bool have, Vecs (&x)[2], Body body) {
+  for (int h = first; h < count; h += 2 * step) {
+    const bool two = h + step < count;
+    if (!have) {
+      x[0].load(src + h * head, apart);
+      if (two) x[1].load(src + (h + step) * head, apart);
+    }
+    have = false;
+    body(h, x[0]);
+    if (two) body(h + step, x[1]);
   }
 }
 
-__device__ __forceinline__ void turn8(const uint4 lo, const uint4 hi, const float (&c)[8], const float (&s)[8],
-                                      float (&a)[8], float (&b)[8]) {
-  unpack_bf16x8(lo, a);
-  unpack_bf16x8(hi, b);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) turn_pair(a[e], b[e], c[e], s[e]);
-}
-
-__global__ void __launch_bounds__(kTileThreads) rope_axes_kernel(const RopeAxesArgs a,
-                                                                 const __grid_constant__ RopeAxesTable table,
-                                                                 const Tile tile) {
+__global__ void __launch_bounds__(kTileThreads, 4) rope_axes_kernel(const RopeAxesArgs a,
+                                                                    const __grid_constant__ RopeAxesTable table,
+                                                                    const Tile tile) {
   extern __shared__ __align__(16) uint8_t rope_axes_smem[];
   float2* cs = reinterpret_cast<float2*>(rope_axes_smem);
-  const int half = a.d / 2, vec_half = half / 8;
+  const int half = a.d / 2, apart = half / 8;
   const unsigned int total = static_cast<unsigned int>(a.B) * a.N, n0 = blockIdx.x * tile.toks;
   const int count = static_cast<int>(min(total - n0, static_cast<unsigned int>(tile.toks)));
-  tile_angles(cs, table, half, count, [&](int tok, int axis) {
-    const unsigned int b = (n0 + tok) / a.N, n = n0 + tok - b * a.N;
-    return static_cast<long long>(a.positions[axis * a.pos_axis + b * a.pos_batch + n * a.pos_token]);
-  });
-  __syncthreads();
   const int j = threadIdx.x % tile.per_tok, rest = threadIdx.x / tile.per_tok;
   const int tok = rest % tile.toks, lane = rest / tile.toks;
-  if (lane >= tile.lanes || tok >= count) return;
-  float c[8], s[8];
-  load_cs(cs + tok * half + 8 * j, c, s, a.inverse ? -1.f : 1.f);
+  const bool works = lane < tile.lanes && tok < count;
   const unsigned int b = (n0 + tok) / a.N, n = n0 + tok - b * a.N;
-  const int heads = a.Hq + a.Hkv;
-  for (int h0 = lane; h0 < heads; h0 += kUnroll * tile.lanes) {
-    uint4 lo[kUnroll], hi[kUnroll];
-#pragma unroll
-    for (int x = 0; x < kUnroll; ++x) {
-      const int h = h0 + x * tile.lanes;
-      if (h < heads) {
-        const uint4* src = (h < a.Hq ? row_of(a.q, b, h, n) : row_of(a.k, b, h - a.Hq, n)) + j;
-        lo[x] = src[0];
-        hi[x] = src[vec_half];
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < kUnroll; ++x) {
-      const int h = h0 + x * tile.lanes;
-      if (h < heads) {
-        float ya[8], yb[8];
-        turn8(lo[x], hi[x], c, s, ya, yb);
-        uint4* dst =
-            const_cast<uint4*>(h < a.Hq ? row_of(a.q_out, b, h, n) : row_of(a.k_out, b, h - a.Hq, n)) + j;
-        dst[0] = pack_bf16x8(ya);
-        dst[vec_half] = pack_bf16x8(yb);
-      }
-    }
+  const uint4* q = row_of(a.q, b, 0, n) + j;
+  const uint4* k = row_of(a.k, b, 0, n) + j;
+  Vecs x[2];
+  if (works) {
+    if (lane < a.Hq) x[0].load(q + lane * a.q.head, apart);
+    if (lane + tile.lanes < a.Hq) x[1].load(q + (lane + tile.lanes) * a.q.head, apart);
   }
+  tile_angles(cs, table, half, count, [&](int at, int axis) {
+    const unsigned int pb = (n0 + at) / a.N, pn = n0 + at - pb * a.N;
+    return static_cast<long long>(a.positions[axis * a.pos_axis + pb * a.pos_batch + pn * a.pos_token]);
+  });
+  __syncthreads();
+  if (!works) return;
+  Turn8 turn;
+  turn.load(cs + tok * half + 8 * j, a.inverse ? -1.f : 1.f);
+  uint4* dst = const_cast<uint4*>(row_of(a.q_out, b, 0, n)) + j;
+  long long head = a.q_out.head;
+  auto body = [&](int h, const Vecs& v) {
+    uint64_t ya[4], yb[4];
+    turn.turn(v.lo, v.hi, ya, yb);
+    uint4* to = dst + h * head;
+    to[0] = pack_pairs(ya);
+    to[apart] = pack_pairs(yb);
+  };
+  walk_heads(q, a.q.head, lane, a.Hq, tile.lanes, apart, true, x, body);
+  // the key heads follow the query heads in the order the lanes share out
+  const int first = ((lane - a.Hq) % tile.lanes + tile.lanes) % tile.lanes;
+  dst = const_cast<uint4*>(row_of(a.k_out, b, 0, n)) + j;
+  head = a.k_out.head;
+  walk_heads(k, a.k.head, first, a.Hkv, tile.lanes, apart, false, x, body);
 }
 
 // Span index (block * Hkv) and offset of a token in the cache, or -1.
@@ -122,102 +165,167 @@ __device__ __forceinline__ long long find_block(const Fp4Slots& at, long long n,
   return blk >= 0 && blk < at.num_blocks ? blk : -1;
 }
 
-// Largest magnitude of 8 values, NaN if one is.
-__device__ __forceinline__ float amax8(const float (&x)[8]) {
+// Quantises groups of one tensor with fp32 scale g.
+//
+// Values of a few bits often lie exactly between two codes, so the quotients
+// have to be the correctly rounded ones; a product with the reciprocal would not
+// see those ties.  They come from the correctly rounded reciprocal r by one
+// step: q = x r, q + (x - q y) r with fused multiply-adds is x / y correctly
+// rounded (Markstein, IBM Journal of Research and Development 34, 1990).
+// That holds while nothing over- or underflows; the rare rest takes the
+// division itself.
+struct Quantiser {
+  float g, six_g, inv_six_g;
+  bool plain;  // 6 g and its reciprocal are of an ordinary size
+  __device__ __forceinline__ explicit Quantiser(float scale) {
+    g = scale;
+    six_g = __fmul_rn(6.f, scale);
+    inv_six_g = __frcp_rn(six_g);
+    plain = six_g > 1e-25f && six_g < 1e25f;
+  }
+
+  // Scale of a group with largest magnitude `amax` (NaN when it holds one):
+  // e4m3(amax / (6 g)), NaN when the group holds a NaN or an infinity, so that
+  // the whole group reads back as NaN.
+  __device__ __forceinline__ uint32_t scale(float amax) const {
+    if (!(amax <= 3.4028234663852886e38f)) return 0x7Fu;
+    float t = __fmul_rn(amax, inv_six_g);
+    if (plain && t < 1000.f)
+      t = __fmaf_rn(__fmaf_rn(-t, six_g, amax), inv_six_g, t);
+    else
+      t = __fdiv_rn(amax, six_g);
+    return f32_to_e4m3(t);
+  }
+
+  // Codes of 16 values with that scale, in order.
+  __device__ __forceinline__ uint2 codes(const float (&x)[16], float amax, uint32_t s8) const {
+    const float y = __fmul_rn(f16_lo(e4m3x2_to_f16(s8)), g);
+    float q[16];
+    // (a scale below the saturated one keeps every quotient under 8)
+    if (plain && s8 < 0x7Eu && s8 > 0u && amax < 1e25f) {
+      const float r = __frcp_rn(y);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float q0 = __fmul_rn(x[e], r);
+        q[e] = __fmaf_rn(__fmaf_rn(-q0, y, x[e]), r, q0);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) q[e] = y == 0.f ? 0.f : __fdiv_rn(x[e], y);
+    }
+    return make_uint2(f32x8_to_e2m1(q), f32x8_to_e2m1(q + 8));
+  }
+};
+
+// Largest magnitude of 16 values, NaN if one is.
+__device__ __forceinline__ float amax16(const float (&x)[16]) {
   float m = fabsf(x[0]);
 #pragma unroll
-  for (int e = 1; e < 8; ++e) m = max_nan(m, fabsf(x[e]));
+  for (int e = 1; e < 16; ++e) m = max_nan(m, fabsf(x[e]));
   return m;
 }
 
-// Append: heads in the order q, k, v.  A rotated key's 8 low (and 8 high)
-// columns are half of a scale group; the neighbouring thread has the other
-// half.  A value's thread takes a whole group.
+// Append.  A rotated key's thread has 8 low and 8 high columns, half of a scale
+// group each; neighbouring threads swap halves, so that the even one has the
+// low group and the odd one the high group.  A value's thread loads a whole
+// group.
 template <int D>
-__global__ void __launch_bounds__(kTileThreads) rope_cache_fp4_kernel(const RopeFp4Args a,
-                                                                      const __grid_constant__ RopeAxesTable table,
-                                                                      const Tile tile) {
+__global__ void __launch_bounds__(kTileThreads, 3) rope_cache_fp4_kernel(const RopeFp4Args a,
+                                                                         const __grid_constant__ RopeAxesTable table,
+                                                                         const Tile tile) {
   using Span = Fp4Span<D>;
-  constexpr int kHalf = D / 2, kVecHalf = kHalf / 8, kPerTok = D / 16;
+  constexpr int kHalf = D / 2, kApart = kHalf / 8, kPerTok = D / 16;
   extern __shared__ __align__(16) uint8_t rope_axes_smem[];
   float2* cs = reinterpret_cast<float2*>(rope_axes_smem);
   const long long n0 = static_cast<long long>(blockIdx.x) * tile.toks;
   const int count = static_cast<int>(a.at.num_tokens - n0 < tile.toks ? a.at.num_tokens - n0 : tile.toks);
-  tile_angles(cs, table, kHalf, count,
-              [&](int tok, int axis) { return static_cast<long long>(a.positions[axis * a.pos_axis + n0 + tok]); });
-  __syncthreads();
   const int j = threadIdx.x % kPerTok, rest = threadIdx.x / kPerTok;
   const int tok = rest % tile.toks, lane = rest / tile.toks;
-  if (lane >= tile.lanes || tok >= count) return;
-  const unsigned int pair_mask = 3u << (threadIdx.x & 30);  // this thread and its neighbour: same token and heads
+  const bool works = lane < tile.lanes && tok < count;
   const long long n = n0 + tok;
-  float c[8], s[8];
-  load_cs(cs + tok * kHalf + 8 * j, c, s, 1.f);
-  int off;
-  const long long blk = find_block(a.at, n, &off);
-  if (blk < 0 && j == 0 && lane == 0) atomicOr(a.at.status, 2u);  // EXATTN_DEVICE_BOUNDS_BIT
-  uint8_t* spans = static_cast<uint8_t*>(a.kv_cache) + (blk < 0 ? 0 : blk) * a.Hkv * Span::kBytes;
-  const int heads = a.Hq + 2 * a.Hkv;
-  for (int h0 = lane; h0 < heads; h0 += kUnroll * tile.lanes) {
-    uint4 lo[kUnroll], hi[kUnroll];
-#pragma unroll
-    for (int x = 0; x < kUnroll; ++x) {
-      const int h = h0 + x * tile.lanes;
-      if (h < a.Hq + a.Hkv) {
-        const uint4* src = (h < a.Hq ? row_of(a.q, 0, h, n) : row_of(a.k, 0, h - a.Hq, n)) + j;
-        lo[x] = src[0];
-        hi[x] = src[kVecHalf];
-      } else if (h < heads) {
-        const uint4* src = row_of(a.v, 0, h - a.Hq - a.Hkv, n) + 2 * j;
-        lo[x] = src[0];
-        hi[x] = src[1];
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < kUnroll; ++x) {
-      const int h = h0 + x * tile.lanes;
-      float ya[8], yb[8];
-      if (h < a.Hq) {
-        turn8(lo[x], hi[x], c, s, ya, yb);
-        uint4* dst = const_cast<uint4*>(row_of(a.q_out, 0, h, n)) + j;
-        dst[0] = pack_bf16x8(ya);
-        dst[kVecHalf] = pack_bf16x8(yb);
-      } else if (h < a.Hq + a.Hkv) {
-        turn8(lo[x], hi[x], c, s, ya, yb);
-        float ma = amax8(ya), mb = amax8(yb);
-        ma = max_nan(ma, __shfl_xor_sync(pair_mask, ma, 1));
-        mb = max_nan(mb, __shfl_xor_sync(pair_mask, mb, 1));
-        float da, db;
-        const uint32_t sa = fp4_group_scale(ma, a.k_scale, &da), sb = fp4_group_scale(mb, a.k_scale, &db);
-        if (blk >= 0) {
-          uint8_t* span = spans + static_cast<size_t>(h - a.Hq) * Span::kBytes;
-          uint32_t* codes = reinterpret_cast<uint32_t*>(span + Span::kKeyCodes + off * Span::kCodeRow) + j;
-          codes[0] = fp4_encode8(ya, da);
-          codes[kPerTok] = fp4_encode8(yb, db);
-          // the even thread of a pair stores the low group's scale, the odd one the high one's
-          span[Span::kKeyScales + off * Span::kScaleRow + j / 2 + (j & 1) * (Span::kScaleRow / 2)] =
-              static_cast<uint8_t>(j & 1 ? sb : sa);
-        }
-      } else if (h < heads && blk >= 0) {
-        unpack_bf16x8(lo[x], ya);
-        unpack_bf16x8(hi[x], yb);
-        float dv;
-        const uint32_t sv = fp4_group_scale(max_nan(amax8(ya), amax8(yb)), a.v_scale, &dv);
-        uint8_t* span = spans + static_cast<size_t>(h - a.Hq - a.Hkv) * Span::kBytes;
-        reinterpret_cast<uint2*>(span + Span::kValueCodes + off * Span::kCodeRow)[j] =
-            make_uint2(fp4_encode8(ya, dv), fp4_encode8(yb, dv));
-        span[Span::kValueScales + off * Span::kScaleRow + j] = static_cast<uint8_t>(sv);
-      }
-    }
+  const uint4* q = row_of(a.q, 0, 0, n) + j;
+  Vecs x[2];
+  int off = 0;
+  long long blk = -1;
+  if (works) {
+    if (lane < a.Hq) x[0].load(q + lane * a.q.head, kApart);
+    if (lane + tile.lanes < a.Hq) x[1].load(q + (lane + tile.lanes) * a.q.head, kApart);
+    blk = find_block(a.at, n, &off);
+    if (blk < 0 && j == 0 && lane == 0) atomicOr(a.at.status, 2u);  // EXATTN_DEVICE_BOUNDS_BIT
   }
+  tile_angles(cs, table, kHalf, count,
+              [&](int at, int axis) { return static_cast<long long>(a.positions[axis * a.pos_axis + n0 + at]); });
+  __syncthreads();
+  if (!works) return;
+  uint8_t* spans = static_cast<uint8_t*>(a.kv_cache) + (blk < 0 ? 0 : blk) * a.Hkv * Span::kBytes;
+  const int step = tile.lanes;
+  {
+    Turn8 turn;
+    turn.load(cs + tok * kHalf + 8 * j, 1.f);
+    uint4* dst = const_cast<uint4*>(row_of(a.q_out, 0, 0, n)) + j;
+    walk_heads(q, a.q.head, lane, a.Hq, step, kApart, true, x, [&](int h, const Vecs& v) {
+      uint64_t ya[4], yb[4];
+      turn.turn(v.lo, v.hi, ya, yb);
+      uint4* to = dst + h * a.q_out.head;
+      to[0] = pack_pairs(ya);
+      to[kApart] = pack_pairs(yb);
+    });
+    // the key and value heads follow the query heads in the order the lanes share out
+    const int first = ((lane - a.Hq) % step + step) % step;
+    const Quantiser quant(a.k_scale);
+    const bool odd = j & 1;
+    const unsigned int pair_mask = 3u << (threadIdx.x & 30);  // this thread and its neighbour: same token and heads
+    // the group this thread ends up with: j / 2 of the low half, or of the high one
+    const int group = j / 2 + (odd ? kPerTok / 2 : 0);
+    uint8_t* code = spans + Span::kKeyCodes + off * Span::kCodeRow + group * 8;
+    uint8_t* scale = spans + Span::kKeyScales + off * Span::kScaleRow + group;
+    walk_heads(row_of(a.k, 0, 0, n) + j, a.k.head, first, a.Hkv, step, kApart, false, x, [&](int h, const Vecs& v) {
+      uint64_t ya[4], yb[4];
+      turn.turn(v.lo, v.hi, ya, yb);
+      float y[16];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // the even thread gives its high half for the odd one's low half
+        const uint64_t mine = odd ? yb[e] : ya[e];
+        const uint64_t other = __shfl_xor_sync(pair_mask, odd ? ya[e] : yb[e], 1);
+        f2_unpack(odd ? other : mine, y[2 * e], y[2 * e + 1]);
+        f2_unpack(odd ? mine : other, y[8 + 2 * e], y[8 + 2 * e + 1]);
+      }
+      const float m = amax16(y);
+      const uint32_t s8 = quant.scale(m);
+      if (blk >= 0) {
+        *reinterpret_cast<uint2*>(code + h * Span::kBytes) = quant.codes(y, m, s8);
+        scale[h * Span::kBytes] = static_cast<uint8_t>(s8);
+      }
+    });
+  }
+  if (blk < 0) return;
+  const Quantiser quant(a.v_scale);
+  const int first = ((lane - a.Hq - a.Hkv) % step + step) % step;
+  uint8_t* code = spans + Span::kValueCodes + off * Span::kCodeRow + j * 8;
+  uint8_t* scale = spans + Span::kValueScales + off * Span::kScaleRow + j;
+  walk_heads(row_of(a.v, 0, 0, n) + 2 * j, a.v.head, first, a.Hkv, step, 1, false, x, [&](int h, const Vecs& v) {
+    float y[16];
+    const uint32_t w[8] = {v.lo.x, v.lo.y, v.lo.z, v.lo.w, v.hi.x, v.hi.y, v.hi.z, v.hi.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[2 * e] = __uint_as_float(w[e] << 16);
+      y[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
+    const float m = amax16(y);
+    const uint32_t s8 = quant.scale(m);
+    *reinterpret_cast<uint2*>(code + h * Span::kBytes) = quant.codes(y, m, s8);
+    scale[h * Span::kBytes] = static_cast<uint8_t>(s8);
+  });
 }
 
 // Read: thread j of a token takes group j of the keys and values of every head
-// it visits.
+// it visits, rows 2 h (key) and 2 h + 1 (value).
 template <int D>
-__global__ void __launch_bounds__(kTileThreads) cache_read_fp4_kernel(const ReadFp4Args a, const Tile tile) {
+__global__ void __launch_bounds__(kTileThreads, 6) cache_read_fp4_kernel(const ReadFp4Args a, const Tile tile) {
   using Span = Fp4Span<D>;
   constexpr int kPerTok = D / 16;
+  constexpr int kUnroll = 2;
   const int j = threadIdx.x % kPerTok, rest = threadIdx.x / kPerTok;
   const int tok = rest % tile.toks, lane = rest / tile.toks;
   const long long n = static_cast<long long>(blockIdx.x) * tile.toks + tok;
@@ -226,7 +334,9 @@ __global__ void __launch_bounds__(kTileThreads) cache_read_fp4_kernel(const Read
   const long long blk = find_block(a.at, n, &off);
   if (blk < 0 && j == 0 && lane == 0) atomicOr(a.at.status, 2u);  // EXATTN_DEVICE_BOUNDS_BIT
   const uint8_t* spans = static_cast<const uint8_t*>(a.kv_cache) + (blk < 0 ? 0 : blk) * a.Hkv * Span::kBytes;
-  // rows 2 h: key of head h, rows 2 h + 1: its value
+  const int code_off = off * Span::kCodeRow + 8 * j, scale_off = off * Span::kScaleRow + j;
+  uint4* k_out = const_cast<uint4*>(row_of(a.k_out, 0, 0, n)) + 2 * j;
+  uint4* v_out = const_cast<uint4*>(row_of(a.v_out, 0, 0, n)) + 2 * j;
   for (int r0 = lane; r0 < 2 * a.Hkv; r0 += kUnroll * tile.lanes) {
     uint2 codes[kUnroll];
     uint32_t scale[kUnroll];
@@ -237,34 +347,25 @@ __global__ void __launch_bounds__(kTileThreads) cache_read_fp4_kernel(const Read
       scale[x] = 0u;
       if (r < 2 * a.Hkv && blk >= 0) {
         const uint8_t* span = spans + static_cast<size_t>(r >> 1) * Span::kBytes;
-        codes[x] = reinterpret_cast<const uint2*>(span + (r & 1 ? Span::kValueCodes : Span::kKeyCodes) +
-                                                  off * Span::kCodeRow)[j];
-        scale[x] = span[(r & 1 ? Span::kValueScales : Span::kKeyScales) + off * Span::kScaleRow + j];
+        codes[x] = *reinterpret_cast<const uint2*>(span + (r & 1 ? Span::kValueCodes : Span::kKeyCodes) + code_off);
+        scale[x] = span[(r & 1 ? Span::kValueScales : Span::kKeyScales) + scale_off];
       }
     }
 #pragma unroll
     for (int x = 0; x < kUnroll; ++x) {
       const int r = r0 + x * tile.lanes;
       if (r >= 2 * a.Hkv) break;
-      const uint32_t s8 = e4m3x2_to_f16(scale[x] | (scale[x] << 8));
+      const uint32_t s8 = e4m3x2_to_f16(__byte_perm(scale[x], 0, 0x4400));
       const float g = r & 1 ? a.v_scale : a.k_scale;
-      uint32_t h[8], w[8];
-      {
-        uint32_t h0[4], h1[4];
-        e2m1x8_to_f16(codes[x].x, h0);
-        e2m1x8_to_f16(codes[x].y, h1);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          h[e] = h0[e];
-          h[4 + e] = h1[e];
-        }
-      }
+      uint32_t h0[4], h1[4], w[8];
+      e2m1x8_to_f16(codes[x].x, h0);
+      e2m1x8_to_f16(codes[x].y, h1);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t v = f16x2_mul(h[e], s8);
+        const uint32_t v = f16x2_mul(e < 4 ? h0[e & 3] : h1[e & 3], s8);
         w[e] = pack_bf16x2(__fmul_rn(f16_lo(v), g), __fmul_rn(f16_hi(v), g));
       }
-      uint4* dst = const_cast<uint4*>(row_of(r & 1 ? a.v_out : a.k_out, 0, r >> 1, n)) + 2 * j;
+      uint4* dst = r & 1 ? v_out + (r >> 1) * a.v_out.head : k_out + (r >> 1) * a.k_out.head;
       dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
       dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
@@ -272,14 +373,15 @@ __global__ void __launch_bounds__(kTileThreads) cache_read_fp4_kernel(const Read
 }
 
 // Tokens per CTA: as many as the threads hold, halved while there are fewer
-// than two CTAs an SM; the other threads share the `rows` heads of a token.
-Tile make_tile(int d, long long tokens, int rows, int sms) {
+// CTAs than `want` and a thread would still have two of a token's `rows` heads
+// to walk; the threads that frees share the heads.
+Tile make_tile(int d, long long tokens, int rows, long long want) {
   Tile t;
   t.per_tok = d / 16;
   const int slots = kTileThreads / t.per_tok;
   t.toks = 1;
   while (2 * t.toks <= slots) t.toks *= 2;
-  while (t.toks > 1 && (tokens + t.toks - 1) / t.toks < 2ll * sms && slots / t.toks < rows) t.toks /= 2;
+  while (t.toks > 1 && (tokens + t.toks - 1) / t.toks < want && 2 * (slots / t.toks) <= rows) t.toks /= 2;
   t.lanes = slots / t.toks;
   return t;
 }
@@ -294,7 +396,7 @@ cudaError_t launch_rope_axes(const RopeAxesArgs& a, const RopeAxesTable& table, 
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   const long long tokens = static_cast<long long>(a.B) * a.N;
-  const Tile t = make_tile(a.d, tokens, a.Hq + a.Hkv, sms);
+  const Tile t = make_tile(a.d, tokens, a.Hq + a.Hkv, 4ll * sms);
   rope_axes_kernel<<<tiles(t, tokens), kTileThreads, sizeof(float2) * t.toks * (a.d / 2), stream>>>(a, table, t);
   return cudaGetLastError();
 }
@@ -302,7 +404,7 @@ cudaError_t launch_rope_axes(const RopeAxesArgs& a, const RopeAxesTable& table, 
 cudaError_t launch_rope_cache_write_fp4(const RopeFp4Args& a, const RopeAxesTable& table, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const Tile t = make_tile(a.d, a.at.num_tokens, a.Hq + 2 * a.Hkv, sms);
+  const Tile t = make_tile(a.d, a.at.num_tokens, a.Hq + 2 * a.Hkv, 4ll * sms);
   const unsigned int grid = tiles(t, a.at.num_tokens);
   const size_t smem = sizeof(float2) * t.toks * (a.d / 2);
   if (a.d == 64)
@@ -315,7 +417,7 @@ cudaError_t launch_rope_cache_write_fp4(const RopeFp4Args& a, const RopeAxesTabl
 cudaError_t launch_cache_read_fp4(const ReadFp4Args& a, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const Tile t = make_tile(a.d, a.at.num_tokens, 2 * a.Hkv, sms);
+  const Tile t = make_tile(a.d, a.at.num_tokens, 2 * a.Hkv, 4ll * sms);
   const unsigned int grid = tiles(t, a.at.num_tokens);
   if (a.d == 64)
     cache_read_fp4_kernel<64><<<grid, kTileThreads, 0, stream>>>(a, t);

@@ -55,14 +55,4 @@ __device__ __forceinline__ float2 turn_cos_sin(unsigned long long turn) {
   return make_float2((quadrant == 1u || quadrant == 2u) ? -cq : cq, quadrant >= 2u ? -sq : sq);
 }
 
-// Turns the pair (a, b) with separately rounded products (no fused
-// multiply-add), so that the fp32 result, and with it every 4-bit code, is the
-// one that the definition's plain fp32 operations give.
-__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
-  const float ya = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-  const float yb = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-  a = ya;
-  b = yb;
-}
-
 }  // namespace exattn
