@@ -24,6 +24,8 @@ namespace exattn {
 namespace {
 
 constexpr int kTileThreads = 256;
+constexpr int kRopeLanes = 8;  // heads of a token in flight together
+constexpr int kFp4Lanes = 4;
 
 // How a CTA's threads cover tokens and heads.
 struct Tile {
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) rope_cache_fp4_kernel(const R
 }
 
 // Read: thread j of a token takes group j of the keys and values of every head
-// it visits, rows 2 h (key) and 2 h + 1 (value).
+// it visits: rows 0 .. Hkv - 1 are keys, the next Hkv values.
 template <int D>
 __global__ void __launch_bounds__(kTileThreads, 6) cache_read_fp4_kernel(const ReadFp4Args a, const Tile tile) {
   using Span = Fp4Span<D>;
@@ -346,9 +348,9 @@ __global__ void __launch_bounds__(kTileThreads, 6) cache_read_fp4_kernel(const R
       codes[x] = make_uint2(0u, 0u);
       scale[x] = 0u;
       if (r < 2 * a.Hkv && blk >= 0) {
-        const uint8_t* span = spans + static_cast<size_t>(r >> 1) * Span::kBytes;
-        codes[x] = *reinterpret_cast<const uint2*>(span + (r & 1 ? Span::kValueCodes : Span::kKeyCodes) + code_off);
-        scale[x] = span[(r & 1 ? Span::kValueScales : Span::kKeyScales) + scale_off];
+        const uint8_t* span = spans + static_cast<size_t>(r >= a.Hkv ? r - a.Hkv : r) * Span::kBytes;
+        codes[x] = *reinterpret_cast<const uint2*>(span + (r >= a.Hkv ? Span::kValueCodes : Span::kKeyCodes) + code_off);
+        scale[x] = span[(r >= a.Hkv ? Span::kValueScales : Span::kKeyScales) + scale_off];
       }
     }
 #pragma unroll
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(kTileThreads, 6) cache_read_fp4_kernel(const R
       const int r = r0 + x * tile.lanes;
       if (r >= 2 * a.Hkv) break;
       const uint32_t s8 = e4m3x2_to_f16(__byte_perm(scale[x], 0, 0x4400));
-      const float g = r & 1 ? a.v_scale : a.k_scale;
+      const float g = r >= a.Hkv ? a.v_scale : a.k_scale;
       uint32_t h0[4], h1[4], w[8];
       e2m1x8_to_f16(codes[x].x, h0);
       e2m1x8_to_f16(codes[x].y, h1);
@@ -365,23 +367,24 @@ __global__ void __launch_bounds__(kTileThreads, 6) cache_read_fp4_kernel(const R
         const uint32_t v = f16x2_mul(e < 4 ? h0[e & 3] : h1[e & 3], s8);
         w[e] = pack_bf16x2(__fmul_rn(f16_lo(v), g), __fmul_rn(f16_hi(v), g));
       }
-      uint4* dst = r & 1 ? v_out + (r >> 1) * a.v_out.head : k_out + (r >> 1) * a.k_out.head;
+      uint4* dst = r >= a.Hkv ? v_out + (r - a.Hkv) * a.v_out.head : k_out + r * a.k_out.head;
       dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
       dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
   }
 }
 
-// Tokens per CTA: as many as the threads hold, halved while there are fewer
-// CTAs than `want` and a thread would still have two of a token's `rows` heads
-// to walk; the threads that frees share the heads.
-Tile make_tile(int d, long long tokens, int rows, long long want) {
+// A tile of as many tokens as the threads hold with `lanes` heads of each
+// walked at once (fewer where a token has fewer rows), halved while it leaves
+// SMs without a CTA and a token still has rows for the threads that frees.
+Tile make_tile(int d, long long tokens, int rows, int lanes, int sms) {
   Tile t;
   t.per_tok = d / 16;
   const int slots = kTileThreads / t.per_tok;
+  while (lanes > rows) lanes /= 2;
   t.toks = 1;
-  while (2 * t.toks <= slots) t.toks *= 2;
-  while (t.toks > 1 && (tokens + t.toks - 1) / t.toks < want && 2 * (slots / t.toks) <= rows) t.toks /= 2;
+  while (2 * t.toks * lanes <= slots) t.toks *= 2;
+  while (t.toks > 1 && (tokens + t.toks - 1) / t.toks < sms && 2 * (slots / t.toks) <= rows) t.toks /= 2;
   t.lanes = slots / t.toks;
   return t;
 }
@@ -396,7 +399,7 @@ cudaError_t launch_rope_axes(const RopeAxesArgs& a, const RopeAxesTable& table, 
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   const long long tokens = static_cast<long long>(a.B) * a.N;
-  const Tile t = make_tile(a.d, tokens, a.Hq + a.Hkv, 4ll * sms);
+  const Tile t = make_tile(a.d, tokens, a.Hq + a.Hkv, kRopeLanes, sms);
   rope_axes_kernel<<<tiles(t, tokens), kTileThreads, sizeof(float2) * t.toks * (a.d / 2), stream>>>(a, table, t);
   return cudaGetLastError();
 }
@@ -404,7 +407,7 @@ cudaError_t launch_rope_axes(const RopeAxesArgs& a, const RopeAxesTable& table, 
 cudaError_t launch_rope_cache_write_fp4(const RopeFp4Args& a, const RopeAxesTable& table, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const Tile t = make_tile(a.d, a.at.num_tokens, a.Hq + 2 * a.Hkv, 4ll * sms);
+  const Tile t = make_tile(a.d, a.at.num_tokens, a.Hq + 2 * a.Hkv, kFp4Lanes, sms);
   const unsigned int grid = tiles(t, a.at.num_tokens);
   const size_t smem = sizeof(float2) * t.toks * (a.d / 2);
   if (a.d == 64)
@@ -417,7 +420,7 @@ cudaError_t launch_rope_cache_write_fp4(const RopeFp4Args& a, const RopeAxesTabl
 cudaError_t launch_cache_read_fp4(const ReadFp4Args& a, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const Tile t = make_tile(a.d, a.at.num_tokens, 2 * a.Hkv, 4ll * sms);
+  const Tile t = make_tile(a.d, a.at.num_tokens, 2 * a.Hkv, kFp4Lanes, sms);
   const unsigned int grid = tiles(t, a.at.num_tokens);
   if (a.d == 64)
     cache_read_fp4_kernel<64><<<grid, kTileThreads, 0, stream>>>(a, t);
