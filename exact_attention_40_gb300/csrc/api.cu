@@ -843,11 +843,8 @@ int attn_cache_read_fp4(const void* kv_cache, const int32_t* seq_ids, const int3
 
 size_t attn_decode_fp4_workspace_bytes(int num_seqs, int Hq, int Hkv, int d, int max_blocks_per_seq) {
   if (num_seqs < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128) || max_blocks_per_seq < 1) return 0;
-  const size_t splits =
-      static_cast<size_t>(exattn::fp4_decode_splits(num_seqs, Hkv, Hq / Hkv, max_blocks_per_seq));
-  if (splits == 1) return 0;
-  const size_t rows = static_cast<size_t>(num_seqs) * Hq * splits;
-  return rows * d * sizeof(float) + ((rows * sizeof(float) + 15) & ~static_cast<size_t>(15));
+  const exattn::Fp4Plan plan(num_seqs, Hkv, Hq / Hkv, max_blocks_per_seq);
+  return plan.fits ? plan.bytes(d) : 0;
 }
 
 int attn_decode_paged_fp4(const void* q, const void* kv_cache, const int32_t* block_table, const int32_t* ctx_lens,
@@ -859,9 +856,7 @@ int attn_decode_paged_fp4(const void* q, const void* kv_cache, const int32_t* bl
   if (rc != EXATTN_OK) return rc;
   if (Hq % Hkv != 0 || !good_scale(scale) || !good_scale(k_scale) || !good_scale(v_scale))
     return EXATTN_ERR_INVALID_ARG;
-  const int group = Hq / Hkv;
-  const int rows = exattn::fp4_decode_rows(group);
-  if (num_seqs > 65535 || Hq > 65535 || static_cast<int64_t>(Hkv) * ((group + rows - 1) / rows) > 65535)
+  if (num_seqs > 65535 || Hq > 65535 || static_cast<int64_t>(num_seqs) * Hq > 0x7FFFFFFF)
     return EXATTN_ERR_UNSUPPORTED;
   if (num_seqs == 0) return EXATTN_OK;
   if (q == nullptr || kv_cache == nullptr || block_table == nullptr || ctx_lens == nullptr || out == nullptr)
@@ -869,31 +864,17 @@ int attn_decode_paged_fp4(const void* q, const void* kv_cache, const int32_t* bl
   if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(out) || !aligned4(block_table) || !aligned4(ctx_lens) ||
       !aligned4(lse))
     return EXATTN_ERR_ALIGNMENT;
-  const size_t need = attn_decode_fp4_workspace_bytes(num_seqs, Hq, Hkv, d, max_blocks_per_seq);
+  const exattn::Fp4Plan plan(num_seqs, Hkv, Hq / Hkv, max_blocks_per_seq);
+  if (!plan.fits) return EXATTN_ERR_UNSUPPORTED;
+  const size_t need = plan.bytes(d);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EXATTN_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return EXATTN_ERR_ALIGNMENT;
-  exattn::DecodeFp4Args a;
   exattn::DeviceGuard g;
   if ((rc = status_word(&g.status)) != EXATTN_OK) return rc;
   g.wait_ns = wait_budget_ns();
-  a.q = q;
-  a.kv_cache = kv_cache;
-  a.block_table = block_table;
-  a.ctx_lens = ctx_lens;
-  a.out = out;
-  a.lse = lse;
-  a.splits = exattn::fp4_decode_splits(num_seqs, Hkv, group, max_blocks_per_seq);
-  a.ws_o = static_cast<float*>(workspace);
-  a.ws_lse = a.ws_o + (need > 0 ? static_cast<size_t>(num_seqs) * Hq * a.splits * d : 0);
-  a.num_seqs = num_seqs;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.d = d;
-  a.num_blocks = num_blocks;
-  a.max_blocks_per_seq = max_blocks_per_seq;
-  a.scale = scale;
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
+  const exattn::DecodeFp4Args a{q,   kv_cache, block_table, ctx_lens, out,       lse,
+                                workspace, plan, num_seqs, Hq, Hkv, d, num_blocks, max_blocks_per_seq,
+                                scale, k_scale, v_scale};
   return exattn::launch_decode_fp4(a, g, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXATTN_OK
                                                                                            : EXATTN_ERR_CUDA;
 }

@@ -173,27 +173,44 @@ struct ReadFp4Args {
 
 cudaError_t launch_cache_read_fp4(const ReadFp4Args& a, cudaStream_t stream);
 
-// Query heads a CTA of the 4-bit decode takes: 8 columns of an mma, or 16 for
-// the larger groups.
-inline int fp4_decode_rows(int group) { return group <= 8 ? 8 : 16; }
+constexpr int kFp4UnitBlocks = 8;       // blocks in a unit of the 4-bit decode's work
+constexpr int kFp4MaxCtas = 152 * 4;    // its grid: one wave, four CTAs for each SM
 
-constexpr int kFp4MinSplitBlocks = 8;      // blocks a split takes at least: a pair per warp
-constexpr int kFp4MaxSplits = 152 * 4;     // four CTAs for each SM
+// A segment (the query heads of one sequence that share a KV head, in chunks
+// of `rows`) that starts in CTA `cta` and goes on through `more` further CTAs.
+struct Fp4Joint {
+  int cta, more;
+  int row;   // its first row of the output
+  int rows;  // and how many
+};
 
-// Splits of a sequence: enough CTAs for three waves of four per SM, but none
-// of fewer than kFp4MinSplitBlocks blocks.  By the call's sizes alone, so that
-// the workspace can be sized on any host.
-#include <cstdlib>
-inline int fp4_decode_splits(int num_seqs, int Hkv, int group, int max_blocks_per_seq) {
-  static const int want_ctas = getenv("FP4_WANT") ? atoi(getenv("FP4_WANT")) : 152*4;
-  static const int min_blk = getenv("FP4_MIN") ? atoi(getenv("FP4_MIN")) : 8;
-  const int rows = fp4_decode_rows(group);
-  const long long base = static_cast<long long>(num_seqs) * Hkv * ((group + rows - 1) / rows);
-  long long want = (want_ctas + base - 1) / base;
-  if (want > kFp4MaxSplits) want = kFp4MaxSplits;
-  const long long most = (static_cast<long long>(max_blocks_per_seq) + min_blk - 1) / min_blk;
-  return static_cast<int>(want < most ? want : most);
-}
+// How the 4-bit decode divides a call.  By the call's sizes alone, so that the
+// workspace can be sized on any host and a captured graph stays good.
+struct Fp4Plan {
+  int rows;               // query heads per segment: 8 columns of an mma, or 16 for larger groups
+  int chunks;             // segments per KV head
+  int ctas;               // shares: one wave, but no more than there can be units
+  int joints;             // entries for segments that several CTAs share; 0 where none can be
+  int joint_per_segment;  // indexed by segment where those are fewer than the CTAs
+  bool fits;              // the units' numbers fit 32 bits
+  Fp4Plan(int num_seqs, int Hkv, int group, int max_blocks_per_seq) {
+    rows = group <= 8 ? 8 : 16;
+    chunks = (group + rows - 1) / rows;
+    const long long segments = static_cast<long long>(num_seqs) * Hkv * chunks;
+    const long long units = segments * ((max_blocks_per_seq + kFp4UnitBlocks - 1) / kFp4UnitBlocks);
+    const int wave = rows == 8 ? kFp4MaxCtas : kFp4MaxCtas / 4 * 3;  // three CTAs an SM with 16 heads
+    ctas = static_cast<int>(units < wave ? units : wave);
+    joint_per_segment = segments <= ctas ? 1 : 0;
+    joints = static_cast<int>(units == segments ? 0 : joint_per_segment ? segments : ctas);
+    fits = units <= 0x7FFFFFFF;
+  }
+  size_t joint_bytes() const { return sizeof(Fp4Joint) * joints; }
+  size_t part_bytes(int d) const { return sizeof(float) * 2 * ctas * rows * d; }
+  // of the workspace: joints, partial outputs, their log-sum-exp
+  size_t bytes(int d) const {
+    return joints == 0 ? 0 : joint_bytes() + part_bytes(d) + sizeof(float) * 2 * ctas * rows;
+  }
+};
 
 struct DecodeFp4Args {
   const void* q;
@@ -202,9 +219,9 @@ struct DecodeFp4Args {
   const int32_t* ctx_lens;
   void* out;
   float* lse;
-  float* ws_o;    // [num_seqs, Hq, splits, d]
-  float* ws_lse;  // [num_seqs, Hq, splits]
-  int num_seqs, Hq, Hkv, d, num_blocks, max_blocks_per_seq, splits;
+  void* workspace;  // joints, then partial outputs [2 ctas][rows][d] and their lse
+  Fp4Plan plan;
+  int num_seqs, Hq, Hkv, d, num_blocks, max_blocks_per_seq;
   float scale, k_scale, v_scale;
 };
 
