@@ -57,7 +57,7 @@ struct Fp4SplitParams {
   const uint8_t* cache;
   const int32_t* block_table;
   const int32_t* ctx_lens;
-  Fp4Joint* joints;  // NULL where no segment can have a second unit
+  Fp4Joint* joints;  // one per CTA: its last segment, where others go on with it; or NULL
   float* ws_o;    // [2 * ctas][rows][d]
   float* ws_lse;  // [2 * ctas][rows]
   __nv_bfloat16* out;
@@ -65,7 +65,6 @@ struct Fp4SplitParams {
   unsigned int* status;
   unsigned long long wait_ns;
   int num_seqs, Hq, Hkv, group, n_chunks, num_blocks, max_blocks_per_seq;
-  int joint_per_segment;  // joints are indexed by segment, else by CTA
   float scale_log2;       // scale * k_scale * log2 e
   float v_scale;
 };
@@ -140,11 +139,9 @@ struct Fp4Smem {
   alignas(128) uint8_t ring[kWarps][kStages][2 * Fp4Span<D>::kBytes];
   float acc[kWarps][8 * NT][kAccStride];
   uint64_t full[kWarps][kStages];
-  float wm[kWarps][8 * NT];   // per-warp running max (log2 units)
-  float wl[kWarps][8 * NT];   // per-warp sum of the weights
-  float wlr[kWarps][8 * NT];  // ... of the rounded weights
-  int scan[kWarps];
-  int first_seq, first_ctx, first_prefix;  // the share's first sequence, units before it per segment
+  float wm[2][kWarps][8 * NT];   // per-warp running max (log2 units)
+  float wl[2][kWarps][8 * NT];   // per-warp sum of the weights
+  float wlr[2][kWarps][8 * NT];  // ... of the rounded weights
 };
 
 // Equal contiguous shares of `total` units for `parts` CTAs, the first
@@ -164,6 +161,75 @@ struct Place {
   int seq, y, k, units, ctx;
 };
 
+__device__ __forceinline__ int units_of(int ctx) { return (ctx + kUnit * kBlk - 1) / (kUnit * kBlk); }
+
+// Sums over the sequences that a warp forms from ctx_lens, each lane holding a
+// contiguous range of them.
+struct Batch {
+  const int32_t* ctx_lens;
+  unsigned int* status;
+  int max_ctx, num_seqs;
+  int lane_begin, before, mine;  // this lane's first sequence, the units before it, in its range
+  int first_ctx;                 // of its first sequence
+  int per_segment;               // units of all sequences (of one segment of each)
+
+  __device__ __forceinline__ int ctx_of(int s) const { return clamp_ctx(__ldg(ctx_lens + s), max_ctx, status); }
+
+  __device__ __forceinline__ Batch(const int32_t* lens, int seqs, int longest, unsigned int* word) {
+    ctx_lens = lens;
+    num_seqs = seqs;
+    max_ctx = longest;
+    status = word;
+    const int lane = threadIdx.x & 31;
+    const int range = (seqs + 31) / 32;
+    lane_begin = min(seqs, lane * range);
+    const int end = min(seqs, lane_begin + range);
+    first_ctx = lane_begin < end ? ctx_of(lane_begin) : 0;
+    mine = units_of(first_ctx);
+#pragma unroll 4
+    for (int s = lane_begin + 1; s < end; ++s) mine += units_of(ctx_of(s));
+    int upto = mine;  // inclusive sum over the lanes
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, x);
+      if (lane >= x) upto += v;
+    }
+    per_segment = __shfl_sync(0xffffffffu, upto, 31);
+    before = upto - mine;
+  }
+
+  // The place of a unit (below per_segment * segs); whole warp, same unit.
+  __device__ __forceinline__ Place find(int unit, int segs) const {
+    const int target = unit / segs;
+    const unsigned int owners = __ballot_sync(0xffffffffu, before <= target && target < before + mine);
+    const int lane = __ffs(owners) - 1;
+    int s = lane_begin, prefix = before, ctx = first_ctx;
+    if ((threadIdx.x & 31) == lane)
+      while (target >= prefix + units_of(ctx)) {
+        prefix += units_of(ctx);
+        ctx = ctx_of(++s);
+      }
+    Place p;
+    p.seq = __shfl_sync(0xffffffffu, s, lane);
+    p.ctx = __shfl_sync(0xffffffffu, ctx, lane);
+    prefix = __shfl_sync(0xffffffffu, prefix, lane);
+    p.units = units_of(p.ctx);
+    const int rest = unit - prefix * segs;
+    p.y = rest / p.units;
+    p.k = rest - p.y * p.units;
+    return p;
+  }
+
+  // The units before a sequence, per segment; whole warp, same s.
+  __device__ __forceinline__ int before_seq(int s) const {
+    const int range = (num_seqs + 31) / 32, lane = s / range;
+    int prefix = before, ctx = first_ctx;
+    if ((threadIdx.x & 31) == lane)
+      for (int i = lane_begin; i < s; ctx = ctx_of(++i)) prefix += units_of(ctx);
+    return __shfl_sync(0xffffffffu, prefix, lane);
+  }
+};
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_fp4_split_kernel(const Fp4SplitParams p) {
   using Span = Fp4Span<D>;
@@ -178,115 +244,67 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_fp4_split_ke
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
 
   cudaTriggerProgrammaticLaunchCompletion();  // the merge may launch and wait while this runs
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // (the same in all lanes, for the compiler too)
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2;  // mma group: rows g, g + 8 of A and the accumulator, column g of B
   const int t = lane & 3;   // thread in group
   const int cta = blockIdx.x;
   const int segs = p.Hkv * p.n_chunks;  // segments of a sequence
-  const int max_ctx = p.max_blocks_per_seq * kBlk;
-  auto ctx_of = [&](int s) { return clamp_ctx(__ldg(p.ctx_lens + s), max_ctx, p.status); };
-  auto units_of = [&](int ctx) { return (ctx + kUnit * kBlk - 1) / (kUnit * kBlk); };
 
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[warp][s], 2);
     fence_mbar_init();
   }
-  // ---- this CTA's share: the units of each sequence summed over the threads
-  const int span_seqs = (p.num_seqs + kThreads - 1) / kThreads;
-  const int s_begin = min(p.num_seqs, static_cast<int>(threadIdx.x) * span_seqs);
-  const int s_end = min(p.num_seqs, s_begin + span_seqs);
-  const int first = s_begin < s_end ? ctx_of(s_begin) : 0;
-  int mine = units_of(first);
-  for (int s = s_begin + 1; s < s_end; ++s) mine += units_of(ctx_of(s));
-  int upto = mine;  // inclusive sum over the threads
-#pragma unroll
-  for (int x = 1; x < 32; x *= 2) {
-    const int v = __shfl_up_sync(0xffffffffu, upto, x);
-    if (lane >= x) upto += v;
-  }
-  if (lane == 31) sm.scan[warp] = upto;
-  __syncthreads();
-  int per_segment = 0;  // units of all sequences, of one of their segments each
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) upto += sm.scan[w];
-    per_segment += sm.scan[w];
-  }
-  const Shares shares(per_segment * segs, gridDim.x);
+  __syncwarp();
+  // ---- this CTA's share; every warp finds it for itself
+  const Batch seqs(p.ctx_lens, p.num_seqs, p.max_blocks_per_seq * kBlk, p.status);
+  const Shares shares(seqs.per_segment * segs, gridDim.x);
   const int begin = shares.begin(cta), begin_next = shares.begin(cta + 1);
   int left = begin_next - begin;  // units of this CTA
-  if (left > 0) {
-    const int target = begin / segs;
-    int before = upto - mine;
-    if (before <= target && target < upto) {
-      int s = s_begin, ctx = first;
-      while (target >= before + units_of(ctx)) {
-        before += units_of(ctx);
-        ctx = ctx_of(++s);
-      }
-      sm.first_seq = s;
-      sm.first_ctx = ctx;
-      sm.first_prefix = before;
-    }
-  }
   // Sequences without a cached token: o = 0, lse = -inf.
   auto clear_empty = [&]() {
     for (int s = cta; s < p.num_seqs; s += gridDim.x) {
-      if (ctx_of(s) > 0) continue;
+      if (seqs.ctx_of(s) > 0) continue;
       for (int idx = threadIdx.x; idx < p.Hq * D; idx += kThreads)
         p.out[static_cast<size_t>(s) * p.Hq * D + idx] = __float2bfloat16_rn(0.f);
       if (p.lse != nullptr)
         for (int h = threadIdx.x; h < p.Hq; h += kThreads) p.lse[static_cast<size_t>(s) * p.Hq + h] = -INFINITY;
-      if (p.joints != nullptr && p.joint_per_segment)
-        for (int y = threadIdx.x; y < segs; y += kThreads) p.joints[static_cast<size_t>(s) * segs + y].more = 0;
     }
   };
-  if (p.joints != nullptr && !p.joint_per_segment && threadIdx.x == 0) p.joints[cta].more = 0;
+  if (p.joints != nullptr && threadIdx.x == 0) p.joints[cta].more = 0;
   if (left == 0) {
     clear_empty();
     return;
   }
-  __syncthreads();
-
-  Place at;  // the next unit to compute
-  at.seq = sm.first_seq;
-  at.ctx = sm.first_ctx;
-  at.units = units_of(at.ctx);
-  {
-    const int r = begin - sm.first_prefix * segs;
-    at.y = r / at.units;
-    at.k = r - at.y * at.units;
-  }
+  Place at = seqs.find(begin, segs);  // the next unit to compute
   auto next_segment = [&](Place& x) {  // the following segment that has units
     x.k = 0;
     if (++x.y < segs) return;
     x.y = 0;
     do {
-      x.ctx = ctx_of(++x.seq);
+      x.ctx = seqs.ctx_of(++x.seq);
     } while (x.ctx == 0);
     x.units = units_of(x.ctx);
   };
 
   const uint64_t stream_policy = l2_policy_evict_first();
-  Place to = at;         // the next unit to copy
   const uint32_t blk_bytes = static_cast<uint32_t>(p.Hkv) * Span::kBytes;
-  const uint8_t* to_head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;
+  Place to = at;         // the next unit to copy
   int to_copy = left;    // units not yet copied
-  int batch = 0;         // of them, those whose physical blocks phys_lane holds
-  int batch_at = 0;      // place of the next one in phys_lane
-  int phys_lane = -1;    // lane 2 i + b: block b of this warp's pair in the batch's unit i
+  int batch = 0;         // of them, those whose blocks phys_lane holds
+  int batch_at = 0;      // lanes batch_at, batch_at + 1 hold the next one's
+  int phys_lane = -1;
+  const uint8_t* to_head = nullptr;  // the cache at the batch's KV head
   int issued = 0, done = 0;
   uint32_t present = 0;  // bits of the blocks copied and not yet used, next first
   // Starts the copies of this warp's next pair into stage issued % kStages (whole
-  // warp calls; lanes 0 and 1 copy a block each).  A block past the end, or whose
-  // table entry is out of range, arrives without a copy.
+  // warp calls; lanes 0 and 1 copy a block each).  Table entries are loaded 16
+  // pairs at a time, a lane each.  A block past the end, or whose entry is out
+  // of range, arrives without a copy.
   auto issue = [&]() {
     if (batch == 0) {
-      if (to.k == to.units) {
-        next_segment(to);
-        to_head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;
-      }
+      if (to.k == to.units) next_segment(to);
+      to_head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;
       batch = min(16, min(to.units - to.k, to_copy));
       batch_at = 0;
       const int blk = (to.k + (lane >> 1)) * kUnit + 2 * warp + (lane & 1);
@@ -298,24 +316,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_fp4_split_ke
           phys_lane = -1;
         }
       }
+      to.k += batch;
     }
-    const int ph = __shfl_sync(0xffffffffu, phys_lane, 2 * batch_at + (lane & 1));
+    const int ph = __shfl_sync(0xffffffffu, phys_lane, batch_at + (lane & 1));
     present |= (__ballot_sync(0xffffffffu, ph >= 0) & 3u) << (2 * (issued - done));
     if (lane < 2) {
-      uint64_t* bar = &sm.full[warp][issued % kStages];
+      const int st = issued % kStages;
+      uint64_t* bar = &sm.full[warp][st];
       if (ph < 0) {
         mbar_arrive(bar);
       } else {
         fence_proxy_async_smem();
         mbar_arrive_expect_tx(bar, Span::kBytes);
-        bulk_load_hint(sm.ring[warp][issued % kStages] + lane * Span::kBytes, to_head + static_cast<uint64_t>(static_cast<uint32_t>(ph)) * blk_bytes,
-                       Span::kBytes, bar, stream_policy);
+        bulk_load_hint(sm.ring[warp][st] + lane * Span::kBytes,
+                       to_head + static_cast<uint64_t>(static_cast<uint32_t>(ph)) * blk_bytes, Span::kBytes, bar,
+                       stream_policy);
       }
     }
     ++issued;
-    ++batch_at;
+    batch_at += 2;
     --batch;
-    ++to.k;
     --to_copy;
   };
   for (int i = 0; i < kStages && to_copy > 0; ++i) issue();
@@ -336,37 +356,48 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_fp4_split_ke
   constexpr int kCodes8 = 8 * Span::kCodeRow, kScales8 = 8 * Span::kScaleRow;  // eight tokens on
   bool ok = true;  // no wait has run out
 
+  // Queries as B fragments: column g = query head hq0 + 8 nt + g; step ks,
+  // indices 2t, 2t + 1 and 2t + 8, 2t + 9 = columns (D/4) t + 4 ks + 0..3, the
+  // columns of the lane's own key codes.
+  uint32_t qb[NT][kKSteps][2];
+  auto load_queries = [&](const Place& x) {
+    const int rows = min(kRows, p.group - x.y % p.n_chunks * kRows);
+    const size_t row0 = static_cast<size_t>(x.seq) * p.Hq + x.y / p.n_chunks * p.group + x.y % p.n_chunks * kRows;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool real = 8 * nt + g < rows;
+      const uint2* row = reinterpret_cast<const uint2*>(p.q + (row0 + (real ? 8 * nt + g : 0)) * D + (D / 4) * t);
+#pragma unroll
+      for (int ks = 0; ks < kKSteps; ++ks) {
+        const uint2 w = real ? __ldg(row + ks) : make_uint2(0u, 0u);
+        qb[nt][ks][0] = w.x;
+        qb[nt][ks][1] = w.y;
+      }
+    }
+  };
+  load_queries(at);
+
+  const bool two_halves = p.group <= 4 * NT;  // staging rows for two segments
+  int buf = 0;
+#pragma unroll 1
   for (;;) {  // segments of this CTA's share
-    const int seq = at.seq;
     const int rows_here = min(kRows, p.group - at.y % p.n_chunks * kRows);
-    const int hq0 = at.y / p.n_chunks * p.group + at.y % p.n_chunks * kRows;
-    const int ctx = at.ctx;
+    const size_t row0 = static_cast<size_t>(at.seq) * p.Hq + at.y / p.n_chunks * p.group + at.y % p.n_chunks * kRows;
     const bool starts = at.k == 0;
     const int n_units = min(at.units - at.k, left);
     const bool ends = at.k + n_units == at.units;
 
-    // Queries as B fragments: column g = query head hq0 + 8 nt + g; step ks,
-    // indices 2t, 2t + 1 and 2t + 8, 2t + 9 = columns (D/4) t + 4 ks + 0..3, the
-    // columns of the lane's own key codes.
-    uint32_t qb[NT][kKSteps][2];
     float factor[NT][2];  // score factor of heads 2t, 2t + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const bool real = 8 * nt + g < rows_here;
-      const uint2* src = reinterpret_cast<const uint2*>(
-          p.q + (static_cast<size_t>(seq) * p.Hq + hq0 + (real ? 8 * nt + g : 0)) * D + (D / 4) * t);
       float top = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < kKSteps; ++ks) {
-        const uint2 w = real ? __ldg(src + ks) : make_uint2(0u, 0u);
-        qb[nt][ks][0] = w.x;
-        qb[nt][ks][1] = w.y;
+      for (int ks = 0; ks < kKSteps; ++ks)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint32_t v = qb[nt][ks][e];
-          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v << 16)), fabsf(__uint_as_float(v & 0xFFFF0000u))));
+          top = max3f(top, fabsf(__uint_as_float(v << 16)), fabsf(__uint_as_float(v & 0xFFFF0000u)));
         }
-      }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // the power of two of the largest element, within what its reciprocal
@@ -416,9 +447,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_fp4_split_ke
       const uint32_t stage = st * (2 * Span::kBytes);
       // Tokens of this warp's two blocks and later ones; both blocks count in
       // full but at the context's end or when one is missing.
-      const int tokens = ctx - ((at.k + i) * kUnit + 2 * warp) * kBlk;
-      const bool full = tokens >= 2 * kBlk && (present & 3u) == 3u;
+      const int tokens = at.ctx - ((at.k + i) * kUnit + 2 * warp) * kBlk;
       const uint32_t here = present & 3u;
+      const bool full = tokens >= 2 * kBlk && here == 3u;
       present >>= 2;
       ++done;
       if (here != 0) {
@@ -585,45 +616,48 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_fp4_split_ke
       if (to_copy > 0) issue();
     }
 
-    __syncthreads();  // the merge staging is free: every warp has merged the segment before
-    // ---- the warp's sums over the eight lanes that share a head
+    // ---- the warps' states merge.  The staging of the segment before may still
+    // be read, unless the two take turns with halves of it.
+    if (!two_halves) __syncthreads();
+    const int half = two_halves ? buf * 4 * NT : 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
         for (int y = 4; y < 32; y *= 2) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], y);
+        const int r = 8 * nt + 2 * t + j;
         if (g == 0) {
-          sm.wm[warp][8 * nt + 2 * t + j] = m[nt][j];
-          sm.wl[warp][8 * nt + 2 * t + j] = l[nt][j];
-          sm.wlr[warp][8 * nt + 2 * t + j] = rounded[nt][j];
+          sm.wm[buf][warp][r] = m[nt][j];
+          sm.wl[buf][warp][r] = l[nt][j];
+          sm.wlr[buf][warp][r] = rounded[nt][j];
         }
-      }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (8 * nt + 2 * t + j < rows_here)
+        if (r < rows_here)
 #pragma unroll
           for (int mt = 0; mt < kMTiles; mt += 2)
-            *reinterpret_cast<float4*>(&sm.acc[warp][8 * nt + 2 * t + j][(D / 8) * g + 2 * mt]) =
+            *reinterpret_cast<float4*>(&sm.acc[warp][half + r][(D / 8) * g + 2 * mt]) =
                 make_float4(acc[mt][nt][j], acc[mt][nt][2 + j], acc[mt + 1][nt][j], acc[mt + 1][nt][2 + j]);
+      }
+    const Place was = at;
+    left -= n_units;
+    if (left > 0) {  // the next segment's queries arrive during the merge
+      next_segment(at);
+      load_queries(at);
+    }
     __syncthreads();
-
-    // ---- merge the warps; thread -> (head, four columns) of real heads
     for (int idx = threadIdx.x; idx < rows_here * (D / 4); idx += kThreads) {
       const int r = idx / (D / 4), col = idx % (D / 4) * 4;
       float M = kNoScore;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.wm[w][r]);
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.wm[buf][w][r]);
       float L = 0.f, Lr = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float wt = ex2_approx(sm.wm[w][r] - M);
-        L += wt * sm.wl[w][r];
-        Lr += wt * sm.wlr[w][r];
-        const float4 a = *reinterpret_cast<const float4*>(&sm.acc[w][r][col]);
+        const float wt = ex2_approx(sm.wm[buf][w][r] - M);
+        L += wt * sm.wl[buf][w][r];
+        Lr += wt * sm.wlr[buf][w][r];
+        const float4 a = *reinterpret_cast<const float4*>(&sm.acc[w][half + r][col]);
         o.x += wt * a.x;
         o.y += wt * a.y;
         o.z += wt * a.z;
@@ -633,10 +667,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_fp4_split_ke
       const float scale = L == 0.f ? 0.f : p.v_scale / Lr;
       const float ls = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
       if (starts && ends) {
-        const size_t row = static_cast<size_t>(seq) * p.Hq + hq0 + r;
-        *reinterpret_cast<uint2*>(p.out + row * D + col) =
+        *reinterpret_cast<uint2*>(p.out + (row0 + r) * D + col) =
             make_uint2(pack_bf16x2(o.x * scale, o.y * scale), pack_bf16x2(o.z * scale, o.w * scale));
-        if (p.lse != nullptr && col == 0) p.lse[row] = ls;
+        if (p.lse != nullptr && col == 0) p.lse[row0 + r] = ls;
       } else {
         const size_t row = static_cast<size_t>(2 * cta + (starts ? 1 : 0)) * kRows + r;
         *reinterpret_cast<float4*>(p.ws_o + row * D + col) =
@@ -644,48 +677,74 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_fp4_split_ke
         if (col == 0) p.ws_lse[row] = ls;
       }
     }
-    if (p.joints != nullptr && starts && threadIdx.x == 0 && (p.joint_per_segment || !ends)) {
-      Fp4Joint& joint = p.joints[p.joint_per_segment ? static_cast<size_t>(seq) * segs + at.y : cta];
-      joint.cta = cta;
-      // the segment's last unit lies units - n_units past this CTA's last
-      joint.more = ends ? 0 : shares.owner(begin_next + at.units - n_units - 1) - cta;
-      joint.row = seq * p.Hq + hq0;
-      joint.rows = rows_here;
+    if (left == 0) {
+      // the only segment that can go on into further CTAs is the last
+      if (p.joints != nullptr && starts && !ends && threadIdx.x == 0)
+        p.joints[cta] = Fp4Joint{cta, shares.owner(begin_next + was.units - n_units - 1) - cta,
+                                 static_cast<int>(row0), rows_here};
+      break;
     }
-    left -= n_units;
-    if (left == 0) break;
-    next_segment(at);
+    buf ^= 1;
   }
   clear_empty();
 }
 
 struct Fp4CombineParams {
-  const Fp4Joint* joints;
+  const Fp4Joint* joints;  // one per CTA of the split kernel, or NULL: one CTA row per segment
+  const int32_t* ctx_lens;
   const float* ws_o;
   const float* ws_lse;
   __nv_bfloat16* out;
   float* lse;
+  unsigned int* status;
+  int num_seqs, Hq, segs, n_chunks, group, max_blocks_per_seq, ctas;
   int rows;  // query heads per segment, at most
 };
 
 // One CTA per (row, segment that several CTAs share): its partial outputs O_i
 // lie in the second place of the CTA where it starts and the first places of
 // the `more` that follow; L = log sum_i exp(lse_i), o = sum_i exp(lse_i - L) O_i.
-// The weights are formed once, one per thread; then D/4 threads take four
-// columns each of every kTeams-th partial output.
+// Where segments are few it finds them from ctx_lens, while the split kernel still
+// runs; else it reads what that wrote down.  The weights are formed once, one
+// per thread; D/4 threads take four columns each of every kTeams-th partial output,
+// the first ones' loads on their way before the weights are known.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) decode_fp4_combine_kernel(const Fp4CombineParams p) {
   constexpr int kTeams = kMergeThreads / (D / 4);
   constexpr int kMergeWarps = kMergeThreads / 32;
+  constexpr int kEarly = 3;
   __shared__ float weight[kFp4MaxCtas];
   __shared__ float top[kMergeWarps], sum[kMergeWarps];
   __shared__ float4 part[kTeams][D / 4];
+  __shared__ Fp4Joint found;
   const int r = blockIdx.x;
+  if (p.joints == nullptr) {
+    if (threadIdx.x < 32) {
+      const Batch seqs(p.ctx_lens, p.num_seqs, p.max_blocks_per_seq * kBlk, p.status);
+      const Shares shares(seqs.per_segment * p.segs, p.ctas);
+      const int seq = blockIdx.y / p.segs, y = blockIdx.y % p.segs;
+      const int units = units_of(seqs.ctx_of(seq));
+      const int unit = seqs.before_seq(seq) * p.segs + y * units;
+      if (threadIdx.x == 0) {
+        found.cta = units > 0 ? shares.owner(unit) : 0;
+        found.more = units > 0 ? shares.owner(unit + units - 1) - found.cta : 0;
+        found.row = seq * p.Hq + y / p.n_chunks * p.group + y % p.n_chunks * p.rows;
+        found.rows = min(p.rows, p.group - y % p.n_chunks * p.rows);
+      }
+    }
+    __syncthreads();
+  }
   cudaGridDependencySynchronize();  // launched while the split kernel runs
-  const Fp4Joint joint = p.joints[blockIdx.y];
+  const Fp4Joint joint = p.joints != nullptr ? p.joints[blockIdx.y] : found;
   if (joint.more == 0 || r >= joint.rows) return;
   const int used = joint.more + 1;
   auto place = [&](int i) { return static_cast<size_t>(2 * (joint.cta + i) + (i == 0 ? 1 : 0)) * p.rows + r; };
+  const int col = threadIdx.x % (D / 4), team = threadIdx.x / (D / 4);
+  auto part_of = [&](int s) { return reinterpret_cast<const float4*>(p.ws_o + place(s) * D)[col]; };
+  float4 early[kEarly];
+#pragma unroll
+  for (int i = 0; i < kEarly; ++i)
+    early[i] = team + i * kTeams < used ? part_of(team + i * kTeams) : make_float4(0.f, 0.f, 0.f, 0.f);
   float M = -INFINITY;
   for (int s = threadIdx.x; s < used; s += kMergeThreads) {
     const float ls = p.ws_lse[place(s)];
@@ -713,17 +772,18 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp4_combine_kernel(const
   W = 0.f;
 #pragma unroll
   for (int w = 0; w < kMergeWarps; ++w) W += sum[w];
-  const int col = threadIdx.x % (D / 4), team = threadIdx.x / (D / 4);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = team; s < used; s += kTeams) {
-    const float w = weight[s];
-    const float4 a = reinterpret_cast<const float4*>(p.ws_o + place(s) * D)[col];
+  auto add = [&](float w, const float4& a) {
     o.x = fmaf(w, a.x, o.x);
     o.y = fmaf(w, a.y, o.y);
     o.z = fmaf(w, a.z, o.z);
     o.w = fmaf(w, a.w, o.w);
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kEarly; ++i)
+    if (team + i * kTeams < used) add(weight[team + i * kTeams], early[i]);
+#pragma unroll 4
+  for (int s = team + kEarly * kTeams; s < used; s += kTeams) add(weight[s], part_of(s));
   part[team][col] = o;
   __syncthreads();
   if (threadIdx.x < D / 4) {
@@ -777,21 +837,29 @@ cudaError_t launch_d(const DecodeFp4Args& a, const DeviceGuard& g, cudaStream_t 
   sp.n_chunks = plan.chunks;
   sp.num_blocks = a.num_blocks;
   sp.max_blocks_per_seq = a.max_blocks_per_seq;
-  sp.joint_per_segment = plan.joint_per_segment;
   sp.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * a.k_scale * 1.4426950408889634);
   sp.v_scale = a.v_scale;
   cudaError_t e = plan.rows == 8 ? launch_split<D, 1>(sp, plan.ctas, stream) : launch_split<D, 2>(sp, plan.ctas, stream);
-  if (e != cudaSuccess || plan.joints == 0) return e;
+  if (e != cudaSuccess || !plan.shared) return e;
 
   Fp4CombineParams cp;
   cp.joints = sp.joints;
+  cp.ctx_lens = a.ctx_lens;
   cp.ws_o = sp.ws_o;
   cp.ws_lse = sp.ws_lse;
   cp.out = sp.out;
   cp.lse = a.lse;
+  cp.status = g.status;
+  cp.num_seqs = a.num_seqs;
+  cp.Hq = a.Hq;
+  cp.segs = a.Hkv * plan.chunks;
+  cp.n_chunks = plan.chunks;
+  cp.group = sp.group;
+  cp.max_blocks_per_seq = a.max_blocks_per_seq;
+  cp.ctas = plan.ctas;
   cp.rows = plan.rows;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sp.group < plan.rows ? sp.group : plan.rows, plan.joints);
+  cfg.gridDim = dim3(sp.group < plan.rows ? sp.group : plan.rows, plan.joints > 0 ? plan.joints : a.num_seqs * cp.segs);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -190,8 +190,8 @@ struct Fp4Plan {
   int rows;               // query heads per segment: 8 columns of an mma, or 16 for larger groups
   int chunks;             // segments per KV head
   int ctas;               // shares: one wave, but no more than there can be units
-  int joints;             // entries for segments that several CTAs share; 0 where none can be
-  int joint_per_segment;  // indexed by segment where those are fewer than the CTAs
+  int joints;             // entries of the list of shared segments; 0 where the merge finds them itself
+  bool shared;            // whether a segment can have units in several CTAs
   bool fits;              // the units' numbers fit 32 bits
   Fp4Plan(int num_seqs, int Hkv, int group, int max_blocks_per_seq) {
     rows = group <= 8 ? 8 : 16;
@@ -200,15 +200,15 @@ struct Fp4Plan {
     const long long units = segments * ((max_blocks_per_seq + kFp4UnitBlocks - 1) / kFp4UnitBlocks);
     const int wave = rows == 8 ? kFp4MaxCtas : kFp4MaxCtas / 4 * 3;  // three CTAs an SM with 16 heads
     ctas = static_cast<int>(units < wave ? units : wave);
-    joint_per_segment = segments <= ctas ? 1 : 0;
-    joints = static_cast<int>(units == segments ? 0 : joint_per_segment ? segments : ctas);
+    shared = units > segments;
+    joints = shared && segments > ctas ? ctas : 0;
     fits = units <= 0x7FFFFFFF;
   }
   size_t joint_bytes() const { return sizeof(Fp4Joint) * joints; }
   size_t part_bytes(int d) const { return sizeof(float) * 2 * ctas * rows * d; }
   // of the workspace: joints, partial outputs, their log-sum-exp
   size_t bytes(int d) const {
-    return joints == 0 ? 0 : joint_bytes() + part_bytes(d) + sizeof(float) * 2 * ctas * rows;
+    return shared ? joint_bytes() + part_bytes(d) + sizeof(float) * 2 * ctas * rows : 0;
   }
 };
 
