@@ -231,7 +231,7 @@ struct Batch {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_fp4_split_kernel(const Fp4SplitParams p) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_kernel(const Fp4SplitParams p) {
   using Span = Fp4Span<D>;
   using Smem = Fp4Smem<D, NT>;
   constexpr int kRows = 8 * NT;      // query heads per CTA

@@ -198,7 +198,7 @@ struct Fp4Plan {
     chunks = (group + rows - 1) / rows;
     const long long segments = static_cast<long long>(num_seqs) * Hkv * chunks;
     const long long units = segments * ((max_blocks_per_seq + kFp4UnitBlocks - 1) / kFp4UnitBlocks);
-    const int wave = rows == 8 ? kFp4MaxCtas : kFp4MaxCtas / 4 * 3;  // three CTAs an SM with 16 heads
+    const int wave = rows == 8 ? kFp4MaxCtas : kFp4MaxCtas / 2;  // two CTAs an SM with 16 heads
     ctas = static_cast<int>(units < wave ? units : wave);
     shared = units > segments;
     joints = shared && segments > ctas ? ctas : 0;
