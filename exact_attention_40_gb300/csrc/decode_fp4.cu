@@ -28,6 +28,9 @@
 //   scale groups.  Weights are rounded to fp16 (at most 2^-12 relative; the output is
 //   rounded to bf16, 2^-9) and the output is divided by the sum of the
 //   rounded weights, the log-sum-exp keeps the unrounded.
+//   Small calls (few segments, none long) take a cluster of 8 CTAs for each
+//   segment instead, which share out its units and merge through distributed
+//   shared memory: one launch and no workspace.
 // decode_fp4_combine_kernel: merges the partial outputs of a segment.
 #include <cuda_bf16.h>
 
@@ -230,7 +233,33 @@ struct Batch {
   }
 };
 
-template <int D, int NT>
+// Waits for every thread of the cluster; shared memory written before is seen after.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Loads from the shared memory of the cluster's CTA `rank`, at an address of one's own.
+__device__ __forceinline__ float4 cluster_load4(const void* own, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(smem_u32(own)), "r"(rank)
+      : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float cluster_load(const void* own, uint32_t rank) {
+  float v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(v)
+               : "r"(smem_u32(own)), "r"(rank)
+               : "memory");
+  return v;
+}
+
+template <int D, int NT, bool kCluster>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_kernel(const Fp4SplitParams p) {
   using Span = Fp4Span<D>;
   using Smem = Fp4Smem<D, NT>;
@@ -256,33 +285,51 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
     fence_mbar_init();
   }
   __syncwarp();
-  // ---- this CTA's share; every warp finds it for itself
-  const Batch seqs(p.ctx_lens, p.num_seqs, p.max_blocks_per_seq * kBlk, p.status);
-  const Shares shares(seqs.per_segment * segs, gridDim.x);
-  const int begin = shares.begin(cta), begin_next = shares.begin(cta + 1);
-  int left = begin_next - begin;  // units of this CTA
+  const int max_ctx = p.max_blocks_per_seq * kBlk;
+  auto ctx_of = [&](int s) { return clamp_ctx(__ldg(p.ctx_lens + s), max_ctx, p.status); };
+  Place at;          // the next unit to compute
+  int left;          // units of this CTA
+  int joint_parts = 0;  // CTAs after this one that its last segment goes on in
+  const uint32_t rank = kCluster ? cta % kFp4ClusterCtas : 0;
   // Sequences without a cached token: o = 0, lse = -inf.
   auto clear_empty = [&]() {
     for (int s = cta; s < p.num_seqs; s += gridDim.x) {
-      if (seqs.ctx_of(s) > 0) continue;
+      if (ctx_of(s) > 0) continue;
       for (int idx = threadIdx.x; idx < p.Hq * D; idx += kThreads)
         p.out[static_cast<size_t>(s) * p.Hq * D + idx] = __float2bfloat16_rn(0.f);
       if (p.lse != nullptr)
         for (int h = threadIdx.x; h < p.Hq; h += kThreads) p.lse[static_cast<size_t>(s) * p.Hq + h] = -INFINITY;
     }
   };
-  if (p.joints != nullptr && threadIdx.x == 0) p.joints[cta].more = 0;
-  if (left == 0) {
-    clear_empty();
-    return;
+  if constexpr (kCluster) {
+    const int seg = cta / kFp4ClusterCtas;
+    at.seq = seg / segs;
+    at.y = seg % segs;
+    at.ctx = ctx_of(at.seq);
+    at.units = units_of(at.ctx);
+    at.k = at.units * rank / kFp4ClusterCtas;
+    left = at.units * (rank + 1) / kFp4ClusterCtas - at.k;
+  } else {
+    // ---- this CTA's share; every warp finds it for itself
+    const Batch seqs(p.ctx_lens, p.num_seqs, max_ctx, p.status);
+    const Shares shares(seqs.per_segment * segs, gridDim.x);
+    const int begin = shares.begin(cta), begin_next = shares.begin(cta + 1);
+    left = begin_next - begin;
+    if (p.joints != nullptr && threadIdx.x == 0) p.joints[cta].more = 0;
+    if (left == 0) {
+      clear_empty();
+      return;
+    }
+    at = seqs.find(begin, segs);
+    const Place last = seqs.find(begin_next - 1, segs);
+    joint_parts = shares.owner(begin_next - 1 + last.units - 1 - last.k) - cta;
   }
-  Place at = seqs.find(begin, segs);  // the next unit to compute
   auto next_segment = [&](Place& x) {  // the following segment that has units
     x.k = 0;
     if (++x.y < segs) return;
     x.y = 0;
     do {
-      x.ctx = seqs.ctx_of(++x.seq);
+      x.ctx = ctx_of(++x.seq);
     } while (x.ctx == 0);
     x.units = units_of(x.ctx);
   };
@@ -375,12 +422,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
       }
     }
   };
-  load_queries(at);
+  if (!kCluster || left > 0) load_queries(at);
+
+  // In a cluster: this CTA's outcome, in the ring, which every copy has left by then.
+  float* const cluster_o = reinterpret_cast<float*>(&sm.ring[0][0][0]);
+  float* const cluster_lse = cluster_o + kRows * D;
+  if constexpr (kCluster)
+    if (left == 0)
+      for (int idx = threadIdx.x; idx < kRows * D; idx += kThreads) {
+        cluster_o[idx] = 0.f;
+        if (idx < kRows) cluster_lse[idx] = -INFINITY;
+      }
 
   const bool two_halves = p.group <= 4 * NT;  // staging rows for two segments
   int buf = 0;
 #pragma unroll 1
-  for (;;) {  // segments of this CTA's share
+  while (left > 0) {  // segments of this CTA's share
     const int rows_here = min(kRows, p.group - at.y % p.n_chunks * kRows);
     const size_t row0 = static_cast<size_t>(at.seq) * p.Hq + at.y / p.n_chunks * p.group + at.y % p.n_chunks * kRows;
     const bool starts = at.k == 0;
@@ -638,7 +695,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
             *reinterpret_cast<float4*>(&sm.acc[warp][half + r][(D / 8) * g + 2 * mt]) =
                 make_float4(acc[mt][nt][j], acc[mt][nt][2 + j], acc[mt + 1][nt][j], acc[mt + 1][nt][2 + j]);
       }
-    const Place was = at;
     left -= n_units;
     if (left > 0) {  // the next segment's queries arrive during the merge
       next_segment(at);
@@ -666,7 +722,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
       // a share all of whose scores are -inf, or whose blocks are all missing, sees nothing
       const float scale = L == 0.f ? 0.f : p.v_scale / Lr;
       const float ls = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
-      if (starts && ends) {
+      if constexpr (kCluster) {
+        *reinterpret_cast<float4*>(cluster_o + r * D + col) =
+            make_float4(o.x * scale, o.y * scale, o.z * scale, o.w * scale);
+        if (col == 0) cluster_lse[r] = ls;
+      } else if (starts && ends) {
         *reinterpret_cast<uint2*>(p.out + (row0 + r) * D + col) =
             make_uint2(pack_bf16x2(o.x * scale, o.y * scale), pack_bf16x2(o.z * scale, o.w * scale));
         if (p.lse != nullptr && col == 0) p.lse[row0 + r] = ls;
@@ -679,14 +739,50 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
     }
     if (left == 0) {
       // the only segment that can go on into further CTAs is the last
-      if (p.joints != nullptr && starts && !ends && threadIdx.x == 0)
-        p.joints[cta] = Fp4Joint{cta, shares.owner(begin_next + was.units - n_units - 1) - cta,
-                                 static_cast<int>(row0), rows_here};
+      if (!kCluster && p.joints != nullptr && starts && !ends && threadIdx.x == 0)
+        p.joints[cta] = Fp4Joint{cta, joint_parts, static_cast<int>(row0), rows_here};
       break;
     }
     buf ^= 1;
   }
-  clear_empty();
+  if constexpr (kCluster) {
+    // ---- the cluster's CTAs merge: L = log sum_i exp(lse_i), o = sum_i exp(lse_i - L) O_i
+    const int rows_here = min(kRows, p.group - at.y % p.n_chunks * kRows);
+    const size_t row0 = static_cast<size_t>(at.seq) * p.Hq + at.y / p.n_chunks * p.group + at.y % p.n_chunks * kRows;
+    cluster_barrier();
+    for (int idx = threadIdx.x * kFp4ClusterCtas + rank; idx < rows_here * (D / 4); idx += kThreads * kFp4ClusterCtas) {
+      const int r = idx / (D / 4), col = idx % (D / 4) * 4;
+      float ls[kFp4ClusterCtas];
+      float4 part[kFp4ClusterCtas];
+#pragma unroll
+      for (int i = 0; i < kFp4ClusterCtas; ++i) {
+        ls[i] = cluster_load(cluster_lse + r, i);
+        part[i] = cluster_load4(cluster_o + r * D + col, i);
+      }
+      float M = ls[0];
+#pragma unroll
+      for (int i = 1; i < kFp4ClusterCtas; ++i) M = max_nan(M, ls[i]);
+      const float ref = M == -INFINITY ? 0.f : M;
+      float W = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kFp4ClusterCtas; ++i) {
+        const float w = ex2_approx((ls[i] - ref) * kLog2e);
+        W += w;
+        o.x = fmaf(w, part[i].x, o.x);
+        o.y = fmaf(w, part[i].y, o.y);
+        o.z = fmaf(w, part[i].z, o.z);
+        o.w = fmaf(w, part[i].w, o.w);
+      }
+      const float inv = W == 0.f ? 0.f : 1.f / W;
+      *reinterpret_cast<uint2*>(p.out + (row0 + r) * D + col) =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+      if (p.lse != nullptr && col == 0) p.lse[row0 + r] = W == 0.f ? -INFINITY : M + __logf(W);
+    }
+    cluster_barrier();  // nobody's shared memory goes away before the others have read it
+  } else {
+    clear_empty();
+  }
 }
 
 struct Fp4CombineParams {
@@ -803,15 +899,30 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp4_combine_kernel(const
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kCluster>
 cudaError_t launch_split(const Fp4SplitParams& sp, int ctas, cudaStream_t stream) {
   const size_t smem = sizeof(Fp4Smem<D, NT>) + 128;
   static std::atomic<int> smem_set[64] = {};
-  cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(decode_fp4_split_kernel<D, NT>),
+  cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(decode_fp4_split_kernel<D, NT, kCluster>),
                                   static_cast<int>(smem), smem_set);
   if (e != cudaSuccess) return e;
-  decode_fp4_split_kernel<D, NT><<<ctas, kThreads, smem, stream>>>(sp);
-  return cudaGetLastError();
+  if (!kCluster) {
+    decode_fp4_split_kernel<D, NT, kCluster><<<ctas, kThreads, smem, stream>>>(sp);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kFp4ClusterCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_fp4_split_kernel<D, NT, kCluster>, sp);
 }
 
 template <int D>
@@ -839,7 +950,11 @@ cudaError_t launch_d(const DecodeFp4Args& a, const DeviceGuard& g, cudaStream_t 
   sp.max_blocks_per_seq = a.max_blocks_per_seq;
   sp.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * a.k_scale * 1.4426950408889634);
   sp.v_scale = a.v_scale;
-  cudaError_t e = plan.rows == 8 ? launch_split<D, 1>(sp, plan.ctas, stream) : launch_split<D, 2>(sp, plan.ctas, stream);
+  if (plan.cluster)
+    return plan.rows == 8 ? launch_split<D, 1, true>(sp, plan.ctas, stream)
+                          : launch_split<D, 2, true>(sp, plan.ctas, stream);
+  const cudaError_t e = plan.rows == 8 ? launch_split<D, 1, false>(sp, plan.ctas, stream)
+                                       : launch_split<D, 2, false>(sp, plan.ctas, stream);
   if (e != cudaSuccess || !plan.shared) return e;
 
   Fp4CombineParams cp;

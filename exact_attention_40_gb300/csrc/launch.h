@@ -175,6 +175,8 @@ cudaError_t launch_cache_read_fp4(const ReadFp4Args& a, cudaStream_t stream);
 
 constexpr int kFp4UnitBlocks = 8;       // blocks in a unit of the 4-bit decode's work
 constexpr int kFp4MaxCtas = 152 * 4;    // its grid: one wave, four CTAs for each SM
+constexpr int kFp4ClusterCtas = 8;      // CTAs of a segment in a small call (the portable cluster size)
+constexpr int kFp4ClusterUnits = 32;    // units of the longest segment of a small call
 
 // A segment (the query heads of one sequence that share a KV head, in chunks
 // of `rows`) that starts in CTA `cta` and goes on through `more` further CTAs.
@@ -191,7 +193,8 @@ struct Fp4Plan {
   int chunks;             // segments per KV head
   int ctas;               // shares: one wave, but no more than there can be units
   int joints;             // entries of the list of shared segments; 0 where the merge finds them itself
-  bool shared;            // whether a segment can have units in several CTAs
+  bool cluster;           // a cluster of CTAs for each segment
+  bool shared;            // whether a segment's partial outputs can lie in several CTAs' workspace
   bool fits;              // the units' numbers fit 32 bits
   Fp4Plan(int num_seqs, int Hkv, int group, int max_blocks_per_seq) {
     rows = group <= 8 ? 8 : 16;
@@ -200,7 +203,10 @@ struct Fp4Plan {
     const long long units = segments * ((max_blocks_per_seq + kFp4UnitBlocks - 1) / kFp4UnitBlocks);
     const int wave = rows == 8 ? kFp4MaxCtas : kFp4MaxCtas / 2;  // two CTAs an SM with 16 heads
     ctas = static_cast<int>(units < wave ? units : wave);
-    shared = units > segments;
+    const bool split = units > segments;
+    cluster = split && segments * kFp4ClusterCtas <= wave && units <= segments * kFp4ClusterUnits;
+    if (cluster) ctas = static_cast<int>(segments * kFp4ClusterCtas);
+    shared = split && !cluster;
     joints = shared && segments > ctas ? ctas : 0;
     fits = units <= 0x7FFFFFFF;
   }

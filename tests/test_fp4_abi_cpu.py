@@ -132,7 +132,7 @@ def test_read_rejections(lib):
 
 
 def dec(lib, ws_bytes=None, **kw):
-    a = dict(q=FAKE, c=FAKE, bt=FAKE, cl=FAKE, out=FAKE, lse=None, S=2, Hq=8, Hkv=2, d=128, nb=10, mb=64, scale=0.1,
+    a = dict(q=FAKE, c=FAKE, bt=FAKE, cl=FAKE, out=FAKE, lse=None, S=2, Hq=8, Hkv=2, d=128, nb=10, mb=512, scale=0.1,
              ks=1.0, vs=1.0, ws=FAKE)
     a.update(kw)
     if ws_bytes is None:
@@ -158,6 +158,8 @@ def test_decode_rejections(lib):
     assert dec(lib, ws_bytes=16) == 4
     assert dec(lib, ws=FAKE + 4) == 3
     assert dec(lib, S=70000) == 2
+    assert dec(lib, S=65535, Hq=65535, Hkv=65535) == 2               # more rows than 2^31
+    assert dec(lib, S=65535, Hq=8, Hkv=8, mb=1 << 26, ws_bytes=1 << 30) == 2  # more work units than 2^31
     assert dec(lib, S=0, q=None) == 0
 
 
@@ -169,7 +171,11 @@ def test_sizes(lib):
     assert lib.attn_decode_fp4_workspace_bytes(0, 8, 2, 64, 4) == 0
     assert lib.attn_decode_fp4_workspace_bytes(1, 8, 3, 64, 4) == 0
     assert lib.attn_decode_fp4_workspace_bytes(1, 8, 2, 96, 4) == 0
-    assert lib.attn_decode_fp4_workspace_bytes(1, 1, 1, 64, 1) == 0  # one split: written directly
+    assert lib.attn_decode_fp4_workspace_bytes(1, 1, 1, 64, 1) == 0     # one CTA a head: written directly
+    assert lib.attn_decode_fp4_workspace_bytes(2, 8, 2, 128, 100) == 0  # few and short: merged in a cluster
+    big = lib.attn_decode_fp4_workspace_bytes(64, 32, 8, 128, 512)
+    assert 0 < big < 16 << 20  # two partial outputs for each of a wave of CTAs, however long the contexts
+    assert lib.attn_decode_fp4_workspace_bytes(64, 32, 8, 128, 1 << 16) == big
 
 
 def test_the_reference_of_the_format():

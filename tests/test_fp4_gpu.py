@@ -88,6 +88,25 @@ def test_decode_head_layouts(env, d, Hq, Hkv):
     run_decode(env, decode_case(401, [200, 1, 47], Hq, Hkv, d, k_scale=0.5, v_scale=0.01), d, k_scale=0.5, v_scale=0.01)
 
 
+@pytest.mark.parametrize("S,Hq,Hkv,hi", [(40, 4, 2, 5000), (160, 8, 4, 600), (700, 2, 1, 40), (130, 24, 2, 300)])
+def test_decode_many_sequences(env, S, Hq, Hkv, hi):
+    """Ragged batches, empty sequences among them: shares that end inside sequences,
+    shares of many sequences, more segments than CTAs, and no segment of two units."""
+    lens = np.floor(synth.uniform01(70 + S, S) ** 2 * (hi + 1)).astype(np.int32)
+    lens[[0, S // 2, S - 1]] = 0
+    lens[1] = hi
+    run_decode(env, decode_case(420, lens, Hq, Hkv, 64), 64)
+
+
+@pytest.mark.parametrize("blocks", [8, 9, 64, 255, 256, 257, 264])
+@pytest.mark.parametrize("Hq,Hkv", [(3, 1), (20, 2)])
+def test_decode_around_the_limits_of_a_small_call(env, blocks, Hq, Hkv):
+    """Lengths at which a sequence gets a second unit, fills the cluster's shares and
+    passes from the cluster to shares of the whole batch."""
+    n = blocks * 16
+    run_decode(env, decode_case(421, [n, n - 15, 1, 0, max(1, n - 128)], Hq, Hkv, 128), 128)
+
+
 def test_decode_serving_batch(env):
     lens = synth.ctx_lengths(5, 24, 512, 8192)
     run_decode(env, decode_case(402, lens, 8, 2, 128, k_scale=0.003, v_scale=0.002), 128, k_scale=0.003, v_scale=0.002)
@@ -210,7 +229,7 @@ def test_decode_cache_past_32_bits(env):
 
 def test_decode_outputs_given_no_lse_and_workspace(env):
     torch, ex, dev = env
-    q, cache, table, lens = decode_case(412, [2000, 100], 8, 1, 128)
+    q, cache, table, lens = decode_case(412, [6000, 100], 8, 1, 128)
     args = [to_dev(x, dev) for x in (q, cache, table, lens)]
     want, want_lse = ex.attn_decode_paged_fp4(*args)
     need = ex.attn_decode_fp4_workspace_bytes(2, 8, 1, 128, table.shape[1])
@@ -238,7 +257,7 @@ def test_decode_outputs_given_no_lse_and_workspace(env):
 def test_decode_captured_replayed_and_sharing_a_workspace(env):
     """Two graphs over one workspace, replayed in turn with changed contents."""
     torch, ex, dev = env
-    q, cache, table, lens = decode_case(413, [2500, 700, 1], 8, 2, 128)
+    q, cache, table, lens = decode_case(413, [5000, 700, 1], 8, 2, 128)
     qd, cd, td, ld = (to_dev(x, dev) for x in (q, cache, table, lens))
     ws = torch.empty(ex.attn_decode_fp4_workspace_bytes(3, 8, 2, 128, table.shape[1]), device=dev, dtype=torch.uint8)
     q2 = qd.flip(0).contiguous()
