@@ -29,7 +29,7 @@
 //   rounded to bf16, 2^-9) and the output is divided by the sum of the
 //   rounded weights, the log-sum-exp keeps the unrounded.
 //   Small calls (few segments, none long) take a cluster of 8 CTAs for each
-//   segment instead, which share out its units and merge through distributed
+//   segment instead, which take its units in turn and merge through distributed
 //   shared memory: one launch and no workspace.
 // decode_fp4_combine_kernel: merges the partial outputs of a segment.
 #include <cuda_bf16.h>
@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
   constexpr int kMTiles = D / 16;    // mma row tiles of O^T
   constexpr int kKeyWords = D / 32;  // 32-bit words of a lane's key codes per token
   constexpr int kValWords = D / 64;  // ... value codes
+  constexpr int kStep = kCluster ? kFp4ClusterCtas : 1;  // from a CTA's unit to its next
 
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
@@ -287,8 +288,27 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
   __syncwarp();
   const int max_ctx = p.max_blocks_per_seq * kBlk;
   auto ctx_of = [&](int s) { return clamp_ctx(__ldg(p.ctx_lens + s), max_ctx, p.status); };
-  Place at;          // the next unit to compute
-  int left;          // units of this CTA
+  // Queries as B fragments: column g = query head hq0 + 8 nt + g; step ks,
+  // indices 2t, 2t + 1 and 2t + 8, 2t + 9 = columns (D/4) t + 4 ks + 0..3, the
+  // columns of the lane's own key codes.
+  uint32_t qb[NT][kKSteps][2];
+  auto load_queries = [&](const Place& x) {
+    const int rows = min(kRows, p.group - x.y % p.n_chunks * kRows);
+    const size_t row0 = static_cast<size_t>(x.seq) * p.Hq + x.y / p.n_chunks * p.group + x.y % p.n_chunks * kRows;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool real = 8 * nt + g < rows;
+      const uint2* row = reinterpret_cast<const uint2*>(p.q + (row0 + (real ? 8 * nt + g : 0)) * D + (D / 4) * t);
+#pragma unroll
+      for (int ks = 0; ks < kKSteps; ++ks) {
+        const uint2 w = real ? __ldg(row + ks) : make_uint2(0u, 0u);
+        qb[nt][ks][0] = w.x;
+        qb[nt][ks][1] = w.y;
+      }
+    }
+  };
+  Place at;             // the next unit to compute
+  int left;             // units of this CTA
   int joint_parts = 0;  // CTAs after this one that its last segment goes on in
   const uint32_t rank = kCluster ? cta % kFp4ClusterCtas : 0;
   // Sequences without a cached token: o = 0, lse = -inf.
@@ -301,14 +321,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
         for (int h = threadIdx.x; h < p.Hq; h += kThreads) p.lse[static_cast<size_t>(s) * p.Hq + h] = -INFINITY;
     }
   };
+  int phys_lane = -1;  // physical block of this warp's block `lane` of a batch of 16 pairs; -1: none, or a bad entry
+  auto check = [&](int ph) {
+    if (ph >= 0 && ph < p.num_blocks) return ph;
+    atomicOr(p.status, 2u);  // EXATTN_DEVICE_BOUNDS_BIT
+    return -1;
+  };
   if constexpr (kCluster) {
+    // Every 8th unit, so that the table entries and queries need not wait for the
+    // context length: the three loads are in flight together.
     const int seg = cta / kFp4ClusterCtas;
     at.seq = seg / segs;
     at.y = seg % segs;
+    at.k = rank;
+    const int blk = (rank + kStep * (lane >> 1)) * kUnit + 2 * warp + (lane & 1);
+    const int entry = blk < p.max_blocks_per_seq && (lane >> 1) < kFp4ClusterUnits / kFp4ClusterCtas
+                          ? __ldg(p.block_table + static_cast<size_t>(at.seq) * p.max_blocks_per_seq + blk)
+                          : -1;
+    load_queries(at);
     at.ctx = ctx_of(at.seq);
     at.units = units_of(at.ctx);
-    at.k = at.units * rank / kFp4ClusterCtas;
-    left = at.units * (rank + 1) / kFp4ClusterCtas - at.k;
+    left = (at.units - static_cast<int>(rank) + kStep - 1) / kStep;
+    if (left > 0 && blk * kBlk < at.ctx) phys_lane = check(entry);
   } else {
     // ---- this CTA's share; every warp finds it for itself
     const Batch seqs(p.ctx_lens, p.num_seqs, max_ctx, p.status);
@@ -321,8 +355,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
       return;
     }
     at = seqs.find(begin, segs);
-    const Place last = seqs.find(begin_next - 1, segs);
-    joint_parts = shares.owner(begin_next - 1 + last.units - 1 - last.k) - cta;
+    load_queries(at);
+    if (p.joints != nullptr) {
+      const Place last = seqs.find(begin_next - 1, segs);
+      joint_parts = shares.owner(begin_next - 1 + last.units - 1 - last.k) - cta;
+    }
   }
   auto next_segment = [&](Place& x) {  // the following segment that has units
     x.k = 0;
@@ -338,10 +375,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
   const uint32_t blk_bytes = static_cast<uint32_t>(p.Hkv) * Span::kBytes;
   Place to = at;         // the next unit to copy
   int to_copy = left;    // units not yet copied
-  int batch = 0;         // of them, those whose blocks phys_lane holds
-  int batch_at = 0;      // lanes batch_at, batch_at + 1 hold the next one's
-  int phys_lane = -1;
-  const uint8_t* to_head = nullptr;  // the cache at the batch's KV head
+  int batch = kCluster ? left : 0;  // of them, those whose blocks phys_lane holds
+  int batch_at = 0;                 // lanes batch_at, batch_at + 1 hold the next one's
+  const uint8_t* to_head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;  // at the batch's KV head
   int issued = 0, done = 0;
   uint32_t present = 0;  // bits of the blocks copied and not yet used, next first
   // Starts the copies of this warp's next pair into stage issued % kStages (whole
@@ -349,20 +385,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
   // pairs at a time, a lane each.  A block past the end, or whose entry is out
   // of range, arrives without a copy.
   auto issue = [&]() {
-    if (batch == 0) {
+    if (!kCluster && batch == 0) {
       if (to.k == to.units) next_segment(to);
       to_head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;
       batch = min(16, min(to.units - to.k, to_copy));
       batch_at = 0;
       const int blk = (to.k + (lane >> 1)) * kUnit + 2 * warp + (lane & 1);
       phys_lane = -1;
-      if ((lane >> 1) < batch && blk * kBlk < to.ctx) {
-        phys_lane = __ldg(p.block_table + static_cast<size_t>(to.seq) * p.max_blocks_per_seq + blk);
-        if (phys_lane < 0 || phys_lane >= p.num_blocks) {
-          atomicOr(p.status, 2u);
-          phys_lane = -1;
-        }
-      }
+      if ((lane >> 1) < batch && blk * kBlk < to.ctx)
+        phys_lane = check(__ldg(p.block_table + static_cast<size_t>(to.seq) * p.max_blocks_per_seq + blk));
       to.k += batch;
     }
     const int ph = __shfl_sync(0xffffffffu, phys_lane, batch_at + (lane & 1));
@@ -403,27 +434,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
   constexpr int kCodes8 = 8 * Span::kCodeRow, kScales8 = 8 * Span::kScaleRow;  // eight tokens on
   bool ok = true;  // no wait has run out
 
-  // Queries as B fragments: column g = query head hq0 + 8 nt + g; step ks,
-  // indices 2t, 2t + 1 and 2t + 8, 2t + 9 = columns (D/4) t + 4 ks + 0..3, the
-  // columns of the lane's own key codes.
-  uint32_t qb[NT][kKSteps][2];
-  auto load_queries = [&](const Place& x) {
-    const int rows = min(kRows, p.group - x.y % p.n_chunks * kRows);
-    const size_t row0 = static_cast<size_t>(x.seq) * p.Hq + x.y / p.n_chunks * p.group + x.y % p.n_chunks * kRows;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const bool real = 8 * nt + g < rows;
-      const uint2* row = reinterpret_cast<const uint2*>(p.q + (row0 + (real ? 8 * nt + g : 0)) * D + (D / 4) * t);
-#pragma unroll
-      for (int ks = 0; ks < kKSteps; ++ks) {
-        const uint2 w = real ? __ldg(row + ks) : make_uint2(0u, 0u);
-        qb[nt][ks][0] = w.x;
-        qb[nt][ks][1] = w.y;
-      }
-    }
-  };
-  if (!kCluster || left > 0) load_queries(at);
-
   // In a cluster: this CTA's outcome, in the ring, which every copy has left by then.
   float* const cluster_o = reinterpret_cast<float*>(&sm.ring[0][0][0]);
   float* const cluster_lse = cluster_o + kRows * D;
@@ -441,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
     const int rows_here = min(kRows, p.group - at.y % p.n_chunks * kRows);
     const size_t row0 = static_cast<size_t>(at.seq) * p.Hq + at.y / p.n_chunks * p.group + at.y % p.n_chunks * kRows;
     const bool starts = at.k == 0;
-    const int n_units = min(at.units - at.k, left);
+    const int n_units = kCluster ? left : min(at.units - at.k, left);
     const bool ends = at.k + n_units == at.units;
 
     float factor[NT][2];  // score factor of heads 2t, 2t + 1
@@ -504,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
       const uint32_t stage = st * (2 * Span::kBytes);
       // Tokens of this warp's two blocks and later ones; both blocks count in
       // full but at the context's end or when one is missing.
-      const int tokens = at.ctx - ((at.k + i) * kUnit + 2 * warp) * kBlk;
+      const int tokens = at.ctx - ((at.k + i * kStep) * kUnit + 2 * warp) * kBlk;
       const uint32_t here = present & 3u;
       const bool full = tokens >= 2 * kBlk && here == 3u;
       present >>= 2;
