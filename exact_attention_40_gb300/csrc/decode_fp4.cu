@@ -234,8 +234,11 @@ struct Batch {
 };
 
 // Waits for every thread of the cluster; shared memory written before is seen after.
+// Not the .aligned form: that needs the warp's lanes together, and after a loop
+// that some of them left early nothing says they are.
 __device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Loads from the shared memory of the cluster's CTA `rank`, at an address of one's own.
@@ -577,6 +580,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
                 if (tok_s >= n_valid[b]) c[b][nt][j] = -INFINITY;
                 if (tok_s + 8 >= n_valid[b]) c[b][nt][2 + j] = -INFINITY;
               }
+          __syncwarp();  // the lanes together again for the next mma
         }
         // Exponents relative to the reference m.  It follows the running maximum
         // only when a score passes it by more than 8 (weights up to 2^8 fit fp16
@@ -649,6 +653,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
             if (tok_v1 >= n_valid[b]) ea1 = 0;
             if (tok_v0 + 8 >= n_valid[b]) eb0 = 0;
             if (tok_v1 + 8 >= n_valid[b]) eb1 = 0;
+            __syncwarp();  // the lanes together again for the next mma
           }
           const uint32_t ta = e4m3x2_to_f16(__byte_perm(ea0, ea1, 0x0040));
           const uint32_t tb = e4m3x2_to_f16(__byte_perm(eb0, eb1, 0x0040));
