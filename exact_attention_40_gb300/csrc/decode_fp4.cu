@@ -3,15 +3,15 @@
 //
 // decode_fp4_split_kernel: the work is units of 8 blocks (128 tokens) of one
 //   (sequence, kv head, chunk of up to 8 NT query heads), its segment, numbered
-//   through all segments in order.  Each CTA takes an equal, contiguous share of them,
-//   so that the longest sequence of a ragged batch holds nobody up and one
+//   through all segments in order.  Each CTA takes an equal, contiguous share of
+//   them, so that the longest sequence of a ragged batch holds nobody up and one
 //   wave of CTAs is enough; it finds its share from ctx_lens itself, so a
-//   captured graph follows their contents.  Of a unit each of the four warps
-//   takes two blocks, streamed as spans (18 d bytes: codes and scales of keys
-//   and values) through a private shared-memory ring, one bulk copy a block;
-//   the copies run ahead across segments.  At a segment's end the warps' states
-//   merge; a segment that lies in one CTA is written to the output, any other
-//   leaves partial outputs, at most two a CTA.
+//   captured graph follows their contents.  One warp copies: units in order into
+//   a ring in shared memory, one bulk copy for each block's span (18 d bytes:
+//   codes and scales of keys and values), across segments.  Four warps compute,
+//   two blocks of a unit each.  At a segment's end their states merge; a segment
+//   that lies in one CTA is written to the output, any other leaves partial
+//   outputs, at most two a CTA.
 //   Everything is computed transposed, so that the 16 tokens of a block are
 //   the rows of mma.sync m16n8k16 and the few query heads of the group its 8
 //   columns (as rows, half or more of them would be padding):
@@ -20,9 +20,9 @@
 //   Codes become fp16 by the cvt of packed e2m1 and are multiplied by their
 //   scale there; the product has 6 significant bits, so keys and values enter
 //   the tensor core exactly.  Queries are bf16: each is multiplied by a power of
-//   two that brings its largest element to [1, 2), after which fp16 holds
-//   every element that is not 2^-24 of the largest or less exactly, and the
-//   power goes into the score's factor.  Both products sum over their inner index
+//   two that brings its largest element to [1, 2), after which fp16 holds its
+//   elements exactly down to 2^-17 and within 2^-25 below, and the power goes
+//   into the score's factor.  Both products sum over their inner index
 //   in any order, so which column or token an mma index stands for is free: it
 //   is chosen so that a lane reads its codes as one vector each, from one or two
 //   scale groups.  Weights are rounded to fp16 (at most 2^-12 relative; the output is
@@ -44,9 +44,10 @@ namespace exattn {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kThreads = kWarps * 32;       // that compute; one warp more copies
+constexpr int kCtaThreads = kThreads + 32;
 constexpr int kMergeThreads = 256;
-constexpr int kStages = 2;  // pairs of blocks in flight per warp
+constexpr int kStages = 3;  // units in flight
 constexpr int kBlk = kDecodeBlockSize;
 constexpr int kUnit = kFp4UnitBlocks;
 static_assert(kUnit == 2 * kWarps, "a pair of blocks per warp");
@@ -139,13 +140,21 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
 template <int D, int NT>
 struct Fp4Smem {
   static constexpr int kAccStride = D + 4;  // row of the merge staging, floats
-  alignas(128) uint8_t ring[kWarps][kStages][2 * Fp4Span<D>::kBytes];
+  alignas(128) uint8_t ring[kStages][kUnit][Fp4Span<D>::kBytes];
   float acc[kWarps][8 * NT][kAccStride];
-  uint64_t full[kWarps][kStages];
+  uint64_t full[kStages];        // a unit's copies have landed
+  uint64_t empty[kStages];       // the four warps have used it
+  int present[kStages];          // bits of its blocks that were copied
   float wm[2][kWarps][8 * NT];   // per-warp running max (log2 units)
   float wl[2][kWarps][8 * NT];   // per-warp sum of the weights
   float wlr[2][kWarps][8 * NT];  // ... of the rounded weights
 };
+
+// Waits for the computing warps of the CTA.
+__device__ __forceinline__ void compute_barrier() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
 
 // Equal contiguous shares of `total` units for `parts` CTAs, the first
 // total % parts of them one larger.  (The host keeps totals below 2^31.)
@@ -263,7 +272,7 @@ __device__ __forceinline__ float cluster_load(const void* own, uint32_t rank) {
 }
 
 template <int D, int NT, bool kCluster>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_kernel(const Fp4SplitParams p) {
+__global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_fp4_split_kernel(const Fp4SplitParams p) {
   using Span = Fp4Span<D>;
   using Smem = Fp4Smem<D, NT>;
   constexpr int kRows = 8 * NT;      // query heads per CTA
@@ -284,11 +293,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
   const int cta = blockIdx.x;
   const int segs = p.Hkv * p.n_chunks;  // segments of a sequence
 
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[warp][s], 2);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.full[s], kUnit);
+      mbar_init(&sm.empty[s], kWarps);
+    }
     fence_mbar_init();
   }
-  __syncwarp();
   const int max_ctx = p.max_blocks_per_seq * kBlk;
   auto ctx_of = [&](int s) { return clamp_ctx(__ldg(p.ctx_lens + s), max_ctx, p.status); };
   // Queries as B fragments: column g = query head hq0 + 8 nt + g; step ks,
@@ -318,13 +329,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
   auto clear_empty = [&]() {
     for (int s = cta; s < p.num_seqs; s += gridDim.x) {
       if (ctx_of(s) > 0) continue;
-      for (int idx = threadIdx.x; idx < p.Hq * D; idx += kThreads)
+      for (int idx = threadIdx.x; idx < p.Hq * D; idx += kCtaThreads)
         p.out[static_cast<size_t>(s) * p.Hq * D + idx] = __float2bfloat16_rn(0.f);
       if (p.lse != nullptr)
-        for (int h = threadIdx.x; h < p.Hq; h += kThreads) p.lse[static_cast<size_t>(s) * p.Hq + h] = -INFINITY;
+        for (int h = threadIdx.x; h < p.Hq; h += kCtaThreads) p.lse[static_cast<size_t>(s) * p.Hq + h] = -INFINITY;
     }
   };
-  int phys_lane = -1;  // physical block of this warp's block `lane` of a batch of 16 pairs; -1: none, or a bad entry
+  const bool copies = warp == kWarps;
+  int phys_lane = -1;  // of the copying warp: physical block of block lane % 8 of a batch's unit lane / 8; -1: none
   auto check = [&](int ph) {
     if (ph >= 0 && ph < p.num_blocks) return ph;
     atomicOr(p.status, 2u);  // EXATTN_DEVICE_BOUNDS_BIT
@@ -333,19 +345,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
   if constexpr (kCluster) {
     // Every 8th unit, so that the table entries and queries need not wait for the
     // context length: the three loads are in flight together.
+    static_assert(kFp4ClusterUnits / kFp4ClusterCtas <= 32 / kUnit, "one batch of table entries");
     const int seg = cta / kFp4ClusterCtas;
     at.seq = seg / segs;
     at.y = seg % segs;
     at.k = rank;
-    const int blk = (rank + kStep * (lane >> 1)) * kUnit + 2 * warp + (lane & 1);
-    const int entry = blk < p.max_blocks_per_seq && (lane >> 1) < kFp4ClusterUnits / kFp4ClusterCtas
+    const int blk = (rank + kStep * (lane / kUnit)) * kUnit + lane % kUnit;
+    const int entry = copies && blk < p.max_blocks_per_seq
                           ? __ldg(p.block_table + static_cast<size_t>(at.seq) * p.max_blocks_per_seq + blk)
                           : -1;
-    load_queries(at);
+    if (!copies) load_queries(at);
     at.ctx = ctx_of(at.seq);
     at.units = units_of(at.ctx);
     left = (at.units - static_cast<int>(rank) + kStep - 1) / kStep;
-    if (left > 0 && blk * kBlk < at.ctx) phys_lane = check(entry);
+    if (copies && blk * kBlk < at.ctx) phys_lane = check(entry);
   } else {
     // ---- this CTA's share; every warp finds it for itself
     const Batch seqs(p.ctx_lens, p.num_seqs, max_ctx, p.status);
@@ -358,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
       return;
     }
     at = seqs.find(begin, segs);
-    load_queries(at);
+    if (!copies) load_queries(at);
     if (p.joints != nullptr) {
       const Place last = seqs.find(begin_next - 1, segs);
       joint_parts = shares.owner(begin_next - 1 + last.units - 1 - last.k) - cta;
@@ -374,52 +387,63 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
     x.units = units_of(x.ctx);
   };
 
-  const uint64_t stream_policy = l2_policy_evict_first();
-  const uint32_t blk_bytes = static_cast<uint32_t>(p.Hkv) * Span::kBytes;
-  Place to = at;         // the next unit to copy
-  int to_copy = left;    // units not yet copied
-  int batch = kCluster ? left : 0;  // of them, those whose blocks phys_lane holds
-  int batch_at = 0;                 // lanes batch_at, batch_at + 1 hold the next one's
-  const uint8_t* to_head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;  // at the batch's KV head
-  int issued = 0, done = 0;
-  uint32_t present = 0;  // bits of the blocks copied and not yet used, next first
-  // Starts the copies of this warp's next pair into stage issued % kStages (whole
-  // warp calls; lanes 0 and 1 copy a block each).  Table entries are loaded 16
-  // pairs at a time, a lane each.  A block past the end, or whose entry is out
-  // of range, arrives without a copy.
-  auto issue = [&]() {
-    if (!kCluster && batch == 0) {
-      if (to.k == to.units) next_segment(to);
-      to_head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;
-      batch = min(16, min(to.units - to.k, to_copy));
-      batch_at = 0;
-      const int blk = (to.k + (lane >> 1)) * kUnit + 2 * warp + (lane & 1);
-      phys_lane = -1;
-      if ((lane >> 1) < batch && blk * kBlk < to.ctx)
-        phys_lane = check(__ldg(p.block_table + static_cast<size_t>(to.seq) * p.max_blocks_per_seq + blk));
-      to.k += batch;
-    }
-    const int ph = __shfl_sync(0xffffffffu, phys_lane, batch_at + (lane & 1));
-    present |= (__ballot_sync(0xffffffffu, ph >= 0) & 3u) << (2 * (issued - done));
-    if (lane < 2) {
-      const int st = issued % kStages;
-      uint64_t* bar = &sm.full[warp][st];
-      if (ph < 0) {
-        mbar_arrive(bar);
-      } else {
-        fence_proxy_async_smem();
-        mbar_arrive_expect_tx(bar, Span::kBytes);
-        bulk_load_hint(sm.ring[warp][st] + lane * Span::kBytes,
-                       to_head + static_cast<uint64_t>(static_cast<uint32_t>(ph)) * blk_bytes, Span::kBytes, bar,
-                       stream_policy);
+  __syncthreads();  // the barriers are set up
+
+  if (copies) {
+    // ---- the copying warp: units in order, as stages come free.  Table entries are
+    // loaded for up to four units of a segment at a time, a lane each; the lane
+    // copies its block.  A block past the end, or whose entry is out of range,
+    // arrives without a copy.
+    const uint64_t stream_policy = l2_policy_evict_first();
+    const uint32_t blk_bytes = static_cast<uint32_t>(p.Hkv) * Span::kBytes;
+    Place to = at;
+    int batch = kCluster ? left : 0, batch_at = 0;  // units whose entries are loaded, and the next of them
+    const uint8_t* head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;  // the cache at their KV head
+    int i = 0;
+#pragma unroll 1
+    for (; i < left; ++i) {
+      if (!kCluster && batch_at == batch) {
+        if (to.k == to.units) next_segment(to);
+        head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;
+        batch = min(32 / kUnit, min(to.units - to.k, left - i));
+        batch_at = 0;
+        const int blk = to.k * kUnit + lane;
+        phys_lane = -1;
+        if (lane < batch * kUnit && blk * kBlk < to.ctx)
+          phys_lane = check(__ldg(p.block_table + static_cast<size_t>(to.seq) * p.max_blocks_per_seq + blk));
+        to.k += batch;
       }
+      const int st = i % kStages;
+      const bool waited = i < kStages || mbar_wait(&sm.empty[st], (i / kStages - 1) & 1, p.wait_ns);
+      if (!__all_sync(0xffffffffu, waited)) {
+        if (lane == 0) atomicOr(p.status, 1u);  // EXATTN_DEVICE_TIMEOUT_BIT
+        break;
+      }
+      const uint32_t present = (__ballot_sync(0xffffffffu, phys_lane >= 0) >> (batch_at * kUnit)) & ((1u << kUnit) - 1);
+      if (lane / kUnit == batch_at) {
+        const int b = lane % kUnit;
+        if (b == 0) sm.present[st] = present;
+        if (phys_lane < 0) {
+          mbar_arrive(&sm.full[st]);
+        } else {
+          mbar_arrive_expect_tx(&sm.full[st], Span::kBytes);
+          bulk_load_hint(sm.ring[st][b], head + static_cast<uint64_t>(static_cast<uint32_t>(phys_lane)) * blk_bytes,
+                         Span::kBytes, &sm.full[st], stream_policy);
+        }
+      }
+      ++batch_at;
     }
-    ++issued;
-    batch_at += 2;
-    --batch;
-    --to_copy;
-  };
-  for (int i = 0; i < kStages && to_copy > 0; ++i) issue();
+    for (int j = max(0, i - kStages); j < i; ++j)  // no copy is left in flight
+      mbar_wait(&sm.full[j % kStages], (j / kStages) & 1, p.wait_ns);
+    __syncwarp();
+    if constexpr (kCluster) {
+      cluster_barrier();
+      cluster_barrier();
+    } else {
+      clear_empty();
+    }
+    return;
+  }
 
   // mma token index r stands for token r ^ ((r >> 1) & 1): neighbouring pairs
   // swapped for odd t, so that the value loads of the four lanes of a group
@@ -427,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
   const int tok_s = g ^ ((g >> 1) & 1);    // this lane's score rows: tok_s, tok_s + 8
   const int tok_v0 = 2 * t + (t & 1);      // mma index 2t (and 2t + 8: + 8)
   const int tok_v1 = 2 * t + 1 - (t & 1);  // mma index 2t + 1 (and 2t + 9: + 8)
-  const uint32_t ring0 = smem_u32(sm.ring[warp][0]);
+  const uint32_t ring0 = smem_u32(sm.ring[0][2 * warp]);
   const uint32_t key_at = ring0 + Span::kKeyCodes + tok_s * Span::kCodeRow + t * (D / 8);
   const uint32_t key_scale_at = ring0 + Span::kKeyScales + tok_s * Span::kScaleRow + t * (D / 64);
   const uint32_t val_at0 = ring0 + Span::kValueCodes + tok_v0 * Span::kCodeRow + g * (D / 16);
@@ -436,6 +460,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
   const uint32_t val_scale_at1 = ring0 + Span::kValueScales + tok_v1 * Span::kScaleRow + g * D / 128;
   constexpr int kCodes8 = 8 * Span::kCodeRow, kScales8 = 8 * Span::kScaleRow;  // eight tokens on
   bool ok = true;  // no wait has run out
+  int done = 0;    // units used
 
   // In a cluster: this CTA's outcome, in the ring, which every copy has left by then.
   float* const cluster_o = reinterpret_cast<float*>(&sm.ring[0][0][0]);
@@ -502,25 +527,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
 #pragma unroll 1
     for (int i = 0; i < n_units; ++i) {
       const int st = done % kStages;
-      if (ok) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[warp][st], (done / kStages) & 1, p.wait_ns));
-        if (!ok) {
-          if (lane == 0) {
-            atomicOr(p.status, 1u);  // EXATTN_DEVICE_TIMEOUT_BIT
-            for (int j = done + 1; j < issued; ++j)  // let copies in flight land
-              mbar_wait(&sm.full[warp][j % kStages], (j / kStages) & 1, p.wait_ns);
-          }
-          __syncwarp();
-        }
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(&sm.full[st], (done / kStages) & 1, p.wait_ns))) {
+        ok = false;  // nothing more is computed, the CTA's barriers are still met
+        if (lane == 0) atomicOr(p.status, 1u);  // EXATTN_DEVICE_TIMEOUT_BIT
       }
-      if (!ok) continue;  // nothing more is copied or computed, the CTA's barriers are still met
-      const uint32_t stage = st * (2 * Span::kBytes);
+      if (!ok) continue;
+      const uint32_t stage = st * (kUnit * Span::kBytes);
       // Tokens of this warp's two blocks and later ones; both blocks count in
       // full but at the context's end or when one is missing.
       const int tokens = at.ctx - ((at.k + i * kStep) * kUnit + 2 * warp) * kBlk;
-      const uint32_t here = present & 3u;
+      const uint32_t here = (sm.present[st] >> (2 * warp)) & 3u;
       const bool full = tokens >= 2 * kBlk && here == 3u;
-      present >>= 2;
       ++done;
       if (here != 0) {
         int n_valid[2];  // tokens of each block that count, where not all do
@@ -684,13 +701,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
         products(std::integral_constant<int, 0>());
         products(std::integral_constant<int, 1>());
       }
-      __syncwarp();  // all lanes done with this stage before it is refilled
-      if (to_copy > 0) issue();
+      __syncwarp();  // all lanes are done with this stage
+      if (lane == 0) mbar_arrive(&sm.empty[st]);
     }
 
     // ---- the warps' states merge.  The staging of the segment before may still
     // be read, unless the two take turns with halves of it.
-    if (!two_halves) __syncthreads();
+    if (!two_halves) compute_barrier();
     const int half = two_halves ? buf * 4 * NT : 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -715,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
       next_segment(at);
       load_queries(at);
     }
-    __syncthreads();
+    compute_barrier();
     for (int idx = threadIdx.x; idx < rows_here * (D / 4); idx += kThreads) {
       const int r = idx / (D / 4), col = idx % (D / 4) * 4;
       float M = kNoScore;
@@ -760,6 +777,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_fp4_split_ke
     }
     buf ^= 1;
   }
+  __syncwarp();
   if constexpr (kCluster) {
     // ---- the cluster's CTAs merge: L = log sum_i exp(lse_i), o = sum_i exp(lse_i - L) O_i
     const int rows_here = min(kRows, p.group - at.y % p.n_chunks * kRows);
@@ -922,12 +940,12 @@ cudaError_t launch_split(const Fp4SplitParams& sp, int ctas, cudaStream_t stream
                                   static_cast<int>(smem), smem_set);
   if (e != cudaSuccess) return e;
   if (!kCluster) {
-    decode_fp4_split_kernel<D, NT, kCluster><<<ctas, kThreads, smem, stream>>>(sp);
+    decode_fp4_split_kernel<D, NT, kCluster><<<ctas, kCtaThreads, smem, stream>>>(sp);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kCtaThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

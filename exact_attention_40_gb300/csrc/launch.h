@@ -174,7 +174,16 @@ struct ReadFp4Args {
 cudaError_t launch_cache_read_fp4(const ReadFp4Args& a, cudaStream_t stream);
 
 constexpr int kFp4UnitBlocks = 8;       // blocks in a unit of the 4-bit decode's work
-constexpr int kFp4MaxCtas = 152 * 4;    // its grid: one wave, four CTAs for each SM
+constexpr int kFp4Sms = 152;
+constexpr int kFp4MaxCtas = kFp4Sms * 3;  // no grid of the batch's shares is larger
+
+// CTAs of the 4-bit decode that share an SM, for segments of `rows` query heads.
+// Three of four computing warps, though registers and shared memory would hold
+// four at d = 64: a batch of 64 x 8192 tokens takes 72.8 us with three, 77.8 with
+// four and 81 with two (d = 128: 110, 118 and 115).  Two for 16 heads, whose
+// accumulators fill the registers.
+constexpr __host__ __device__ int fp4_decode_ctas(int rows) { return rows > 8 ? 2 : 3; }
+
 constexpr int kFp4ClusterCtas = 8;      // CTAs of a segment in a small call (the portable cluster size)
 constexpr int kFp4ClusterUnits = 32;    // units of the longest segment of a small call
 
@@ -201,7 +210,7 @@ struct Fp4Plan {
     chunks = (group + rows - 1) / rows;
     const long long segments = static_cast<long long>(num_seqs) * Hkv * chunks;
     const long long units = segments * ((max_blocks_per_seq + kFp4UnitBlocks - 1) / kFp4UnitBlocks);
-    const int wave = rows == 8 ? kFp4MaxCtas : kFp4MaxCtas / 2;  // two CTAs an SM with 16 heads
+    const int wave = kFp4Sms * fp4_decode_ctas(rows);
     ctas = static_cast<int>(units < wave ? units : wave);
     const bool split = units > segments;
     cluster = split && segments * kFp4ClusterCtas <= wave && units <= segments * kFp4ClusterUnits;
