@@ -54,6 +54,7 @@ static_assert(kUnit == 2 * kWarps, "a pair of blocks per warp");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint32_t kOnes = 0x3C003C00u;  // fp16 (1, 1)
+constexpr int kWhole = static_cast<int>(0x80000000u);
 constexpr float kNoScore = -3.0e38f;     // below any score; -inf would give inf - inf
 
 struct Fp4SplitParams {
@@ -144,7 +145,7 @@ struct Fp4Smem {
   float acc[kWarps][8 * NT][kAccStride];
   uint64_t full[kStages];        // a unit's copies have landed
   uint64_t empty[kStages];       // the four warps have used it
-  int present[kStages];          // bits of its blocks that were copied
+  int present[kStages];          // bits of its blocks that were copied, kWhole where all are and are full
   float wm[2][kWarps][8 * NT];   // per-warp running max (log2 units)
   float wl[2][kWarps][8 * NT];   // per-warp sum of the weights
   float wlr[2][kWarps][8 * NT];  // ... of the rounded weights
@@ -400,6 +401,9 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
     int batch = kCluster ? left : 0, batch_at = 0;  // units whose entries are loaded, and the next of them
     const uint8_t* head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;  // the cache at their KV head
     int i = 0;
+    int st = 0;
+    uint32_t parity = 1;  // of the stage's last use; the first round waits for none
+    int to_ctx = to.ctx - (to.k + 1) * kUnit * kBlk;  // the context's tokens past the unit
 #pragma unroll 1
     for (; i < left; ++i) {
       if (!kCluster && batch_at == batch) {
@@ -407,14 +411,14 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
         head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;
         batch = min(32 / kUnit, min(to.units - to.k, left - i));
         batch_at = 0;
+        to_ctx = to.ctx - (to.k + 1) * kUnit * kBlk;
         const int blk = to.k * kUnit + lane;
         phys_lane = -1;
         if (lane < batch * kUnit && blk * kBlk < to.ctx)
           phys_lane = check(__ldg(p.block_table + static_cast<size_t>(to.seq) * p.max_blocks_per_seq + blk));
         to.k += batch;
       }
-      const int st = i % kStages;
-      const bool waited = i < kStages || mbar_wait(&sm.empty[st], (i / kStages - 1) & 1, p.wait_ns);
+      const bool waited = i < kStages || mbar_wait(&sm.empty[st], parity, p.wait_ns);
       if (!__all_sync(0xffffffffu, waited)) {
         if (lane == 0) atomicOr(p.status, 1u);  // EXATTN_DEVICE_TIMEOUT_BIT
         break;
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
       const uint32_t present = (__ballot_sync(0xffffffffu, phys_lane >= 0) >> (batch_at * kUnit)) & ((1u << kUnit) - 1);
       if (lane / kUnit == batch_at) {
         const int b = lane % kUnit;
-        if (b == 0) sm.present[st] = present;
+        if (b == 0) sm.present[st] = to_ctx >= 0 && present == (1u << kUnit) - 1 ? kWhole : static_cast<int>(present);
         if (phys_lane < 0) {
           mbar_arrive(&sm.full[st]);
         } else {
@@ -432,6 +436,11 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
         }
       }
       ++batch_at;
+      to_ctx -= kStep * kUnit * kBlk;
+      if (++st == kStages) {
+        st = 0;
+        parity ^= 1u;
+      }
     }
     for (int j = max(0, i - kStages); j < i; ++j)  // no copy is left in flight
       mbar_wait(&sm.full[j % kStages], (j / kStages) & 1, p.wait_ns);
@@ -460,7 +469,8 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
   const uint32_t val_scale_at1 = ring0 + Span::kValueScales + tok_v1 * Span::kScaleRow + g * D / 128;
   constexpr int kCodes8 = 8 * Span::kCodeRow, kScales8 = 8 * Span::kScaleRow;  // eight tokens on
   bool ok = true;  // no wait has run out
-  int done = 0;    // units used
+  int st = 0;      // stage of the next unit
+  uint32_t parity = 0;
 
   // In a cluster: this CTA's outcome, in the ring, which every copy has left by then.
   float* const cluster_o = reinterpret_cast<float*>(&sm.ring[0][0][0]);
@@ -526,24 +536,22 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
 
 #pragma unroll 1
     for (int i = 0; i < n_units; ++i) {
-      const int st = done % kStages;
-      if (ok && !__all_sync(0xffffffffu, mbar_wait(&sm.full[st], (done / kStages) & 1, p.wait_ns))) {
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(&sm.full[st], parity, p.wait_ns))) {
         ok = false;  // nothing more is computed, the CTA's barriers are still met
         if (lane == 0) atomicOr(p.status, 1u);  // EXATTN_DEVICE_TIMEOUT_BIT
       }
       if (!ok) continue;
       const uint32_t stage = st * (kUnit * Span::kBytes);
-      // Tokens of this warp's two blocks and later ones; both blocks count in
-      // full but at the context's end or when one is missing.
-      const int tokens = at.ctx - ((at.k + i * kStep) * kUnit + 2 * warp) * kBlk;
-      const uint32_t here = (sm.present[st] >> (2 * warp)) & 3u;
-      const bool full = tokens >= 2 * kBlk && here == 3u;
-      ++done;
-      if (here != 0) {
-        int n_valid[2];  // tokens of each block that count, where not all do
-        n_valid[0] = here & 1u ? tokens : 0;
-        n_valid[1] = here & 2u ? tokens - kBlk : 0;
-
+      const int present = sm.present[st];
+      // Whether all of this warp's two blocks' tokens count; else, how many of each.
+      const bool full = present == kWhole;
+      int n_valid[2] = {kBlk, kBlk};
+      if (!full) {
+        const int tokens = at.ctx - ((at.k + i * kStep) * kUnit + 2 * warp) * kBlk;
+        n_valid[0] = present >> (2 * warp) & 1 ? tokens : 0;
+        n_valid[1] = present >> (2 * warp) & 2 ? tokens - kBlk : 0;
+      }
+      if (full || max(n_valid[0], n_valid[1]) > 0) {
         // ---- S^T = K Q^T
         float c[2][NT][4];
         auto scores = [&](auto block) {
@@ -703,6 +711,10 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
       }
       __syncwarp();  // all lanes are done with this stage
       if (lane == 0) mbar_arrive(&sm.empty[st]);
+      if (++st == kStages) {
+        st = 0;
+        parity ^= 1u;
+      }
     }
 
     // ---- the warps' states merge.  The staging of the segment before may still
