@@ -25,9 +25,10 @@
 //   into the score's factor.  Both products sum over their inner index
 //   in any order, so which column or token an mma index stands for is free: it
 //   is chosen so that a lane reads its codes as one vector each, from one or two
-//   scale groups.  Weights are rounded to fp16 (at most 2^-12 relative; the output is
-//   rounded to bf16, 2^-9) and the output is divided by the sum of the
-//   rounded weights, the log-sum-exp keeps the unrounded.
+//   scale groups.  Weights are rounded to fp16 for the second product, at most
+//   2^-12 relative (the output is rounded to bf16, 2^-9); their sums are fp32 and
+//   take them unrounded (a second sum, of the rounded weights, cost 1 to 2% of the
+//   time and changed no digit that bf16 keeps).
 //   Small calls (few segments, none long) take a cluster of 8 CTAs for each
 //   segment instead, which take its units in turn and merge through distributed
 //   shared memory: one launch and no workspace.
@@ -53,7 +54,6 @@ constexpr int kUnit = kFp4UnitBlocks;
 static_assert(kUnit == 2 * kWarps, "a pair of blocks per warp");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr uint32_t kOnes = 0x3C003C00u;  // fp16 (1, 1)
 constexpr int kWhole = static_cast<int>(0x80000000u);
 constexpr float kNoScore = -3.0e38f;     // below any score; -inf would give inf - inf
 
@@ -148,7 +148,6 @@ struct Fp4Smem {
   int present[kStages];          // bits of its blocks that were copied, kWhole where all are and are full
   float wm[2][kWarps][8 * NT];   // per-warp running max (log2 units)
   float wl[2][kWarps][8 * NT];   // per-warp sum of the weights
-  float wlr[2][kWarps][8 * NT];  // ... of the rounded weights
 };
 
 // Waits for the computing warps of the CTA.
@@ -524,12 +523,10 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
 
     float m[NT][2], l[NT][2];     // heads 2t, 2t + 1; l: this lane's tokens only
     float acc[kMTiles][NT][4];
-    float rounded[NT][4];         // sums of the rounded weights: the product with a row of ones
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = kNoScore;
       l[nt][0] = l[nt][1] = 0.f;
-      rounded[nt][0] = rounded[nt][1] = rounded[nt][2] = rounded[nt][3] = 0.f;
 #pragma unroll
       for (int mt = 0; mt < kMTiles; ++mt) acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.f;
     }
@@ -636,7 +633,6 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
               const float alpha = ex2_approx(m[nt][j] - mn);
               m[nt][j] = mn;
               l[nt][j] *= alpha;
-              rounded[nt][j] *= alpha;
 #pragma unroll
               for (int mt = 0; mt < kMTiles; ++mt) {
                 acc[mt][nt][j] *= alpha;
@@ -671,7 +667,6 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
             l[nt][1] += w[1] + w[3];
             pb[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
             pb[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
-            mma_f16_16816(rounded[nt], kOnes, kOnes, kOnes, kOnes, pb[nt][0], pb[nt][1]);
           }
           if (!full) {
             if (tok_v0 >= n_valid[b]) ea0 = 0;
@@ -731,7 +726,6 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
         if (g == 0) {
           sm.wm[buf][warp][r] = m[nt][j];
           sm.wl[buf][warp][r] = l[nt][j];
-          sm.wlr[buf][warp][r] = rounded[nt][j];
         }
         if (r < rows_here)
 #pragma unroll
@@ -750,13 +744,12 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
       float M = kNoScore;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.wm[buf][w][r]);
-      float L = 0.f, Lr = 0.f;
+      float L = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float wt = ex2_approx(sm.wm[buf][w][r] - M);
         L += wt * sm.wl[buf][w][r];
-        Lr += wt * sm.wlr[buf][w][r];
         const float4 a = *reinterpret_cast<const float4*>(&sm.acc[w][half + r][col]);
         o.x += wt * a.x;
         o.y += wt * a.y;
@@ -764,7 +757,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
         o.w += wt * a.w;
       }
       // a share all of whose scores are -inf, or whose blocks are all missing, sees nothing
-      const float scale = L == 0.f ? 0.f : p.v_scale / Lr;
+      const float scale = L == 0.f ? 0.f : p.v_scale / L;
       const float ls = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
       if constexpr (kCluster) {
         *reinterpret_cast<float4*>(cluster_o + r * D + col) =
