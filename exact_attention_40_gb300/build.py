@@ -90,7 +90,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         # torch's own libraries are in the process before this one is imported
         tmp = BINDING + ".tmp%d" % os.getpid()
         cmd = ["g++", "-shared", "-o", tmp, binding_obj, "-L" + HERE, "-l:libexattn.so", "-Wl,-rpath,$ORIGIN",
-               "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+               "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))

@@ -9,7 +9,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -101,10 +101,16 @@ struct Sections {
   }
 };
 
+// A new contiguous tensor, straight from the CUDA allocator (through the
+// operators' dispatcher it takes half a microsecond more).
+Tensor fresh(c10::Device device, at::IntArrayRef shape, at::ScalarType type) {
+  return at::detail::empty_cuda(shape, type, device, std::nullopt);
+}
+
 // The output `o`, or a new contiguous tensor where it is None.
 Tensor output(PyObject* o, const char* name, c10::Device device, at::IntArrayRef shape, at::ScalarType type,
               bool contiguous) {
-  if (o == Py_None) return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+  if (o == Py_None) return fresh(device, shape, type);
   const Tensor& t = tensor(o, name, static_cast<int64_t>(shape.size()), type);
   check(t, name, device, shape, contiguous);
   return t;
@@ -292,8 +298,7 @@ PyObject* decode_paged_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   size_t bytes = 0;
   if (a[9] == Py_None) {
     bytes = attn_decode_fp4_workspace_bytes(iS, iHq, c.Hkv, c.d, mb);
-    if (bytes > 0)
-      workspace = at::empty({static_cast<int64_t>(bytes)}, at::TensorOptions().dtype(at::kByte).device(c.device));
+    if (bytes > 0) workspace = fresh(c.device, {static_cast<int64_t>(bytes)}, at::kByte);
   } else {
     if (!THPVariable_Check(a[9])) fail(PyExc_TypeError, "workspace must be a torch.Tensor");
     workspace = THPVariable_Unpack(a[9]);
