@@ -179,26 +179,25 @@ __device__ __forceinline__ int units_of(int ctx) { return (ctx + kUnit * kBlk - 
 // contiguous range of them.
 struct Batch {
   const int32_t* ctx_lens;
-  unsigned int* status;
   int max_ctx, num_seqs;
   int lane_begin, before, mine;  // this lane's first sequence, the units before it, in its range
   int first_ctx;                 // of its first sequence
   int per_segment;               // units of all sequences (of one segment of each)
 
-  __device__ __forceinline__ int ctx_of(int s) const { return clamp_ctx(__ldg(ctx_lens + s), max_ctx, status); }
+  // Clamped without a word: whoever handles the sequence reports it.
+  __device__ __forceinline__ int ctx_of(int s) const { return max(0, min(max_ctx, __ldg(ctx_lens + s))); }
 
-  __device__ __forceinline__ Batch(const int32_t* lens, int seqs, int longest, unsigned int* word) {
+  __device__ __forceinline__ Batch(const int32_t* lens, int seqs, int longest) {
     ctx_lens = lens;
     num_seqs = seqs;
     max_ctx = longest;
-    status = word;
     const int lane = threadIdx.x & 31;
     const int range = (seqs + 31) / 32;
     lane_begin = min(seqs, lane * range);
     const int end = min(seqs, lane_begin + range);
     first_ctx = lane_begin < end ? ctx_of(lane_begin) : 0;
     mine = units_of(first_ctx);
-#pragma unroll 4
+#pragma unroll 8
     for (int s = lane_begin + 1; s < end; ++s) mine += units_of(ctx_of(s));
     int upto = mine;  // inclusive sum over the lanes
 #pragma unroll
@@ -325,14 +324,21 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
   int left;             // units of this CTA
   int joint_parts = 0;  // CTAs after this one that its last segment goes on in
   const uint32_t rank = kCluster ? cta % kFp4ClusterCtas : 0;
-  // Sequences without a cached token: o = 0, lse = -inf.
+  // Sequences without a cached token: o = 0, lse = -inf.  A lane looks at one, the
+  // warp clears what is found.  (Every sequence's length passes here once, so that
+  // one out of range is reported.)
   auto clear_empty = [&]() {
-    for (int s = cta; s < p.num_seqs; s += gridDim.x) {
-      if (ctx_of(s) > 0) continue;
-      for (int idx = threadIdx.x; idx < p.Hq * D; idx += kCtaThreads)
-        p.out[static_cast<size_t>(s) * p.Hq * D + idx] = __float2bfloat16_rn(0.f);
-      if (p.lse != nullptr)
-        for (int h = threadIdx.x; h < p.Hq; h += kCtaThreads) p.lse[static_cast<size_t>(s) * p.Hq + h] = -INFINITY;
+    for (int i = 32 * warp; cta + static_cast<int>(gridDim.x) * i < p.num_seqs; i += kCtaThreads) {
+      const int s = cta + gridDim.x * (i + lane);
+      for (uint32_t empty = __ballot_sync(0xffffffffu, s < p.num_seqs && ctx_of(s) == 0); empty != 0;
+           empty &= empty - 1) {
+        const size_t row0 = static_cast<size_t>(cta + gridDim.x * (i + __ffs(empty) - 1)) * p.Hq;
+        for (int idx = lane; idx < p.Hq * (D / 8); idx += 32)
+          reinterpret_cast<uint4*>(p.out + row0 * D)[idx] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.lse != nullptr)
+          for (int h = lane; h < p.Hq; h += 32) p.lse[row0 + h] = -INFINITY;
+        __syncwarp();
+      }
     }
   };
   const bool copies = warp == kWarps;
@@ -361,7 +367,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
     if (copies && blk * kBlk < at.ctx) phys_lane = check(entry);
   } else {
     // ---- this CTA's share; every warp finds it for itself
-    const Batch seqs(p.ctx_lens, p.num_seqs, max_ctx, p.status);
+    const Batch seqs(p.ctx_lens, p.num_seqs, max_ctx);
     const Shares shares(seqs.per_segment * segs, gridDim.x);
     const int begin = shares.begin(cta), begin_next = shares.begin(cta + 1);
     left = begin_next - begin;
@@ -390,32 +396,56 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
   __syncthreads();  // the barriers are set up
 
   if (copies) {
-    // ---- the copying warp: units in order, as stages come free.  Table entries are
-    // loaded for up to four units of a segment at a time, a lane each; the lane
-    // copies its block.  A block past the end, or whose entry is out of range,
-    // arrives without a copy.
+    // ---- the copying warp: units in order, as stages come free; the lane that holds a
+    // block's table entry copies it.  A block past the end, or whose entry is out of
+    // range, arrives without a copy.
     const uint64_t stream_policy = l2_policy_evict_first();
     const uint32_t blk_bytes = static_cast<uint32_t>(p.Hkv) * Span::kBytes;
     Place to = at;
-    int batch = kCluster ? left : 0, batch_at = 0;  // units whose entries are loaded, and the next of them
-    const uint8_t* head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;  // the cache at their KV head
+    int to_load = left;  // units whose table entries are not yet asked for
+    // A batch: up to four units of one segment; lane 8 i + b has unit i's block b.
+    struct Entries {
+      int units, raw;  // raw: this lane's table entry, if it has one (`mine`)
+      bool mine;
+      int past;  // tokens of the context past the batch's first unit
+      const uint8_t* head;
+    };
+    auto load_batch = [&]() {
+      Entries e;
+      if (to.k == to.units) {
+        next_segment(to);
+        // its queries into the L1 cache, for the computing warps
+        const int rows = min(kRows, p.group - to.y % p.n_chunks * kRows);
+        const size_t row = static_cast<size_t>(to.seq) * p.Hq + to.y / p.n_chunks * p.group + to.y % p.n_chunks * kRows;
+        if (lane < rows * D / 64) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.q + row * D + lane * 64));
+      }
+      e.units = min(32 / kUnit, min(to.units - to.k, to_load));
+      const int blk = to.k * kUnit + lane;
+      e.mine = lane < e.units * kUnit && blk * kBlk < to.ctx;
+      e.raw = e.mine ? __ldg(p.block_table + static_cast<size_t>(to.seq) * p.max_blocks_per_seq + blk) : -1;
+      e.past = to.ctx - (to.k + 1) * kUnit * kBlk;
+      e.head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;
+      to.k += e.units;
+      to_load -= e.units;
+      return e;
+    };
+    Entries now, next;  // the entries of the next batch are on their way while this one's blocks are copied
+    if constexpr (kCluster)
+      now = Entries{left, phys_lane, phys_lane >= 0, at.ctx - (at.k + 1) * kUnit * kBlk,
+                    p.cache + static_cast<size_t>(at.y / p.n_chunks) * Span::kBytes};
+    else
+      next = load_batch();
+    int batch_at = kCluster ? 0 : 4;
+    if (!kCluster) now.units = 4;
     int i = 0;
     int st = 0;
     uint32_t parity = 1;  // of the stage's last use; the first round waits for none
-    int to_ctx = to.ctx - (to.k + 1) * kUnit * kBlk;  // the context's tokens past the unit
 #pragma unroll 1
     for (; i < left; ++i) {
-      if (!kCluster && batch_at == batch) {
-        if (to.k == to.units) next_segment(to);
-        head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;
-        batch = min(32 / kUnit, min(to.units - to.k, left - i));
+      if (!kCluster && batch_at == now.units) {
+        now = next;
         batch_at = 0;
-        to_ctx = to.ctx - (to.k + 1) * kUnit * kBlk;
-        const int blk = to.k * kUnit + lane;
-        phys_lane = -1;
-        if (lane < batch * kUnit && blk * kBlk < to.ctx)
-          phys_lane = check(__ldg(p.block_table + static_cast<size_t>(to.seq) * p.max_blocks_per_seq + blk));
-        to.k += batch;
+        phys_lane = now.mine ? check(now.raw) : -1;
       }
       const bool waited = i < kStages || mbar_wait(&sm.empty[st], parity, p.wait_ns);
       if (!__all_sync(0xffffffffu, waited)) {
@@ -425,17 +455,18 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
       const uint32_t present = (__ballot_sync(0xffffffffu, phys_lane >= 0) >> (batch_at * kUnit)) & ((1u << kUnit) - 1);
       if (lane / kUnit == batch_at) {
         const int b = lane % kUnit;
-        if (b == 0) sm.present[st] = to_ctx >= 0 && present == (1u << kUnit) - 1 ? kWhole : static_cast<int>(present);
+        if (b == 0) sm.present[st] = now.past >= 0 && present == (1u << kUnit) - 1 ? kWhole : static_cast<int>(present);
         if (phys_lane < 0) {
           mbar_arrive(&sm.full[st]);
         } else {
           mbar_arrive_expect_tx(&sm.full[st], Span::kBytes);
-          bulk_load_hint(sm.ring[st][b], head + static_cast<uint64_t>(static_cast<uint32_t>(phys_lane)) * blk_bytes,
+          bulk_load_hint(sm.ring[st][b], now.head + static_cast<uint64_t>(static_cast<uint32_t>(phys_lane)) * blk_bytes,
                          Span::kBytes, &sm.full[st], stream_policy);
         }
       }
+      if (!kCluster && batch_at == 0 && to_load > 0) next = load_batch();
       ++batch_at;
-      to_ctx -= kStep * kUnit * kBlk;
+      now.past -= kStep * kUnit * kBlk;
       if (++st == kStages) {
         st = 0;
         parity ^= 1u;
@@ -757,7 +788,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
         o.w += wt * a.w;
       }
       // a share all of whose scores are -inf, or whose blocks are all missing, sees nothing
-      const float scale = L == 0.f ? 0.f : p.v_scale / L;
+      const float scale = L == 0.f ? 0.f : __fdividef(p.v_scale, L);
       const float ls = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
       if constexpr (kCluster) {
         *reinterpret_cast<float4*>(cluster_o + r * D + col) =
@@ -830,7 +861,6 @@ struct Fp4CombineParams {
   const float* ws_lse;
   __nv_bfloat16* out;
   float* lse;
-  unsigned int* status;
   int num_seqs, Hq, segs, n_chunks, group, max_blocks_per_seq, ctas;
   int rows;  // query heads per segment, at most
 };
@@ -854,7 +884,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp4_combine_kernel(const
   const int r = blockIdx.x;
   if (p.joints == nullptr) {
     if (threadIdx.x < 32) {
-      const Batch seqs(p.ctx_lens, p.num_seqs, p.max_blocks_per_seq * kBlk, p.status);
+      const Batch seqs(p.ctx_lens, p.num_seqs, p.max_blocks_per_seq * kBlk);
       const Shares shares(seqs.per_segment * p.segs, p.ctas);
       const int seq = blockIdx.y / p.segs, y = blockIdx.y % p.segs;
       const int units = units_of(seqs.ctx_of(seq));
@@ -1002,7 +1032,6 @@ cudaError_t launch_d(const DecodeFp4Args& a, const DeviceGuard& g, cudaStream_t 
   cp.ws_lse = sp.ws_lse;
   cp.out = sp.out;
   cp.lse = a.lse;
-  cp.status = g.status;
   cp.num_seqs = a.num_seqs;
   cp.Hq = a.Hq;
   cp.segs = a.Hkv * plan.chunks;
