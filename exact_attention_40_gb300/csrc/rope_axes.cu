@@ -49,44 +49,34 @@ __device__ __forceinline__ void tile_angles(float2* cs, const RopeAxesTable& tab
   }
 }
 
-// A thread's 8 cosines and sines as packed pairs.
+// A thread's 8 cosines and sines.
 struct Turn8 {
-  uint64_t c[4], s[4];
+  float c[8], s[8];
   __device__ __forceinline__ void load(const float2* cs, float sign) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float4 x = *reinterpret_cast<const float4*>(cs + 2 * e);
-      c[e] = f2_pack(x.x, x.z);
-      s[e] = f2_pack(sign * x.y, sign * x.w);
+    for (int e = 0; e < 8; e += 2) {
+      const float4 x = *reinterpret_cast<const float4*>(cs + e);
+      c[e] = x.x;
+      s[e] = sign * x.y;
+      c[e + 1] = x.z;
+      s[e + 1] = sign * x.w;
     }
   }
-  // The turned pairs (a, b) of the vectors (lo, hi), two values in a register pair.
-  // Products are rounded before they are added (the one fused operation
-  // multiplies by -1), so that the fp32 result, and with it every 4-bit code, is
-  // the one that the definition's plain fp32 operations give.
-  __device__ __forceinline__ void turn(const uint4 lo, const uint4 hi, uint64_t (&ya)[4], uint64_t (&yb)[4]) const {
-    const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
-    const uint64_t minus_one = f2_pack(-1.f, -1.f);
+  // The turned pairs of the vectors (lo, hi).  Products are rounded before they are
+  // added, so that the fp32 result, and with it every 4-bit code, is the one
+  // that the definition's plain fp32 operations give.  (Packed f32x2
+  // operations do not keep that: their products end up fused into the sums.)
+  __device__ __forceinline__ void turn(const uint4 lo, const uint4 hi, float (&ya)[8], float (&yb)[8]) const {
+    float a[8], b[8];
+    unpack_bf16x8(lo, a);
+    unpack_bf16x8(hi, b);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint64_t a = f2_pack(__uint_as_float(l[e] << 16), __uint_as_float(l[e] & 0xFFFF0000u));
-      const uint64_t b = f2_pack(__uint_as_float(h[e] << 16), __uint_as_float(h[e] & 0xFFFF0000u));
-      ya[e] = f2_fma(f2_mul(b, s[e]), minus_one, f2_mul(a, c[e]));
-      yb[e] = f2_add(f2_mul(b, c[e]), f2_mul(a, s[e]));
+    for (int e = 0; e < 8; ++e) {
+      ya[e] = __fsub_rn(__fmul_rn(a[e], c[e]), __fmul_rn(b[e], s[e]));
+      yb[e] = __fadd_rn(__fmul_rn(b[e], c[e]), __fmul_rn(a[e], s[e]));
     }
   }
 };
-
-__device__ __forceinline__ uint4 pack_pairs(const uint64_t (&y)[4]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float a, b;
-    f2_unpack(y[e], a, b);
-    w[e] = pack_bf16x2(a, b);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // Two 16-byte vectors of one head.
 struct Vecs {
@@ -144,11 +134,11 @@ __global__ void __launch_bounds__(kTileThreads, 4) rope_axes_kernel(const RopeAx
   uint4* dst = const_cast<uint4*>(row_of(a.q_out, b, 0, n)) + j;
   long long head = a.q_out.head;
   auto body = [&](int h, const Vecs& v) {
-    uint64_t ya[4], yb[4];
+    float ya[8], yb[8];
     turn.turn(v.lo, v.hi, ya, yb);
     uint4* to = dst + h * head;
-    to[0] = pack_pairs(ya);
-    to[apart] = pack_pairs(yb);
+    to[0] = pack_bf16x8(ya);
+    to[apart] = pack_bf16x8(yb);
   };
   walk_heads(q, a.q.head, lane, a.Hq, tile.lanes, apart, true, x, body);
   // the key heads follow the query heads in the order the lanes share out
@@ -266,11 +256,11 @@ __global__ void __launch_bounds__(kTileThreads, 3) rope_cache_fp4_kernel(const R
     turn.load(cs + tok * kHalf + 8 * j, 1.f);
     uint4* dst = const_cast<uint4*>(row_of(a.q_out, 0, 0, n)) + j;
     walk_heads(q, a.q.head, lane, a.Hq, step, kApart, true, x, [&](int h, const Vecs& v) {
-      uint64_t ya[4], yb[4];
+      float ya[8], yb[8];
       turn.turn(v.lo, v.hi, ya, yb);
       uint4* to = dst + h * a.q_out.head;
-      to[0] = pack_pairs(ya);
-      to[kApart] = pack_pairs(yb);
+      to[0] = pack_bf16x8(ya);
+      to[kApart] = pack_bf16x8(yb);
     });
     // the key and value heads follow the query heads in the order the lanes share out
     const int first = ((lane - a.Hq) % step + step) % step;
@@ -282,16 +272,16 @@ __global__ void __launch_bounds__(kTileThreads, 3) rope_cache_fp4_kernel(const R
     uint8_t* code = spans + Span::kKeyCodes + off * Span::kCodeRow + group * 8;
     uint8_t* scale = spans + Span::kKeyScales + off * Span::kScaleRow + group;
     walk_heads(row_of(a.k, 0, 0, n) + j, a.k.head, first, a.Hkv, step, kApart, false, x, [&](int h, const Vecs& v) {
-      uint64_t ya[4], yb[4];
+      float ya[8], yb[8];
       turn.turn(v.lo, v.hi, ya, yb);
       float y[16];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 8; ++e) {
         // the even thread gives its high half for the odd one's low half
-        const uint64_t mine = odd ? yb[e] : ya[e];
-        const uint64_t other = __shfl_xor_sync(pair_mask, odd ? ya[e] : yb[e], 1);
-        f2_unpack(odd ? other : mine, y[2 * e], y[2 * e + 1]);
-        f2_unpack(odd ? mine : other, y[8 + 2 * e], y[8 + 2 * e + 1]);
+        const float mine = odd ? yb[e] : ya[e];
+        const float other = __shfl_xor_sync(pair_mask, odd ? ya[e] : yb[e], 1);
+        y[e] = odd ? other : mine;
+        y[8 + e] = odd ? mine : other;
       }
       const float m = amax16(y);
       const uint32_t s8 = quant.scale(m);

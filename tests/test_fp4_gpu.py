@@ -329,12 +329,12 @@ def run_append(env, seed, lens, new, Hq, Hkv, d, sections, base=10000.0, per_axi
     got = [v[blk, :, off] for v in views]
     assert np.array_equal(got[1], ref.pack(cv)), "value codes"
     assert np.array_equal(got[3], sv), "value scales"
-    # keys: a cosine that is one unit in the last place off moves a key across a
-    # border between two codes now and then; what moved lies on the border
+    # keys: a cosine that is one unit in the last place off (3 in 10,000 are) moves a
+    # key across a border between two codes once in ten million; what moved lies on it
     bad_scale = got[2] != sk
-    assert bad_scale.mean() <= 1e-5
+    assert bad_scale.sum() <= 1
     diff = (ref.unpack(got[0]) != ck) & ~np.repeat(bad_scale, 16, -1)
-    assert diff.mean() <= 1e-5
+    assert diff.sum() <= 1
     if diff.any():
         div = np.repeat(ref.E4M3[sk].astype(np.float32) * np.float32(k_scale), 16, -1)
         y = np.abs(k32[diff] / div[diff])
@@ -372,6 +372,35 @@ def test_append_scales(env, k_scale, v_scale, per_axis):
 
 def test_append_many_heads_and_long_positions(env):
     run_append(env, 511, [32768, 20000], 8, 128, 16, 128, (64,), base=500000.0)
+
+
+def test_append_rounds_products_before_their_difference(env):
+    """Keys whose two products nearly cancel: what is left is 2^-9 of a product, so a
+    product that was not rounded to fp32 (a fused multiply-add) shows up as
+    2^-15 of the key.  With the oracle's own products fused that way 36 codes and
+    scales of these move; a cosine one unit off does it to 3 in 10,000 of those."""
+    torch, ex, dev = env
+    T, Hkv, d = 2048, 4, 128
+    half = d // 2
+    pos = np.arange(1, T + 1, dtype=np.int32)[None]
+    c, s = ref.cos_sin(pos, (half,), 10000.0, False)
+    a = synth.bf16_bits_to_f32(synth.normal_bf16(570, 1, (T, Hkv, half)))
+    b = np.where(np.abs(s[:, None]) > 0.01, a * c[:, None] / s[:, None], a)
+    k = synth.f32_to_bf16_bits(np.concatenate([a, b], -1).astype(np.float32))
+    k32 = ref.turn(synth.bf16_bits_to_f32(k), c.astype(np.float32)[:, None], s.astype(np.float32)[:, None])
+    codes, s8 = ref.quantise(k32, 1e-4)
+    kd = to_dev(k, dev)
+    z = torch.zeros(T, device=dev, dtype=torch.int32)
+    at = torch.arange(T, device=dev, dtype=torch.int32)
+    tbl = torch.arange(T // 16, device=dev, dtype=torch.int32).view(1, -1)
+    cache = ex.attn_fp4_cache(T // 16, Hkv, d)
+    ex.attn_rope_cache_write_fp4(kd, kd, kd, z, at, to_dev(pos, dev), tbl, cache, (half,), base=10000.0, k_scale=1e-4)
+    got = ref.split(cache.cpu().numpy(), d)
+    got_codes = got[0].transpose(0, 2, 1, 3).reshape(T, Hkv, -1)
+    got_s8 = got[2].transpose(0, 2, 1, 3).reshape(T, Hkv, -1)
+    low = slice(0, half // 16)  # the low halves hold the differences
+    wrong = (got_s8 != s8)[..., low].sum() + (ref.unpack(got_codes) != codes)[..., :half].sum()
+    assert wrong <= 3, wrong
 
 
 def test_append_special_values(env):
