@@ -720,7 +720,8 @@ int attn_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const
   if (rc != EXATTN_OK) return rc;
   if (B == 0 || N == 0 || Hq + Hkv == 0) return EXATTN_OK;
   if (positions == nullptr || (Hq > 0 && (q == nullptr || q_out == nullptr)) ||
-      (Hkv > 0 && (k == nullptr || k_out == nullptr)) || (Hq > 0 && Hkv > 0 && q_out == k_out))
+      (Hkv > 0 && (k == nullptr || k_out == nullptr)) ||
+      (Hq > 0 && Hkv > 0 && (q_out == k_out || q_out == k || k_out == q)))
     return EXATTN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || !aligned4(positions))
     return EXATTN_ERR_ALIGNMENT;
@@ -769,7 +770,8 @@ int attn_rope_cache_write_fp4(const void* q, const void* k, const void* v, void*
   if ((rc = rope_table(sections, num_axes, d, base, per_axis, &table)) != EXATTN_OK) return rc;
   if (num_tokens == 0) return EXATTN_OK;
   if ((Hq > 0 && (q == nullptr || q_out == nullptr)) || k == nullptr || v == nullptr || seq_ids == nullptr ||
-      slots == nullptr || positions == nullptr || block_table == nullptr || kv_cache == nullptr)
+      slots == nullptr || positions == nullptr || block_table == nullptr || kv_cache == nullptr ||
+      (Hq > 0 && (q_out == k || q_out == v)))
     return EXATTN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) || !aligned16(kv_cache) ||
       !aligned4(seq_ids) || !aligned4(slots) || !aligned4(positions) || !aligned4(block_table))
@@ -842,7 +844,9 @@ int attn_cache_read_fp4(const void* kv_cache, const int32_t* seq_ids, const int3
 }
 
 size_t attn_decode_fp4_workspace_bytes(int num_seqs, int Hq, int Hkv, int d, int max_blocks_per_seq) {
-  if (num_seqs < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128) || max_blocks_per_seq < 1) return 0;
+  if (num_seqs < 1 || num_seqs > 65535 || Hq < 1 || Hq > 65535 || Hkv < 1 || Hq % Hkv != 0 ||
+      fp4_sizes(Hkv, d, 1, 1, max_blocks_per_seq) != EXATTN_OK)
+    return 0;
   const exattn::Fp4Plan plan(num_seqs, Hkv, Hq / Hkv, max_blocks_per_seq);
   return plan.fits ? plan.bytes(d) : 0;
 }
@@ -854,7 +858,8 @@ int attn_decode_paged_fp4(const void* q, const void* kv_cache, const int32_t* bl
   if (num_seqs < 0 || Hq < 1) return EXATTN_ERR_INVALID_ARG;
   int rc = fp4_sizes(Hkv, d, num_blocks, 1, max_blocks_per_seq);
   if (rc != EXATTN_OK) return rc;
-  if (Hq % Hkv != 0 || !good_scale(scale) || !good_scale(k_scale) || !good_scale(v_scale))
+  if (Hq % Hkv != 0 || !good_scale(scale) || !good_scale(k_scale) || !good_scale(v_scale) ||
+      !good_scale(static_cast<float>(2.0 * scale * k_scale)))
     return EXATTN_ERR_INVALID_ARG;
   if (num_seqs > 65535 || Hq > 65535 || static_cast<int64_t>(num_seqs) * Hq > 0x7FFFFFFF)
     return EXATTN_ERR_UNSUPPORTED;

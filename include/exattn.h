@@ -301,7 +301,8 @@ int attn_rope_cache_write(void* q, const void* k, const void* v, const int32_t* 
  * position), the rotation is in fp32, one rounding to bf16.
  *   q, q_out [B, Hq, N, d], k, k_out [B, Hkv, N, d] bf16 by their strides, d
  *            contiguous; q_out may be q and k_out k (with the same strides, in
- *            place), no other overlap.  Hq or Hkv may be 0 (its pointers NULL).
+ *            place), no other overlap (an output at the other input's or output's
+ *            address: EXATTN_ERR_INVALID_ARG).  Hq or Hkv may be 0 (its pointers NULL).
  *   positions int32 by its strides
  *   strides  host array of 15, in elements: q (batch, head, token), k, q_out,
  *            k_out, positions (axis, batch, token).  Those of dimensions of
@@ -341,7 +342,8 @@ size_t attn_fp4_cache_bytes(int num_blocks, int Hkv, int d);
  * rounded to nearest, ties to even, e2m1 saturating at 6.  The keys are the
  * fp32 results of the rotation, not rounded to bf16 before.  A group that holds
  * a NaN or an infinity gets a NaN scale: all of it reads back as NaN.
- *   q, q_out  [num_tokens, Hq, d] bf16 by strides; q_out may be q.  Hq may be 0.
+ *   q, q_out  [num_tokens, Hq, d] bf16 by strides; q_out may be q, and overlaps
+ *             nothing else.  Hq may be 0.
  *   k, v      [num_tokens, Hkv, d] bf16 by strides
  *   seq_ids, slots int32 [num_tokens]: sequence, and the token's index in it
  *             (with one axis usually its position too)
@@ -386,10 +388,12 @@ int attn_cache_read_fp4(const void* kv_cache, const int32_t* seq_ids, const int3
  * values that the cache stands for.  q, out [num_seqs, Hq, d] bf16, lse
  * [num_seqs, Hq] fp32 or NULL, block_table, ctx_lens and their checks on the
  * device as attn_decode_paged; keys and values enter exactly, the weights are
- * rounded to fp16.  ctx_len 0 gives out = 0, lse = -inf.
+ * rounded to fp16.  ctx_len 0 gives out = 0, lse = -inf.  scale, k_scale and
+ * v_scale are finite and > 0, and so is 2 scale k_scale in fp32
+ * (EXATTN_ERR_INVALID_ARG).
  *   workspace: attn_decode_fp4_workspace_bytes(...) bytes, 16-byte aligned, its
- *   contents clobbered; NULL where that is 0.  Calls whose executions overlap
- *   need one each.
+ *   contents clobbered; NULL where that is 0 (also for invalid arguments).
+ *   Calls whose executions overlap need one each.
  * One or two launches on `stream` (the second merges the splits of a sequence,
  * a programmatic dependent launch), asynchronous, deterministic; it can be
  * captured into a CUDA graph.  A bounded wait that runs out sets

@@ -69,6 +69,13 @@ def test_rope_axes_rejections(lib):
     assert rope(lib, Hq=0, Hkv=0, q=None, k=None, qo=None, ko=None, pos=None) == 0
 
 
+def test_outputs_over_another_tensors_place_are_refused(lib):
+    assert rope(lib, qo=FAKE + 16) == 1               # queries over the keys
+    assert rope(lib, ko=FAKE) == 1                    # keys over the queries
+    assert append(lib, qo=FAKE + 16) == 1             # queries over the keys
+    assert append(lib, qo=FAKE + 32) == 1             # ... the values
+
+
 def append(lib, q=FAKE, k=FAKE + 16, v=FAKE + 32, qo=FAKE + 48, sid=FAKE + 64, slots=FAKE + 80, pos=FAKE + 96,
            bt=FAKE + 112, cache=FAKE + 128, strides="default", sections=(64,), T=4, Hq=8, Hkv=2, d=128, S=2, nb=10,
            mb=4, base=10000.0, per_axis=0, ks=1.0, vs=1.0, **change):
@@ -161,6 +168,17 @@ def test_decode_rejections(lib):
     assert dec(lib, S=65535, Hq=65535, Hkv=65535) == 2               # more rows than 2^31
     assert dec(lib, S=65535, Hq=8, Hkv=8, mb=1 << 26, ws_bytes=1 << 30) == 2  # more work units than 2^31
     assert dec(lib, S=0, q=None) == 0
+
+
+def test_decode_scale_products_out_of_range_are_refused(lib):
+    assert dec(lib, scale=1e30, ks=1e30) == 1         # infinite: zeros times it would be NaN
+    assert dec(lib, scale=1e-30, ks=1e-30) == 1       # zero: every weight the same
+
+
+def test_workspace_of_refused_sizes_is_zero(lib):
+    assert lib.attn_decode_fp4_workspace_bytes(2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 64, 2 ** 31 - 1) == 0
+    assert lib.attn_decode_fp4_workspace_bytes(65536, 8, 8, 64, 64) == 0
+    assert lib.attn_decode_fp4_workspace_bytes(1, 8, 8, 64, (1 << 26) + 1) == 0
 
 
 def test_sizes(lib):
