@@ -26,6 +26,7 @@ namespace {
 constexpr int kTileThreads = 256;
 constexpr int kRopeLanes = 8;  // heads of a token in flight together
 constexpr int kFp4Lanes = 4;
+constexpr int kFp4Stages = 5;  // rows of a thread on their way, and the one at hand
 
 // How a CTA's threads cover tokens and heads.
 struct Tile {
@@ -217,6 +218,23 @@ __device__ __forceinline__ float amax16(const float (&x)[16]) {
   return m;
 }
 
+// Rows of a token on their way into shared memory, where a thread finds its own two
+// vectors of each; only it reads them, so no barrier is needed.  A stage is filled
+// again after the row after it has been waited for, when its vectors are long in
+// registers.
+template <int kStages>
+struct RowRing {
+  uint4* slot;  // this thread's: vector x of stage s at slot[(2 s + x) * kTileThreads]
+  static constexpr size_t kBytes = sizeof(uint4) * 2 * kStages * kTileThreads;
+  __device__ __forceinline__ void fetch(int stage, const uint4* src, int apart) const {
+    cp_async16(smem_u32(slot + 2 * stage * kTileThreads), src, true);
+    cp_async16(smem_u32(slot + (2 * stage + 1) * kTileThreads), src + apart, true);
+  }
+  __device__ __forceinline__ Vecs take(int stage) const {
+    return Vecs{slot[2 * stage * kTileThreads], slot[(2 * stage + 1) * kTileThreads]};
+  }
+};
+
 // Append.  A rotated key's thread has 8 low and 8 high columns, half of a scale
 // group each; neighbouring threads swap halves, so that the even one has the
 // low group and the odd one the high group.  A value's thread loads a whole
@@ -226,22 +244,38 @@ __global__ void __launch_bounds__(kTileThreads, 3) rope_cache_fp4_kernel(const R
                                                                          const __grid_constant__ RopeAxesTable table,
                                                                          const Tile tile) {
   using Span = Fp4Span<D>;
+  using Ring = RowRing<kFp4Stages>;
   constexpr int kHalf = D / 2, kApart = kHalf / 8, kPerTok = D / 16;
   extern __shared__ __align__(16) uint8_t rope_axes_smem[];
-  float2* cs = reinterpret_cast<float2*>(rope_axes_smem);
+  float2* cs = reinterpret_cast<float2*>(rope_axes_smem + Ring::kBytes);
+  const Ring ring{reinterpret_cast<uint4*>(rope_axes_smem) + threadIdx.x};
   const long long n0 = static_cast<long long>(blockIdx.x) * tile.toks;
   const int count = static_cast<int>(a.at.num_tokens - n0 < tile.toks ? a.at.num_tokens - n0 : tile.toks);
   const int j = threadIdx.x % kPerTok, rest = threadIdx.x / kPerTok;
   const int tok = rest % tile.toks, lane = rest / tile.toks;
   const bool works = lane < tile.lanes && tok < count;
   const long long n = n0 + tok;
+  const int step = tile.lanes;
+  // rows of a token: query heads, key heads, value heads
+  const int first_key = a.Hq, first_value = a.Hq + a.Hkv, rows = works ? a.Hq + 2 * a.Hkv : 0;
   const uint4* q = row_of(a.q, 0, 0, n) + j;
-  Vecs x[2];
+  const uint4* k = row_of(a.k, 0, -first_key, n) + j;
+  const uint4* v = row_of(a.v, 0, -first_value, n) + 2 * j;
+  int next = lane;  // row to fetch
+  auto fetch = [&](int stage) {
+    if (next < first_value) {
+      if (next < rows) ring.fetch(stage, next < first_key ? q + next * a.q.head : k + next * a.k.head, kApart);
+    } else if (next < rows) {
+      ring.fetch(stage, v + next * a.v.head, 1);
+    }
+    cp_async_commit();
+    next += step;
+  };
+#pragma unroll
+  for (int s = 0; s < kFp4Stages - 1; ++s) fetch(s);
   int off = 0;
   long long blk = -1;
   if (works) {
-    if (lane < a.Hq) x[0].load(q + lane * a.q.head, kApart);
-    if (lane + tile.lanes < a.Hq) x[1].load(q + (lane + tile.lanes) * a.q.head, kApart);
     blk = find_block(a.at, n, &off);
     if (blk < 0 && j == 0 && lane == 0) atomicOr(a.at.status, 2u);  // EXATTN_DEVICE_BOUNDS_BIT
   }
@@ -250,30 +284,39 @@ __global__ void __launch_bounds__(kTileThreads, 3) rope_cache_fp4_kernel(const R
   __syncthreads();
   if (!works) return;
   uint8_t* spans = static_cast<uint8_t*>(a.kv_cache) + (blk < 0 ? 0 : blk) * a.Hkv * Span::kBytes;
-  const int step = tile.lanes;
+  int stage = 0, behind = kFp4Stages - 1;  // of the row at hand, and of the one before it
+  auto take = [&]() {
+    cp_async_wait<kFp4Stages - 2>();
+    const Vecs x = ring.take(stage);
+    fetch(behind);
+    behind = stage;
+    stage = stage + 1 == kFp4Stages ? 0 : stage + 1;
+    return x;
+  };
+  int r = lane;
   {
     Turn8 turn;
     turn.load(cs + tok * kHalf + 8 * j, 1.f);
     uint4* dst = const_cast<uint4*>(row_of(a.q_out, 0, 0, n)) + j;
-    walk_heads(q, a.q.head, lane, a.Hq, step, kApart, true, x, [&](int h, const Vecs& v) {
+    for (; r < first_key; r += step) {
+      const Vecs x = take();
       float ya[8], yb[8];
-      turn.turn(v.lo, v.hi, ya, yb);
-      uint4* to = dst + h * a.q_out.head;
+      turn.turn(x.lo, x.hi, ya, yb);
+      uint4* to = dst + r * a.q_out.head;
       to[0] = pack_bf16x8(ya);
       to[kApart] = pack_bf16x8(yb);
-    });
-    // the key and value heads follow the query heads in the order the lanes share out
-    const int first = ((lane - a.Hq) % step + step) % step;
+    }
     const Quantiser quant(a.k_scale);
     const bool odd = j & 1;
-    const unsigned int pair_mask = 3u << (threadIdx.x & 30);  // this thread and its neighbour: same token and heads
+    const unsigned int pair_mask = 3u << (threadIdx.x & 30);  // this thread and its neighbour: same token and rows
     // the group this thread ends up with: j / 2 of the low half, or of the high one
     const int group = j / 2 + (odd ? kPerTok / 2 : 0);
     uint8_t* code = spans + Span::kKeyCodes + off * Span::kCodeRow + group * 8;
     uint8_t* scale = spans + Span::kKeyScales + off * Span::kScaleRow + group;
-    walk_heads(row_of(a.k, 0, 0, n) + j, a.k.head, first, a.Hkv, step, kApart, false, x, [&](int h, const Vecs& v) {
+    for (; r < first_value; r += step) {
+      const Vecs x = take();
       float ya[8], yb[8];
-      turn.turn(v.lo, v.hi, ya, yb);
+      turn.turn(x.lo, x.hi, ya, yb);
       float y[16];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -286,19 +329,19 @@ __global__ void __launch_bounds__(kTileThreads, 3) rope_cache_fp4_kernel(const R
       const float m = amax16(y);
       const uint32_t s8 = quant.scale(m);
       if (blk >= 0) {
-        *reinterpret_cast<uint2*>(code + h * Span::kBytes) = quant.codes(y, m, s8);
-        scale[h * Span::kBytes] = static_cast<uint8_t>(s8);
+        const int at = (r - first_key) * Span::kBytes;
+        *reinterpret_cast<uint2*>(code + at) = quant.codes(y, m, s8);
+        scale[at] = static_cast<uint8_t>(s8);
       }
-    });
+    }
   }
-  if (blk < 0) return;
   const Quantiser quant(a.v_scale);
-  const int first = ((lane - a.Hq - a.Hkv) % step + step) % step;
   uint8_t* code = spans + Span::kValueCodes + off * Span::kCodeRow + j * 8;
   uint8_t* scale = spans + Span::kValueScales + off * Span::kScaleRow + j;
-  walk_heads(row_of(a.v, 0, 0, n) + 2 * j, a.v.head, first, a.Hkv, step, 1, false, x, [&](int h, const Vecs& v) {
+  for (; r < rows; r += step) {
+    const Vecs x = take();
     float y[16];
-    const uint32_t w[8] = {v.lo.x, v.lo.y, v.lo.z, v.lo.w, v.hi.x, v.hi.y, v.hi.z, v.hi.w};
+    const uint32_t w[8] = {x.lo.x, x.lo.y, x.lo.z, x.lo.w, x.hi.x, x.hi.y, x.hi.z, x.hi.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       y[2 * e] = __uint_as_float(w[e] << 16);
@@ -306,9 +349,12 @@ __global__ void __launch_bounds__(kTileThreads, 3) rope_cache_fp4_kernel(const R
     }
     const float m = amax16(y);
     const uint32_t s8 = quant.scale(m);
-    *reinterpret_cast<uint2*>(code + h * Span::kBytes) = quant.codes(y, m, s8);
-    scale[h * Span::kBytes] = static_cast<uint8_t>(s8);
-  });
+    if (blk >= 0) {
+      const int at = (r - first_value) * Span::kBytes;
+      *reinterpret_cast<uint2*>(code + at) = quant.codes(y, m, s8);
+      scale[at] = static_cast<uint8_t>(s8);
+    }
+  }
 }
 
 // Read: thread j of a token takes group j of the keys and values of every head
@@ -399,7 +445,7 @@ cudaError_t launch_rope_cache_write_fp4(const RopeFp4Args& a, const RopeAxesTabl
   if (sms <= 0) return cudaErrorInvalidDevice;
   const Tile t = make_tile(a.d, a.at.num_tokens, a.Hq + 2 * a.Hkv, kFp4Lanes, sms);
   const unsigned int grid = tiles(t, a.at.num_tokens);
-  const size_t smem = sizeof(float2) * t.toks * (a.d / 2);
+  const size_t smem = RowRing<kFp4Stages>::kBytes + sizeof(float2) * t.toks * (a.d / 2);
   if (a.d == 64)
     rope_cache_fp4_kernel<64><<<grid, kTileThreads, smem, stream>>>(a, table, t);
   else
