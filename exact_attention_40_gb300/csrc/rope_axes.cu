@@ -11,8 +11,8 @@
 // its threads then walk the heads.  Thread (token, j) of d/16 threads a token
 // owns the 8 pairs 8 j .. 8 j + 7 of every head it visits (two 16-byte loads,
 // two 16-byte stores), so its cosines and sines stay in registers; `lanes`
-// such sets of threads share the heads.  The first heads are loaded before the
-// angles are formed, so the two latencies overlap.
+// such sets of threads share the heads.  Its loads run three or four heads ahead,
+// through shared memory, and start before the angles are formed.
 #include <cuda_bf16.h>
 
 #include "fp4.cuh"
@@ -24,9 +24,16 @@ namespace exattn {
 namespace {
 
 constexpr int kTileThreads = 256;
-constexpr int kRopeLanes = 8;  // heads of a token in flight together
+// Measured choices (heads of a token in flight together, rows of a thread in the ring
+// with the one at hand, CTAs an SM).  Rotation of 8 x 4096 tokens, 32 + 32 heads of 128:
+// 155 us with 8 lanes, 4 or 5 stages and 4 CTAs, 157 with 4 lanes, 166 with 5 CTAs of 3
+// stages, 157 with two rows in registers and no ring.  Append of 16,384 tokens, 32 + 2 * 8
+// heads: 58 us with 4 lanes, 5 stages and 3 CTAs, 59 with 4 stages, 63 with 4 CTAs, 67
+// with 8 lanes, 61 with 2, 67 without the ring.
+constexpr int kRopeLanes = 8;
+constexpr int kRopeStages = 4;  // rows of a thread on their way, and the one at hand
 constexpr int kFp4Lanes = 4;
-constexpr int kFp4Stages = 5;  // rows of a thread on their way, and the one at hand
+constexpr int kFp4Stages = 5;
 
 // How a CTA's threads cover tokens and heads.
 struct Tile {
@@ -79,37 +86,35 @@ struct Turn8 {
   }
 };
 
-// Two 16-byte vectors of one head.
+// Two 16-byte vectors of one row.
 struct Vecs {
   uint4 lo, hi;
-  __device__ __forceinline__ void load(const uint4* src, int apart) {
-    lo = src[0];
-    hi = src[apart];
-  }
 };
 
-// Heads first, first + step, ... below count of one view, two at a time: body(head,
-// vectors).  `have`: the first two are already in x.
-template <typename Body>
-__device__ __forceinline__ void walk_heads(const uint4* src, long long head, int first, int count, int step,
-                                           int apart, bool have, Vecs (&x)[2], Body body) {
-  for (int h = first; h < count; h += 2 * step) {
-    const bool two = h + step < count;
-    if (!have) {
-      x[0].load(src + h * head, apart);
-      if (two) x[1].load(src + (h + step) * head, apart);
-    }
-    have = false;
-    body(h, x[0]);
-    if (two) body(h + step, x[1]);
+// Rows of a token on their way into shared memory, where a thread finds its own two
+// vectors of each; only it reads them, so no barrier is needed.  A stage is filled
+// again after the row after it has been waited for, when its vectors are long in
+// registers.
+template <int kStages>
+struct RowRing {
+  uint4* slot;  // this thread's: vector x of stage s at slot[(2 s + x) * kTileThreads]
+  static constexpr size_t kBytes = sizeof(uint4) * 2 * kStages * kTileThreads;
+  __device__ __forceinline__ void fetch(int stage, const uint4* src, int apart) const {
+    cp_async16(smem_u32(slot + 2 * stage * kTileThreads), src, true);
+    cp_async16(smem_u32(slot + (2 * stage + 1) * kTileThreads), src + apart, true);
   }
-}
+  __device__ __forceinline__ Vecs take(int stage) const {
+    return Vecs{slot[2 * stage * kTileThreads], slot[(2 * stage + 1) * kTileThreads]};
+  }
+};
 
 __global__ void __launch_bounds__(kTileThreads, 4) rope_axes_kernel(const RopeAxesArgs a,
                                                                     const __grid_constant__ RopeAxesTable table,
                                                                     const Tile tile) {
+  using Ring = RowRing<kRopeStages>;
   extern __shared__ __align__(16) uint8_t rope_axes_smem[];
-  float2* cs = reinterpret_cast<float2*>(rope_axes_smem);
+  float2* cs = reinterpret_cast<float2*>(rope_axes_smem + Ring::kBytes);
+  const Ring ring{reinterpret_cast<uint4*>(rope_axes_smem) + threadIdx.x};
   const int half = a.d / 2, apart = half / 8;
   const unsigned int total = static_cast<unsigned int>(a.B) * a.N, n0 = blockIdx.x * tile.toks;
   const int count = static_cast<int>(min(total - n0, static_cast<unsigned int>(tile.toks)));
@@ -117,13 +122,19 @@ __global__ void __launch_bounds__(kTileThreads, 4) rope_axes_kernel(const RopeAx
   const int tok = rest % tile.toks, lane = rest / tile.toks;
   const bool works = lane < tile.lanes && tok < count;
   const unsigned int b = (n0 + tok) / a.N, n = n0 + tok - b * a.N;
+  const int step = tile.lanes;
+  // rows of a token: query heads, key heads
+  const int rows = works ? a.Hq + a.Hkv : 0;
   const uint4* q = row_of(a.q, b, 0, n) + j;
-  const uint4* k = row_of(a.k, b, 0, n) + j;
-  Vecs x[2];
-  if (works) {
-    if (lane < a.Hq) x[0].load(q + lane * a.q.head, apart);
-    if (lane + tile.lanes < a.Hq) x[1].load(q + (lane + tile.lanes) * a.q.head, apart);
-  }
+  const uint4* k = row_of(a.k, b, -a.Hq, n) + j;
+  int next = lane;  // row to fetch
+  auto fetch = [&](int stage) {
+    if (next < rows) ring.fetch(stage, next < a.Hq ? q + next * a.q.head : k + next * a.k.head, apart);
+    cp_async_commit();
+    next += step;
+  };
+#pragma unroll
+  for (int s = 0; s < kRopeStages - 1; ++s) fetch(s);
   tile_angles(cs, table, half, count, [&](int at, int axis) {
     const unsigned int pb = (n0 + at) / a.N, pn = n0 + at - pb * a.N;
     return static_cast<long long>(a.positions[axis * a.pos_axis + pb * a.pos_batch + pn * a.pos_token]);
@@ -132,21 +143,21 @@ __global__ void __launch_bounds__(kTileThreads, 4) rope_axes_kernel(const RopeAx
   if (!works) return;
   Turn8 turn;
   turn.load(cs + tok * half + 8 * j, a.inverse ? -1.f : 1.f);
-  uint4* dst = const_cast<uint4*>(row_of(a.q_out, b, 0, n)) + j;
-  long long head = a.q_out.head;
-  auto body = [&](int h, const Vecs& v) {
+  uint4* q_out = const_cast<uint4*>(row_of(a.q_out, b, 0, n)) + j;
+  uint4* k_out = const_cast<uint4*>(row_of(a.k_out, b, -a.Hq, n)) + j;
+  int stage = 0, behind = kRopeStages - 1;  // of the row at hand, and of the one before it
+  for (int r = lane; r < rows; r += step) {
+    cp_async_wait<kRopeStages - 2>();
+    const Vecs x = ring.take(stage);
+    fetch(behind);
+    behind = stage;
+    stage = stage + 1 == kRopeStages ? 0 : stage + 1;
     float ya[8], yb[8];
-    turn.turn(v.lo, v.hi, ya, yb);
-    uint4* to = dst + h * head;
+    turn.turn(x.lo, x.hi, ya, yb);
+    uint4* to = r < a.Hq ? q_out + r * a.q_out.head : k_out + r * a.k_out.head;
     to[0] = pack_bf16x8(ya);
     to[apart] = pack_bf16x8(yb);
-  };
-  walk_heads(q, a.q.head, lane, a.Hq, tile.lanes, apart, true, x, body);
-  // the key heads follow the query heads in the order the lanes share out
-  const int first = ((lane - a.Hq) % tile.lanes + tile.lanes) % tile.lanes;
-  dst = const_cast<uint4*>(row_of(a.k_out, b, 0, n)) + j;
-  head = a.k_out.head;
-  walk_heads(k, a.k.head, first, a.Hkv, tile.lanes, apart, false, x, body);
+  }
 }
 
 // Span index (block * Hkv) and offset of a token in the cache, or -1.
@@ -217,23 +228,6 @@ __device__ __forceinline__ float amax16(const float (&x)[16]) {
   for (int e = 1; e < 16; ++e) m = max_nan(m, fabsf(x[e]));
   return m;
 }
-
-// Rows of a token on their way into shared memory, where a thread finds its own two
-// vectors of each; only it reads them, so no barrier is needed.  A stage is filled
-// again after the row after it has been waited for, when its vectors are long in
-// registers.
-template <int kStages>
-struct RowRing {
-  uint4* slot;  // this thread's: vector x of stage s at slot[(2 s + x) * kTileThreads]
-  static constexpr size_t kBytes = sizeof(uint4) * 2 * kStages * kTileThreads;
-  __device__ __forceinline__ void fetch(int stage, const uint4* src, int apart) const {
-    cp_async16(smem_u32(slot + 2 * stage * kTileThreads), src, true);
-    cp_async16(smem_u32(slot + (2 * stage + 1) * kTileThreads), src + apart, true);
-  }
-  __device__ __forceinline__ Vecs take(int stage) const {
-    return Vecs{slot[2 * stage * kTileThreads], slot[(2 * stage + 1) * kTileThreads]};
-  }
-};
 
 // Append.  A rotated key's thread has 8 low and 8 high columns, half of a scale
 // group each; neighbouring threads swap halves, so that the even one has the
@@ -418,6 +412,11 @@ Tile make_tile(int d, long long tokens, int rows, int lanes, int sms) {
   t.per_tok = d / 16;
   const int slots = kTileThreads / t.per_tok;
   while (lanes > rows) lanes /= 2;
+  // A ring and the cosines and sines, 4 d bytes a token and so 64 for each of its d/16
+  // threads, divided by the lanes: within the 48 KB that a launch has without asking (an
+  // append's tokens have two rows or more, so two lanes).
+  static_assert(RowRing<kRopeStages>::kBytes + 64 * kTileThreads <= 48 * 1024, "shared memory of the rotation");
+  static_assert(RowRing<kFp4Stages>::kBytes + 32 * kTileThreads <= 48 * 1024, "shared memory of the append");
   t.toks = 1;
   while (2 * t.toks * lanes <= slots) t.toks *= 2;
   while (t.toks > 1 && (tokens + t.toks - 1) / t.toks < sms && 2 * (slots / t.toks) <= rows) t.toks /= 2;
@@ -436,7 +435,7 @@ cudaError_t launch_rope_axes(const RopeAxesArgs& a, const RopeAxesTable& table, 
   if (sms <= 0) return cudaErrorInvalidDevice;
   const long long tokens = static_cast<long long>(a.B) * a.N;
   const Tile t = make_tile(a.d, tokens, a.Hq + a.Hkv, kRopeLanes, sms);
-  rope_axes_kernel<<<tiles(t, tokens), kTileThreads, sizeof(float2) * t.toks * (a.d / 2), stream>>>(a, table, t);
+  rope_axes_kernel<<<tiles(t, tokens), kTileThreads, RowRing<kRopeStages>::kBytes + sizeof(float2) * t.toks * (a.d / 2), stream>>>(a, table, t);
   return cudaGetLastError();
 }
 

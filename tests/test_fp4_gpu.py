@@ -356,7 +356,8 @@ def run_append(env, seed, lens, new, Hq, Hkv, d, sections, base=10000.0, per_axi
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("lens,new,Hq,Hkv,axes", [
     ([1], 1, 1, 1, 1), ([1, 16, 17, 300], 1, 8, 2, 1), ([40, 3, 70, 33], 40, 4, 4, 3), ([500], 333, 14, 2, 3),
-    ([64] * 20, 64, 4, 1, 2), ([2000, 700], 700, 3, 1, 4)])
+    ([64] * 20, 64, 4, 1, 2), ([2000, 700], 700, 3, 1, 4),
+    ([2500] * 3, 2500, 0, 1, 1)])
 def test_append_bytes_and_read(env, d, lens, new, Hq, Hkv, axes):
     half = d // 2
     sections = {1: (half,), 2: (half // 2, half // 2), 3: (half // 4, half // 4 + 4, half // 2 - 4),

@@ -65,6 +65,8 @@ CASES = [  # B, N, Hq, Hkv, d, sections, per_axis
     (1, 90, 3, 2, 48, (8, 8, 8), True),
     (1, 50, 2, 2, 96, (0, 48), False),
     (2, 3000, 2, 1, 112, (56,), True),
+    (1, 5000, 1, 0, 256, (128,), False),  # one head and many tokens: the largest tiles
+    (1, 60000, 0, 1, 16, (8,), True),
 ]
 
 
