@@ -284,7 +284,6 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
 
-  cudaTriggerProgrammaticLaunchCompletion();  // the merge may launch and wait while this runs
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // (the same in all lanes, for the compiler too)
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2;  // mma group: rows g, g + 8 of A and the accumulator, column g of B
@@ -299,6 +298,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
     }
     fence_mbar_init();
   }
+  dependency_sync();  // (the merge may launch and wait while this runs)
   const int max_ctx = p.max_blocks_per_seq * kBlk;
   auto ctx_of = [&](int s) { return clamp_ctx(__ldg(p.ctx_lens + s), max_ctx, p.status); };
   // Queries as B fragments: column g = query head hq0 + 8 nt + g; step ks,
@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp4_combine_kernel(const
     }
     __syncthreads();
   }
-  cudaGridDependencySynchronize();  // launched while the split kernel runs
+  dependency_sync();  // launched while the split kernel runs, which has begun after all before it ended
   const Fp4Joint joint = p.joints != nullptr ? p.joints[blockIdx.y] : found;
   if (joint.more == 0 || r >= joint.rows) return;
   const int used = joint.more + 1;
@@ -974,23 +974,8 @@ cudaError_t launch_split(const Fp4SplitParams& sp, int ctas, cudaStream_t stream
   cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(decode_fp4_split_kernel<D, NT, kCluster>),
                                   static_cast<int>(smem), smem_set);
   if (e != cudaSuccess) return e;
-  if (!kCluster) {
-    decode_fp4_split_kernel<D, NT, kCluster><<<ctas, kCtaThreads, smem, stream>>>(sp);
-    return cudaGetLastError();
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kCtaThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kFp4ClusterCtas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_fp4_split_kernel<D, NT, kCluster>, sp);
+  return launch_overlapped(decode_fp4_split_kernel<D, NT, kCluster>, ctas, kCtaThreads, smem, stream,
+                           kCluster ? kFp4ClusterCtas : 1, sp);
 }
 
 template <int D>
@@ -1040,16 +1025,8 @@ cudaError_t launch_d(const DecodeFp4Args& a, const DeviceGuard& g, cudaStream_t 
   cp.max_blocks_per_seq = a.max_blocks_per_seq;
   cp.ctas = plan.ctas;
   cp.rows = plan.rows;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sp.group < plan.rows ? sp.group : plan.rows, plan.joints > 0 ? plan.joints : a.num_seqs * cp.segs);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_fp4_combine_kernel<D>, cp);
+  const dim3 grid(sp.group < plan.rows ? sp.group : plan.rows, plan.joints > 0 ? plan.joints : a.num_seqs * cp.segs);
+  return launch_overlapped(decode_fp4_combine_kernel<D>, grid, kMergeThreads, 0, stream, 1, cp);
 }
 
 }  // namespace

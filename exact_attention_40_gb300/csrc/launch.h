@@ -25,6 +25,29 @@ inline int device_sm_count() {
   return n;
 }
 
+// Launches a kernel that may take its place on the SMs while the one before it on the
+// stream ends (programmatic dependent launch): it calls dependency_sync() before
+// it reads or writes any tensor.  `cluster`: CTAs of a cluster.
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                              int cluster, const Args&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Raises `func`'s dynamic shared-memory limit to `bytes` once per device:
 // `done` is the calling launcher's own per-device record of the value set
 // (callers racing on a device's first launch set the same attribute).

@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kTileThreads, 4) rope_axes_kernel(const RopeAx
     cp_async_commit();
     next += step;
   };
+  dependency_sync();
 #pragma unroll
   for (int s = 0; s < kRopeStages - 1; ++s) fetch(s);
   tile_angles(cs, table, half, count, [&](int at, int axis) {
@@ -265,6 +266,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) rope_cache_fp4_kernel(const R
     cp_async_commit();
     next += step;
   };
+  dependency_sync();
 #pragma unroll
   for (int s = 0; s < kFp4Stages - 1; ++s) fetch(s);
   int off = 0;
@@ -361,6 +363,7 @@ __global__ void __launch_bounds__(kTileThreads, 6) cache_read_fp4_kernel(const R
   const int j = threadIdx.x % kPerTok, rest = threadIdx.x / kPerTok;
   const int tok = rest % tile.toks, lane = rest / tile.toks;
   const long long n = static_cast<long long>(blockIdx.x) * tile.toks + tok;
+  dependency_sync();
   if (lane >= tile.lanes || n >= a.at.num_tokens) return;
   int off;
   const long long blk = find_block(a.at, n, &off);
@@ -435,33 +438,25 @@ cudaError_t launch_rope_axes(const RopeAxesArgs& a, const RopeAxesTable& table, 
   if (sms <= 0) return cudaErrorInvalidDevice;
   const long long tokens = static_cast<long long>(a.B) * a.N;
   const Tile t = make_tile(a.d, tokens, a.Hq + a.Hkv, kRopeLanes, sms);
-  rope_axes_kernel<<<tiles(t, tokens), kTileThreads, RowRing<kRopeStages>::kBytes + sizeof(float2) * t.toks * (a.d / 2), stream>>>(a, table, t);
-  return cudaGetLastError();
+  const size_t smem = RowRing<kRopeStages>::kBytes + sizeof(float2) * t.toks * (a.d / 2);
+  return launch_overlapped(rope_axes_kernel, tiles(t, tokens), kTileThreads, smem, stream, 1, a, table, t);
 }
 
 cudaError_t launch_rope_cache_write_fp4(const RopeFp4Args& a, const RopeAxesTable& table, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   const Tile t = make_tile(a.d, a.at.num_tokens, a.Hq + 2 * a.Hkv, kFp4Lanes, sms);
-  const unsigned int grid = tiles(t, a.at.num_tokens);
   const size_t smem = RowRing<kFp4Stages>::kBytes + sizeof(float2) * t.toks * (a.d / 2);
-  if (a.d == 64)
-    rope_cache_fp4_kernel<64><<<grid, kTileThreads, smem, stream>>>(a, table, t);
-  else
-    rope_cache_fp4_kernel<128><<<grid, kTileThreads, smem, stream>>>(a, table, t);
-  return cudaGetLastError();
+  return launch_overlapped(a.d == 64 ? rope_cache_fp4_kernel<64> : rope_cache_fp4_kernel<128>,
+                           tiles(t, a.at.num_tokens), kTileThreads, smem, stream, 1, a, table, t);
 }
 
 cudaError_t launch_cache_read_fp4(const ReadFp4Args& a, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   const Tile t = make_tile(a.d, a.at.num_tokens, 2 * a.Hkv, kFp4Lanes, sms);
-  const unsigned int grid = tiles(t, a.at.num_tokens);
-  if (a.d == 64)
-    cache_read_fp4_kernel<64><<<grid, kTileThreads, 0, stream>>>(a, t);
-  else
-    cache_read_fp4_kernel<128><<<grid, kTileThreads, 0, stream>>>(a, t);
-  return cudaGetLastError();
+  return launch_overlapped(a.d == 64 ? cache_read_fp4_kernel<64> : cache_read_fp4_kernel<128>,
+                           tiles(t, a.at.num_tokens), kTileThreads, 0, stream, 1, a, t);
 }
 
 }  // namespace exattn
