@@ -298,7 +298,8 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
     }
     fence_mbar_init();
   }
-  dependency_sync();  // (the merge may launch and wait while this runs)
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();  // the merge may launch and wait while this runs
   const int max_ctx = p.max_blocks_per_seq * kBlk;
   auto ctx_of = [&](int s) { return clamp_ctx(__ldg(p.ctx_lens + s), max_ctx, p.status); };
   // Queries as B fragments: column g = query head hq0 + 8 nt + g; step ks,
@@ -898,7 +899,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp4_combine_kernel(const
     }
     __syncthreads();
   }
-  dependency_sync();  // launched while the split kernel runs, which has begun after all before it ended
+  cudaGridDependencySynchronize();  // launched while the split kernel runs, after all before that had ended
   const Fp4Joint joint = p.joints != nullptr ? p.joints[blockIdx.y] : found;
   if (joint.more == 0 || r >= joint.rows) return;
   const int used = joint.more + 1;

@@ -391,15 +391,6 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
-// Waits until the kernels before this one on the stream have ended and their results can
-// be seen, then lets the next one take its place on the SMs that this grid leaves
-// free.  (In that order: a kernel that is let in early may rely on everything
-// before this one.)
-__device__ __forceinline__ void dependency_sync() {
-  cudaGridDependencySynchronize();
-  cudaTriggerProgrammaticLaunchCompletion();
-}
-
 // ---------------------------------------------------------------- cp.async
 // Per-thread asynchronous copies global -> shared; with valid false nothing
 // is read and the destination is zero-filled.  A thread sees its own copies

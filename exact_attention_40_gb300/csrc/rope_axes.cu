@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kTileThreads, 4) rope_axes_kernel(const RopeAx
     cp_async_commit();
     next += step;
   };
-  dependency_sync();
+  cudaGridDependencySynchronize();
 #pragma unroll
   for (int s = 0; s < kRopeStages - 1; ++s) fetch(s);
   tile_angles(cs, table, half, count, [&](int at, int axis) {
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) rope_cache_fp4_kernel(const R
     cp_async_commit();
     next += step;
   };
-  dependency_sync();
+  cudaGridDependencySynchronize();
 #pragma unroll
   for (int s = 0; s < kFp4Stages - 1; ++s) fetch(s);
   int off = 0;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kTileThreads, 6) cache_read_fp4_kernel(const R
   const int j = threadIdx.x % kPerTok, rest = threadIdx.x / kPerTok;
   const int tok = rest % tile.toks, lane = rest / tile.toks;
   const long long n = static_cast<long long>(blockIdx.x) * tile.toks + tok;
-  dependency_sync();
+  cudaGridDependencySynchronize();
   if (lane >= tile.lanes || n >= a.at.num_tokens) return;
   int off;
   const long long blk = find_block(a.at, n, &off);

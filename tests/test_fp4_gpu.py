@@ -631,6 +631,58 @@ def test_workspace_of_a_call_on_another_stream_is_not_reused_while_it_runs(env):
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
 
 
+@pytest.mark.parametrize("S,ctx,Hq,Hkv", [(5, 3000, 8, 2), (40, 900, 8, 4), (2, 300, 4, 2)])
+def test_calls_that_follow_each_other_wait_for_what_they_use(env, S, ctx, Hq, Hkv):
+    """Each call may begin while the one before it ends, so each has to wait for what it
+    reads (queries, lengths, the cache) and overwrites (the next step turns the same
+    tensors in place): the same bits with and without a synchronisation after every
+    call, and from a replayed graph."""
+    torch, ex, dev = env
+    d, steps = 128, 6
+    blocks = (ctx + steps + 15) // 16
+    table = torch.arange(S * blocks, device=dev, dtype=torch.int32).view(S, blocks)
+    seq = torch.arange(S, device=dev, dtype=torch.int32)
+    lens = [torch.tensor([ctx - 3 * i + step for i in range(S)], device=dev, dtype=torch.int32)
+            for step in range(steps + 1)]
+    start = ex.attn_fp4_cache(S * blocks, Hkv, d)
+    kv = to_dev(synth.normal_bf16(576, 1, (S * ctx, Hkv, d)), dev)
+    every = seq.repeat_interleave(ctx)
+    place = torch.arange(ctx, device=dev, dtype=torch.int32).repeat(S)
+    ex.attn_rope_cache_write_fp4(kv[:, :0], kv, kv, every, place, place[None], table, start, (64,))
+    q0 = to_dev(synth.normal_bf16(576, 2, (S, Hq, d)), dev)
+    q, x, cache = q0.clone(), q0.clone(), start.clone()
+    seen = torch.empty(steps, S, Hq, d, device=dev, dtype=torch.bfloat16)
+    back = torch.empty(steps, S, Hkv, d, device=dev, dtype=torch.bfloat16)
+
+    def run(after):
+        x.copy_(q0), cache.copy_(start), after()
+        for i in range(steps):
+            at = lens[i]
+            ex.attn_rope_cache_write_fp4(x, x[:, :Hkv], x[:, Hq - Hkv:], seq, at, at[None], table, cache, (64,),
+                                         q_out=q), after()
+            ex.attn_decode_paged_fp4(q, cache, table, lens[i + 1], out=seen[i]), after()
+            ex.attn_rope_axes(q[None].transpose(1, 2), q[None, :, :0].transpose(1, 2), at[None], (64,), inverse=True,
+                              q_out=q[None].transpose(1, 2)), after()
+            ex.attn_decode_paged_fp4(q, cache, table, lens[i + 1], out=x), after()
+            ex.attn_cache_read_fp4(cache, seq, at, table, k_out=back[i]), after()
+
+    run(torch.cuda.synchronize)
+    want, want_back, want_cache = seen.clone(), back.clone(), cache.clone()
+    assert torch.isfinite(want.float()).all() and want.float().abs().max() > 0
+    for _ in range(10):
+        seen.zero_(), back.zero_()
+        run(lambda: None)
+        assert torch.equal(seen, want) and torch.equal(back, want_back) and torch.equal(cache, want_cache)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(lambda: None)
+    for _ in range(3):
+        seen.zero_(), back.zero_()
+        g.replay()
+        assert torch.equal(seen, want) and torch.equal(back, want_back) and torch.equal(cache, want_cache)
+    assert ex.attn_get_device_status() == 0
+
+
 def test_append_captured_and_replayed(env):
     torch, ex, dev = env
     d, Hkv = 128, 2
