@@ -246,3 +246,37 @@ def test_training_step_over_rotated_heads(env):
     for name, got, leaf in zip(("dq", "dk", "dv"), (dq, dk, dv), leaves):
         rel = ((got.double() - leaf.grad).norm() / leaf.grad.norm()).item()
         assert rel <= 2e-2, "%s: %.3e" % (name, rel)
+
+
+@pytest.mark.parametrize("Hq,Hkv,Nq,Nk", [(4, 4, 1500, 1500), (8, 2, 1000, 1000), (2, 2, 70, 4000), (2, 2, 3000, 100)])
+def test_gradients_are_whole_when_they_are_turned_back(env, Hq, Hkv, Nq, Nk):
+    """The turn may start while the backward's last kernel ends, whose own
+    predecessor may still be running then: the same bits as with a synchronisation
+    between the two."""
+    torch, ex, dev = env
+    q = to_dev(synth.normal_bf16(320, 1, (2, Hq, Nq, 128)), dev)
+    k = to_dev(synth.normal_bf16(320, 2, (2, Hkv, Nk, 128)), dev)
+    v = to_dev(synth.normal_bf16(320, 3, (2, Hkv, Nk, 128)), dev)
+    do = to_dev(synth.normal_bf16(320, 4, (2, Hq, Nq, 128)), dev)
+    pq = torch.arange(Nk - Nq, Nk, device=dev, dtype=torch.int32)[None]
+    pk = torch.arange(Nk, device=dev, dtype=torch.int32)[None]
+    out, lse = ex.attn_fwd(q, k, v, causal=True)
+    none_q, none_k = q[:, :0], k[:, :0]
+
+    def step(between):
+        dq, dk, dv = ex.attn_bwd(q, k, v, out, do, lse, causal=True)
+        between()
+        ex.attn_rope_axes(dq, none_q, pq, (64,), inverse=True, q_out=dq)
+        between()
+        ex.attn_rope_axes(none_k, dk, pk, (64,), inverse=True, k_out=dk)
+        between()
+        return dq, dk, dv
+
+    want = step(torch.cuda.synchronize)
+    assert want[0].float().abs().max() > 0
+    for _ in range(10):
+        got = [step(lambda: None) for _ in range(3)]
+        for g in got:
+            for a, b in zip(g, want):
+                assert torch.equal(a, b)
+    assert ex.attn_get_device_status() == 0
