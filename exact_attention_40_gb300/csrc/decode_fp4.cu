@@ -156,49 +156,78 @@ __device__ __forceinline__ void compute_barrier() {
   asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
 
-// Equal contiguous shares of `total` units for `parts` CTAs, the first
+// Equal contiguous shares of `total` places for `parts` CTAs, the first
 // total % parts of them one larger.  (The host keeps totals below 2^31.)
 struct Shares {
   int base, extra;
   __device__ __forceinline__ Shares(int total, int parts) : base(total / parts), extra(total % parts) {}
   __device__ __forceinline__ int begin(int c) const { return c * base + min(c, extra); }
-  __device__ __forceinline__ int owner(int unit) const {
+  __device__ __forceinline__ int owner(int place) const {
     const int large = extra * (base + 1);
-    return unit < large ? unit / (base + 1) : extra + (unit - large) / base;
+    return place < large ? place / (base + 1) : extra + (place - large) / base;
   }
 };
 
-// A place in the numbered units: unit k of `units` of segment (seq, y).
+// A place in the numbering of all segments: unit k of `units` of segment (seq, y), or
+// (k == units) the place that stands for the segment's end.
 struct Place {
   int seq, y, k, units, ctx;
 };
 
 __device__ __forceinline__ int units_of(int ctx) { return (ctx + kUnit * kBlk - 1) / (kUnit * kBlk); }
 
-// Sums over the sequences that a warp forms from ctx_lens, each lane holding a
-// contiguous range of them.
+// Places of a segment: its units and one for its end, whose merge and change of
+// queries take a CTA 2400 cycles, about what a unit does (2100).  (With units alone the
+// CTAs that got the short sequences of a batch were the last to finish: 128 sequences
+// of 1 to 2000 tokens took 45.8 us, 38.4 with the ends counted.)
+__device__ __forceinline__ int places_of(int ctx) { return units_of(ctx) + (ctx > 0 ? 1 : 0); }
+
+// Sums over the sequences that a warp forms from ctx_lens, each lane holding those of a
+// contiguous range of them.  In a large batch the warp reads 32 neighbours together: with
+// every lane reading its own range, no two of a load's addresses share a line, and 4096
+// sequences took each CTA 40 us before its first copy.
 struct Batch {
   const int32_t* ctx_lens;
   int max_ctx, num_seqs;
-  int lane_begin, before, mine;  // this lane's first sequence, the units before it, in its range
-  int first_ctx;                 // of its first sequence
-  int per_segment;               // units of all sequences (of one segment of each)
+  int range;                     // sequences per lane; a multiple of 32 where the warp reads them together
+  int lane_begin, before, mine;  // this lane's first sequence, the places before it, in its range
+  int first_ctx;                 // of its first sequence (small batches)
+  int per_segment;               // places of all sequences (of one segment of each)
+
+  static constexpr int kAlone = 4;  // longest range that a lane reads by itself
 
   // Clamped without a word: whoever handles the sequence reports it.
   __device__ __forceinline__ int ctx_of(int s) const { return max(0, min(max_ctx, __ldg(ctx_lens + s))); }
+  __device__ __forceinline__ int places_at(int s, int end) const { return s < end ? places_of(ctx_of(s)) : 0; }
 
   __device__ __forceinline__ Batch(const int32_t* lens, int seqs, int longest) {
     ctx_lens = lens;
     num_seqs = seqs;
     max_ctx = longest;
     const int lane = threadIdx.x & 31;
-    const int range = (seqs + 31) / 32;
+    const bool alone = seqs <= 32 * kAlone;
+    range = alone ? (seqs + 31) / 32 : (seqs + 1023) / 1024 * 32;
     lane_begin = min(seqs, lane * range);
-    const int end = min(seqs, lane_begin + range);
-    first_ctx = lane_begin < end ? ctx_of(lane_begin) : 0;
-    mine = units_of(first_ctx);
+    first_ctx = mine = 0;
+    if (alone) {
+      const int end = min(seqs, lane_begin + range);
+      if (lane_begin < end) first_ctx = ctx_of(lane_begin);
+      mine = places_of(first_ctx);
+#pragma unroll
+      for (int i = 1; i < kAlone; ++i) mine += places_at(lane_begin + i, end);
+    } else {
+      const int groups = (seqs + 31) / 32, per_lane = range / 32;
+      int owner = 0, left = per_lane;
 #pragma unroll 8
-    for (int s = lane_begin + 1; s < end; ++s) mine += units_of(ctx_of(s));
+      for (int i = 0; i < groups; ++i) {
+        const int sum = __reduce_add_sync(0xffffffffu, places_at(32 * i + lane, seqs));
+        if (lane == owner) mine += sum;
+        if (--left == 0) {
+          left = per_lane;
+          ++owner;
+        }
+      }
+    }
     int upto = mine;  // inclusive sum over the lanes
 #pragma unroll
     for (int x = 1; x < 32; x *= 2) {
@@ -209,35 +238,67 @@ struct Batch {
     before = upto - mine;
   }
 
-  // The place of a unit (below per_segment * segs); whole warp, same unit.
-  __device__ __forceinline__ Place find(int unit, int segs) const {
-    const int target = unit / segs;
+  // The unit or end at a place (below per_segment * segs); whole warp, same place.
+  __device__ __forceinline__ Place find(int place, int segs) const {
+    const int target = place / segs;
     const unsigned int owners = __ballot_sync(0xffffffffu, before <= target && target < before + mine);
     const int lane = __ffs(owners) - 1;
-    int s = lane_begin, prefix = before, ctx = first_ctx;
-    if ((threadIdx.x & 31) == lane)
-      while (target >= prefix + units_of(ctx)) {
-        prefix += units_of(ctx);
-        ctx = ctx_of(++s);
-      }
     Place p;
-    p.seq = __shfl_sync(0xffffffffu, s, lane);
-    p.ctx = __shfl_sync(0xffffffffu, ctx, lane);
-    prefix = __shfl_sync(0xffffffffu, prefix, lane);
+    int prefix;
+    if (num_seqs <= 32 * kAlone) {
+      int s = lane_begin, ctx = first_ctx;
+      prefix = before;
+      if ((threadIdx.x & 31) == lane)
+        while (target >= prefix + places_of(ctx)) {
+          prefix += places_of(ctx);
+          ctx = ctx_of(++s);
+        }
+      p.seq = __shfl_sync(0xffffffffu, s, lane);
+      p.ctx = __shfl_sync(0xffffffffu, ctx, lane);
+      prefix = __shfl_sync(0xffffffffu, prefix, lane);
+    } else {
+      const int end = min(num_seqs, (lane + 1) * range);
+      int base = lane * range;
+      prefix = __shfl_sync(0xffffffffu, before, lane);
+      while (true) {  // 32 sequences at a time; one of the range has the place
+        const int n = places_at(base + (threadIdx.x & 31), end);
+        int upto = n;
+#pragma unroll
+        for (int x = 1; x < 32; x *= 2) {
+          const int v = __shfl_up_sync(0xffffffffu, upto, x);
+          if ((threadIdx.x & 31) >= x) upto += v;
+        }
+        const unsigned int past = __ballot_sync(0xffffffffu, target < prefix + upto);
+        if (past != 0 || base + 32 >= end) {
+          const int at = past != 0 ? __ffs(past) - 1 : 0;
+          prefix += __shfl_sync(0xffffffffu, upto - n, at);
+          p.seq = base + at;
+          break;
+        }
+        prefix += __shfl_sync(0xffffffffu, upto, 31);
+        base += 32;
+      }
+      p.ctx = ctx_of(p.seq);
+    }
     p.units = units_of(p.ctx);
-    const int rest = unit - prefix * segs;
-    p.y = rest / p.units;
-    p.k = rest - p.y * p.units;
+    const int places = max(1, places_of(p.ctx)), rest = place - prefix * segs;
+    p.y = rest / places;
+    p.k = rest - p.y * places;
     return p;
   }
 
-  // The units before a sequence, per segment; whole warp, same s.
+  // The places before a sequence, per segment; whole warp, same s.
   __device__ __forceinline__ int before_seq(int s) const {
-    const int range = (num_seqs + 31) / 32, lane = s / range;
+    const int lane = s / range;
     int prefix = before, ctx = first_ctx;
-    if ((threadIdx.x & 31) == lane)
-      for (int i = lane_begin; i < s; ctx = ctx_of(++i)) prefix += units_of(ctx);
-    return __shfl_sync(0xffffffffu, prefix, lane);
+    if (num_seqs <= 32 * kAlone) {
+      if ((threadIdx.x & 31) == lane)
+        for (int i = lane_begin; i < s; ctx = ctx_of(++i)) prefix += places_of(ctx);
+      return __shfl_sync(0xffffffffu, prefix, lane);
+    }
+    int sum = 0;
+    for (int i = lane * range + (threadIdx.x & 31); i < s; i += 32) sum += places_of(ctx_of(i));
+    return __shfl_sync(0xffffffffu, prefix, lane) + __reduce_add_sync(0xffffffffu, sum);
   }
 };
 
@@ -322,7 +383,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
     }
   };
   Place at;             // the next unit to compute
-  int left;             // units of this CTA
+  int left;             // units (in a cluster) or places of this CTA that are not yet computed
   int joint_parts = 0;  // CTAs after this one that its last segment goes on in
   const uint32_t rank = kCluster ? cta % kFp4ClusterCtas : 0;
   // Sequences without a cached token: o = 0, lse = -inf.  A lane looks at one, the
@@ -341,6 +402,15 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
         __syncwarp();
       }
     }
+  };
+  auto next_segment = [&](Place& x) {  // the following segment that has units
+    x.k = 0;
+    if (++x.y < segs) return;
+    x.y = 0;
+    do {
+      x.ctx = ctx_of(++x.seq);
+    } while (x.ctx == 0);
+    x.units = units_of(x.ctx);
   };
   const bool copies = warp == kWarps;
   int phys_lane = -1;  // of the copying warp: physical block of block lane % 8 of a batch's unit lane / 8; -1: none
@@ -378,21 +448,19 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
       return;
     }
     at = seqs.find(begin, segs);
+    if (at.k == at.units) {  // the end of a segment that others compute
+      if (--left == 0) {
+        clear_empty();
+        return;
+      }
+      next_segment(at);
+    }
     if (!copies) load_queries(at);
     if (p.joints != nullptr) {
       const Place last = seqs.find(begin_next - 1, segs);
       joint_parts = shares.owner(begin_next - 1 + last.units - 1 - last.k) - cta;
     }
   }
-  auto next_segment = [&](Place& x) {  // the following segment that has units
-    x.k = 0;
-    if (++x.y < segs) return;
-    x.y = 0;
-    do {
-      x.ctx = ctx_of(++x.seq);
-    } while (x.ctx == 0);
-    x.units = units_of(x.ctx);
-  };
 
   __syncthreads();  // the barriers are set up
 
@@ -403,7 +471,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
     const uint64_t stream_policy = l2_policy_evict_first();
     const uint32_t blk_bytes = static_cast<uint32_t>(p.Hkv) * Span::kBytes;
     Place to = at;
-    int to_load = left;  // units whose table entries are not yet asked for
+    int to_load = left;  // places whose table entries are not yet asked for
     // A batch: up to four units of one segment; lane 8 i + b has unit i's block b.
     struct Entries {
       int units, raw;  // raw: this lane's table entry, if it has one (`mine`)
@@ -428,6 +496,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
       e.head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;
       to.k += e.units;
       to_load -= e.units;
+      if (to.k == to.units && to_load > 0) --to_load;
       return e;
     };
     Entries now, next;  // the entries of the next batch are on their way while this one's blocks are copied
@@ -436,15 +505,18 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
                     p.cache + static_cast<size_t>(at.y / p.n_chunks) * Span::kBytes};
     else
       next = load_batch();
-    int batch_at = kCluster ? 0 : 4;
-    if (!kCluster) now.units = 4;
+    bool more = !kCluster;  // `next` holds a batch
+    if (!kCluster) now.units = 0;
+    int batch_at = 0;
     int i = 0;
     int st = 0;
     uint32_t parity = 1;  // of the stage's last use; the first round waits for none
 #pragma unroll 1
-    for (; i < left; ++i) {
-      if (!kCluster && batch_at == now.units) {
+    for (;; ++i) {
+      if (batch_at == now.units) {
+        if (!more) break;
         now = next;
+        more = false;
         batch_at = 0;
         phys_lane = now.mine ? check(now.raw) : -1;
       }
@@ -465,7 +537,10 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
                          Span::kBytes, &sm.full[st], stream_policy);
         }
       }
-      if (!kCluster && batch_at == 0 && to_load > 0) next = load_batch();
+      if (!kCluster && batch_at == 0 && to_load > 0) {
+        next = load_batch();
+        more = true;
+      }
       ++batch_at;
       now.past -= kStep * kUnit * kBlk;
       if (++st == kStages) {
@@ -766,6 +841,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
                 make_float4(acc[mt][nt][j], acc[mt][nt][2 + j], acc[mt + 1][nt][j], acc[mt + 1][nt][2 + j]);
       }
     left -= n_units;
+    if (!kCluster && ends && left > 0) --left;
     if (left > 0) {  // the next segment's queries arrive during the merge
       next_segment(at);
       load_queries(at);
@@ -856,7 +932,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
 }
 
 struct Fp4CombineParams {
-  const Fp4Joint* joints;  // one per CTA of the split kernel, or NULL: one CTA row per segment
+  const Fp4Joint* joints;  // one per CTA of the split kernel, or NULL (kFind): one CTA row per segment
   const int32_t* ctx_lens;
   const float* ws_o;
   const float* ws_lse;
@@ -869,12 +945,16 @@ struct Fp4CombineParams {
 // One CTA per (row, segment that several CTAs share): its partial outputs O_i
 // lie in the second place of the CTA where it starts and the first places of
 // the `more` that follow; L = log sum_i exp(lse_i), o = sum_i exp(lse_i - L) O_i.
-// Where segments are few it finds them from ctx_lens, while the split kernel still
-// runs; else it reads what that wrote down.  The weights are formed once, one
+// Where segments are few (kFind) it finds them from ctx_lens, while the split kernel
+// still runs; else it reads what that wrote down.  Registers: with 40, not 64, where it
+// reads (64 sequences of 512 to 8192 tokens 62.7 us, 63.7); with 48 where it finds: 66
+// would leave it no room beside a split kernel for 16 heads (32 sequences of 96 heads
+// 59.7 us, 55.4 with 48), and fewer slow the search (one of 8000 tokens 8.4 us with 66,
+// 8.8 with 48, 9.1 with 40).  The weights are formed once, one
 // per thread; D/4 threads take four columns each of every kTeams-th partial output,
 // the first ones' loads on their way before the weights are known.
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) decode_fp4_combine_kernel(const Fp4CombineParams p) {
+template <int D, bool kFind>
+__global__ void __launch_bounds__(kMergeThreads, kFind ? 5 : 6) decode_fp4_combine_kernel(const Fp4CombineParams p) {
   constexpr int kTeams = kMergeThreads / (D / 4);
   constexpr int kMergeWarps = kMergeThreads / 32;
   constexpr int kEarly = 3;
@@ -883,13 +963,13 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp4_combine_kernel(const
   __shared__ float4 part[kTeams][D / 4];
   __shared__ Fp4Joint found;
   const int r = blockIdx.x;
-  if (p.joints == nullptr) {
+  if constexpr (kFind) {
     if (threadIdx.x < 32) {
       const Batch seqs(p.ctx_lens, p.num_seqs, p.max_blocks_per_seq * kBlk);
       const Shares shares(seqs.per_segment * p.segs, p.ctas);
       const int seq = blockIdx.y / p.segs, y = blockIdx.y % p.segs;
-      const int units = units_of(seqs.ctx_of(seq));
-      const int unit = seqs.before_seq(seq) * p.segs + y * units;
+      const int ctx = seqs.ctx_of(seq), units = units_of(ctx);
+      const int unit = seqs.before_seq(seq) * p.segs + y * places_of(ctx);  // the place of its first
       if (threadIdx.x == 0) {
         found.cta = units > 0 ? shares.owner(unit) : 0;
         found.more = units > 0 ? shares.owner(unit + units - 1) - found.cta : 0;
@@ -900,7 +980,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp4_combine_kernel(const
     __syncthreads();
   }
   cudaGridDependencySynchronize();  // launched while the split kernel runs, after all before that had ended
-  const Fp4Joint joint = p.joints != nullptr ? p.joints[blockIdx.y] : found;
+  const Fp4Joint joint = kFind ? found : p.joints[blockIdx.y];
   if (joint.more == 0 || r >= joint.rows) return;
   const int used = joint.more + 1;
   auto place = [&](int i) { return static_cast<size_t>(2 * (joint.cta + i) + (i == 0 ? 1 : 0)) * p.rows + r; };
@@ -1027,7 +1107,8 @@ cudaError_t launch_d(const DecodeFp4Args& a, const DeviceGuard& g, cudaStream_t 
   cp.ctas = plan.ctas;
   cp.rows = plan.rows;
   const dim3 grid(sp.group < plan.rows ? sp.group : plan.rows, plan.joints > 0 ? plan.joints : a.num_seqs * cp.segs);
-  return launch_overlapped(decode_fp4_combine_kernel<D>, grid, kMergeThreads, 0, stream, 1, cp);
+  return launch_overlapped(plan.joints > 0 ? decode_fp4_combine_kernel<D, false> : decode_fp4_combine_kernel<D, true>,
+                           grid, kMergeThreads, 0, stream, 1, cp);
 }
 
 }  // namespace

@@ -229,24 +229,27 @@ struct Fp4Joint {
 struct Fp4Plan {
   int rows;               // query heads per segment: 8 columns of an mma, or 16 for larger groups
   int chunks;             // segments per KV head
-  int ctas;               // shares: one wave, but no more than there can be units
+  int ctas;               // shares: one wave, but no more than there can be places
   int joints;             // entries of the list of shared segments; 0 where the merge finds them itself
   bool cluster;           // a cluster of CTAs for each segment
   bool shared;            // whether a segment's partial outputs can lie in several CTAs' workspace
-  bool fits;              // the units' numbers fit 32 bits
+  bool fits;              // the numbers of the work's places fit 32 bits
   Fp4Plan(int num_seqs, int Hkv, int group, int max_blocks_per_seq) {
     rows = group <= 8 ? 8 : 16;
     chunks = (group + rows - 1) / rows;
     const long long segments = static_cast<long long>(num_seqs) * Hkv * chunks;
     const long long units = segments * ((max_blocks_per_seq + kFp4UnitBlocks - 1) / kFp4UnitBlocks);
     const int wave = kFp4Sms * fp4_decode_ctas(rows);
-    ctas = static_cast<int>(units < wave ? units : wave);
     const bool split = units > segments;
+    // (with a place more for each segment's end, which a CTA may get alone, where that
+    // leaves every other CTA a single unit)
+    const long long shares = split ? units + segments : units;
+    ctas = static_cast<int>(shares < wave ? shares : wave);
     cluster = split && segments * kFp4ClusterCtas <= wave && units <= segments * kFp4ClusterUnits;
     if (cluster) ctas = static_cast<int>(segments * kFp4ClusterCtas);
     shared = split && !cluster;
     joints = shared && segments > ctas ? ctas : 0;
-    fits = units <= 0x7FFFFFFF;
+    fits = units + segments <= 0x7FFFFFFF;  // the places of units and of segments' ends
   }
   size_t joint_bytes() const { return sizeof(Fp4Joint) * joints; }
   size_t part_bytes(int d) const { return sizeof(float) * 2 * ctas * rows * d; }

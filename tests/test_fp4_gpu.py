@@ -88,7 +88,8 @@ def test_decode_head_layouts(env, d, Hq, Hkv):
     run_decode(env, decode_case(401, [200, 1, 47], Hq, Hkv, d, k_scale=0.5, v_scale=0.01), d, k_scale=0.5, v_scale=0.01)
 
 
-@pytest.mark.parametrize("S,Hq,Hkv,hi", [(40, 4, 2, 5000), (160, 8, 4, 600), (700, 2, 1, 40), (130, 24, 2, 300)])
+@pytest.mark.parametrize("S,Hq,Hkv,hi", [(40, 4, 2, 5000), (160, 8, 4, 600), (700, 2, 1, 40), (130, 24, 2, 300),
+                                         (129, 2, 1, 3000), (400, 3, 1, 1500), (1100, 4, 2, 280), (2100, 1, 1, 200)])
 def test_decode_many_sequences(env, S, Hq, Hkv, hi):
     """Ragged batches, empty sequences among them: shares that end inside sequences,
     shares of many sequences, more segments than CTAs, and no segment of two units."""
