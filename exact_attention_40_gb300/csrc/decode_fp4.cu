@@ -168,10 +168,10 @@ struct Shares {
   }
 };
 
-// A place in the numbering of all segments: unit k of `units` of segment (seq, y), or
-// (k == units) the place that stands for the segment's end.
+// A place in the numbering of all segments: unit k of `units` of segment (seq, head,
+// chunk), or (k == units) the place that stands for the segment's end.
 struct Place {
-  int seq, y, k, units, ctx;
+  int seq, head, chunk, k, units, ctx;
 };
 
 __device__ __forceinline__ int units_of(int ctx) { return (ctx + kUnit * kBlk - 1) / (kUnit * kBlk); }
@@ -239,7 +239,7 @@ struct Batch {
   }
 
   // The unit or end at a place (below per_segment * segs); whole warp, same place.
-  __device__ __forceinline__ Place find(int place, int segs) const {
+  __device__ __forceinline__ Place find(int place, int segs, int n_chunks) const {
     const int target = place / segs;
     const unsigned int owners = __ballot_sync(0xffffffffu, before <= target && target < before + mine);
     const int lane = __ffs(owners) - 1;
@@ -282,8 +282,10 @@ struct Batch {
     }
     p.units = units_of(p.ctx);
     const int places = max(1, places_of(p.ctx)), rest = place - prefix * segs;
-    p.y = rest / places;
-    p.k = rest - p.y * places;
+    const int y = rest / places;
+    p.k = rest - y * places;
+    p.head = n_chunks == 1 ? y : y / n_chunks;
+    p.chunk = y - p.head * n_chunks;
     return p;
   }
 
@@ -367,9 +369,13 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
   // indices 2t, 2t + 1 and 2t + 8, 2t + 9 = columns (D/4) t + 4 ks + 0..3, the
   // columns of the lane's own key codes.
   uint32_t qb[NT][kKSteps][2];
+  auto rows_of = [&](const Place& x) { return min(kRows, p.group - x.chunk * kRows); };
+  auto row_of = [&](const Place& x) {  // first row of the queries and the output
+    return static_cast<size_t>(x.seq) * p.Hq + x.head * p.group + x.chunk * kRows;
+  };
   auto load_queries = [&](const Place& x) {
-    const int rows = min(kRows, p.group - x.y % p.n_chunks * kRows);
-    const size_t row0 = static_cast<size_t>(x.seq) * p.Hq + x.y / p.n_chunks * p.group + x.y % p.n_chunks * kRows;
+    const int rows = rows_of(x);
+    const size_t row0 = row_of(x);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const bool real = 8 * nt + g < rows;
@@ -384,7 +390,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
   };
   Place at;             // the next unit to compute
   int left;             // units (in a cluster) or places of this CTA that are not yet computed
-  int joint_parts = 0;  // CTAs after this one that its last segment goes on in
+  int joint_parts = 0;  // CTAs after this one that its last segment goes on in (warp 0)
   const uint32_t rank = kCluster ? cta % kFp4ClusterCtas : 0;
   // Sequences without a cached token: o = 0, lse = -inf.  A lane looks at one, the
   // warp clears what is found.  (Every sequence's length passes here once, so that
@@ -405,8 +411,10 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
   };
   auto next_segment = [&](Place& x) {  // the following segment that has units
     x.k = 0;
-    if (++x.y < segs) return;
-    x.y = 0;
+    if (++x.chunk < p.n_chunks) return;
+    x.chunk = 0;
+    if (++x.head < p.Hkv) return;
+    x.head = 0;
     do {
       x.ctx = ctx_of(++x.seq);
     } while (x.ctx == 0);
@@ -425,7 +433,8 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
     static_assert(kFp4ClusterUnits / kFp4ClusterCtas <= 32 / kUnit, "one batch of table entries");
     const int seg = cta / kFp4ClusterCtas;
     at.seq = seg / segs;
-    at.y = seg % segs;
+    at.head = seg % segs / p.n_chunks;
+    at.chunk = seg % p.n_chunks;
     at.k = rank;
     const int blk = (rank + kStep * (lane / kUnit)) * kUnit + lane % kUnit;
     const int entry = copies && blk < p.max_blocks_per_seq
@@ -447,7 +456,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
       clear_empty();
       return;
     }
-    at = seqs.find(begin, segs);
+    at = seqs.find(begin, segs, p.n_chunks);
     if (at.k == at.units) {  // the end of a segment that others compute
       if (--left == 0) {
         clear_empty();
@@ -456,8 +465,8 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
       next_segment(at);
     }
     if (!copies) load_queries(at);
-    if (p.joints != nullptr) {
-      const Place last = seqs.find(begin_next - 1, segs);
+    if (p.joints != nullptr && warp == 0) {
+      const Place last = seqs.find(begin_next - 1, segs, p.n_chunks);
       joint_parts = shares.owner(begin_next - 1 + last.units - 1 - last.k) - cta;
     }
   }
@@ -484,16 +493,15 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
       if (to.k == to.units) {
         next_segment(to);
         // its queries into the L1 cache, for the computing warps
-        const int rows = min(kRows, p.group - to.y % p.n_chunks * kRows);
-        const size_t row = static_cast<size_t>(to.seq) * p.Hq + to.y / p.n_chunks * p.group + to.y % p.n_chunks * kRows;
-        if (lane < rows * D / 64) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.q + row * D + lane * 64));
+        if (lane < rows_of(to) * D / 64)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(p.q + row_of(to) * D + lane * 64));
       }
       e.units = min(32 / kUnit, min(to.units - to.k, to_load));
       const int blk = to.k * kUnit + lane;
       e.mine = lane < e.units * kUnit && blk * kBlk < to.ctx;
       e.raw = e.mine ? __ldg(p.block_table + static_cast<size_t>(to.seq) * p.max_blocks_per_seq + blk) : -1;
       e.past = to.ctx - (to.k + 1) * kUnit * kBlk;
-      e.head = p.cache + static_cast<size_t>(to.y / p.n_chunks) * Span::kBytes;
+      e.head = p.cache + static_cast<size_t>(to.head) * Span::kBytes;
       to.k += e.units;
       to_load -= e.units;
       if (to.k == to.units && to_load > 0) --to_load;
@@ -502,7 +510,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
     Entries now, next;  // the entries of the next batch are on their way while this one's blocks are copied
     if constexpr (kCluster)
       now = Entries{left, phys_lane, phys_lane >= 0, at.ctx - (at.k + 1) * kUnit * kBlk,
-                    p.cache + static_cast<size_t>(at.y / p.n_chunks) * Span::kBytes};
+                    p.cache + static_cast<size_t>(at.head) * Span::kBytes};
     else
       next = load_batch();
     bool more = !kCluster;  // `next` holds a batch
@@ -592,8 +600,8 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
   int buf = 0;
 #pragma unroll 1
   while (left > 0) {  // segments of this CTA's share
-    const int rows_here = min(kRows, p.group - at.y % p.n_chunks * kRows);
-    const size_t row0 = static_cast<size_t>(at.seq) * p.Hq + at.y / p.n_chunks * p.group + at.y % p.n_chunks * kRows;
+    const int rows_here = rows_of(at);
+    const size_t row0 = row_of(at);
     const bool starts = at.k == 0;
     const int n_units = kCluster ? left : min(at.units - at.k, left);
     const bool ends = at.k + n_units == at.units;
@@ -893,8 +901,8 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
   __syncwarp();
   if constexpr (kCluster) {
     // ---- the cluster's CTAs merge: L = log sum_i exp(lse_i), o = sum_i exp(lse_i - L) O_i
-    const int rows_here = min(kRows, p.group - at.y % p.n_chunks * kRows);
-    const size_t row0 = static_cast<size_t>(at.seq) * p.Hq + at.y / p.n_chunks * p.group + at.y % p.n_chunks * kRows;
+    const int rows_here = rows_of(at);
+    const size_t row0 = row_of(at);
     cluster_barrier();
     for (int idx = threadIdx.x * kFp4ClusterCtas + rank; idx < rows_here * (D / 4); idx += kThreads * kFp4ClusterCtas) {
       const int r = idx / (D / 4), col = idx % (D / 4) * 4;
