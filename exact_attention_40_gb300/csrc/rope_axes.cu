@@ -34,6 +34,7 @@ constexpr int kRopeLanes = 8;
 constexpr int kRopeStages = 4;  // rows of a thread on their way, and the one at hand
 constexpr int kFp4Lanes = 4;
 constexpr int kFp4Stages = 5;
+constexpr int kReadLanes = 4;  // of the read
 
 // How a CTA's threads cover tokens and heads.
 struct Tile {
@@ -354,9 +355,13 @@ __global__ void __launch_bounds__(kTileThreads, 3) rope_cache_fp4_kernel(const R
 }
 
 // Read: thread j of a token takes group j of the keys and values of every head
-// it visits: rows 0 .. Hkv - 1 are keys, the next Hkv values.
+// it visits: rows 0 .. Hkv - 1 are keys, the next Hkv values.  Bound by its writes and
+// by the chain from a token's place through the block table to its codes, which many
+// small CTAs overlap best.  32,768 tokens of 8 heads of 128 (172 MB): 28.7 us = 6.0 TB/s;
+// 30.0 with six CTAs an SM instead of eight, 32.9 with 8 lanes, 34.8 with 1, and two
+// us more with each group stored as two vectors of 16 bytes, which touch a sector twice.
 template <int D>
-__global__ void __launch_bounds__(kTileThreads, 6) cache_read_fp4_kernel(const ReadFp4Args a, const Tile tile) {
+__global__ void __launch_bounds__(kTileThreads, 8) cache_read_fp4_kernel(const ReadFp4Args a, const Tile tile) {
   using Span = Fp4Span<D>;
   constexpr int kPerTok = D / 16;
   constexpr int kUnroll = 2;
@@ -401,8 +406,12 @@ __global__ void __launch_bounds__(kTileThreads, 6) cache_read_fp4_kernel(const R
         w[e] = pack_bf16x2(__fmul_rn(f16_lo(v), g), __fmul_rn(f16_hi(v), g));
       }
       uint4* dst = r >= a.Hkv ? v_out + (r - a.Hkv) * a.v_out.head : k_out + r * a.k_out.head;
-      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {  // (rows are on 16-byte boundaries)
+        st_global_v8(dst, w);
+      } else {
+        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
     }
   }
 }
@@ -454,7 +463,7 @@ cudaError_t launch_rope_cache_write_fp4(const RopeFp4Args& a, const RopeAxesTabl
 cudaError_t launch_cache_read_fp4(const ReadFp4Args& a, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const Tile t = make_tile(a.d, a.at.num_tokens, 2 * a.Hkv, kFp4Lanes, sms);
+  const Tile t = make_tile(a.d, a.at.num_tokens, 2 * a.Hkv, kReadLanes, sms);
   return launch_overlapped(a.d == 64 ? cache_read_fp4_kernel<64> : cache_read_fp4_kernel<128>,
                            tiles(t, a.at.num_tokens), kTileThreads, 0, stream, 1, a, t);
 }

@@ -516,6 +516,28 @@ def test_append_strided_in_place_and_read_into_views(env):
     assert torch.equal(c1, c2)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_read_onto_every_16_byte_boundary(env, d):
+    """Rows on 16-byte boundaries that are not 32-byte ones, or on both kinds in turn, and
+    nothing written between them."""
+    torch, ex, dev = env
+    T, Hkv = 37, 3
+    inp, slots, pos = append_case(531, [T], T, 1, Hkv, d)
+    idx = [to_dev(x, dev) for x in (inp["seq_ids"], slots)]
+    tbl = to_dev(inp["block_table"], dev)
+    cache = ex.attn_fp4_cache(inp["num_blocks"], Hkv, d)
+    t = [to_dev(inp[x], dev) for x in ("q", "k", "v")]
+    ex.attn_rope_cache_write_fp4(*t, *idx, to_dev(pos, dev), tbl, cache, (d // 2,))
+    want = ex.attn_cache_read_fp4(cache, *idx, tbl)
+    for gap, start in ((0, 8), (8, 0), (8, 8), (16, 8)):
+        room = torch.full((2, T * Hkv * (d + gap) + 32), 5.0, device=dev, dtype=torch.bfloat16)
+        outs = [x[start:start + T * Hkv * (d + gap)].view(T, Hkv, d + gap) for x in room]
+        ex.attn_cache_read_fp4(cache, *idx, tbl, k_out=outs[0][..., :d], v_out=outs[1][..., :d])
+        for x, w in zip(outs, want):
+            assert torch.equal(x[..., :d], w) and (x[..., d:] == 5).all()
+        assert (room[:, :start] == 5).all() and (room[:, start + T * Hkv * (d + gap):] == 5).all()
+
+
 # ------------------------------------------------------------------- together
 @pytest.mark.parametrize("d", [64, 128])
 def test_serving_run(env, d):
