@@ -4,7 +4,7 @@
 //
 // A serving step makes these calls with a handful of tokens, where the kernels take
 // a few microseconds; marshalling the same call through ctypes takes about 20
-// (attribute look-ups and 20 converted arguments), through here 6.  Arguments
+// (attribute look-ups and 20 converted arguments), through here 5.  Arguments
 // come positionally from the functions of exattn.py, which document them.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
