@@ -26,12 +26,17 @@
 //   in any order, so which column or token an mma index stands for is free: it
 //   is chosen so that a lane reads its codes as one vector each, from one or two
 //   scale groups.  Weights are rounded to fp16 for the second product, at most
-//   2^-12 relative (the output is rounded to bf16, 2^-9); their sums are fp32 and
+//   2^-11 relative (the output is rounded to bf16, 2^-8); their sums are fp32 and
 //   take them unrounded (a second sum, of the rounded weights, cost 1 to 2% of the
 //   time and changed no digit that bf16 keeps).
+//   What bounds it: conversions and the multiplications by the scales, which share a
+//   pipe (4 + 4 of them and one mma take 15 cycles of an SM's quarter, each of the
+//   three alone 8), then DRAM.  64 sequences of 8192 tokens, 32 heads over 8 of 128:
+//   105.8 us = 5.72 TB/s; the copies alone take 94.  64 sequences of 512 to 8192
+//   tokens with the merge 62.4 us = 5.16 TB/s.
 //   Small calls (few segments, none long) take a cluster of 8 CTAs for each
 //   segment instead, which take its units in turn and merge through distributed
-//   shared memory: one launch and no workspace.
+//   shared memory: one launch and no workspace (six of up to 1500 tokens 3.9 us).
 // decode_fp4_combine_kernel: merges the partial outputs of a segment.
 #include <cuda_bf16.h>
 
@@ -159,12 +164,13 @@ __device__ __forceinline__ void compute_barrier() {
 // Equal contiguous shares of `total` places for `parts` CTAs, the first
 // total % parts of them one larger.  (The host keeps totals below 2^31.)
 struct Shares {
-  int base, extra;
-  __device__ __forceinline__ Shares(int total, int parts) : base(total / parts), extra(total % parts) {}
+  int base, extra, parts;
+  __device__ __forceinline__ Shares(int total, int n) : base(total / n), extra(total % n), parts(n) {}
   __device__ __forceinline__ int begin(int c) const { return c * base + min(c, extra); }
   __device__ __forceinline__ int owner(int place) const {
     const int large = extra * (base + 1);
-    return place < large ? place / (base + 1) : extra + (place - large) / base;
+    const int c = place < large ? place / (base + 1) : extra + (place - large) / max(1, base);
+    return max(0, min(parts - 1, c));
   }
 };
 
@@ -185,7 +191,9 @@ __device__ __forceinline__ int places_of(int ctx) { return units_of(ctx) + (ctx 
 // Sums over the sequences that a warp forms from ctx_lens, each lane holding those of a
 // contiguous range of them.  In a large batch the warp reads 32 neighbours together: with
 // every lane reading its own range, no two of a load's addresses share a line, and 4096
-// sequences took each CTA 40 us before its first copy.
+// sequences took each CTA 40 us before its first copy.  (Lengths are read more than
+// once; if another stream changes them meanwhile the result is undefined, but every
+// place that comes out is clamped to one that exists.)
 struct Batch {
   const int32_t* ctx_lens;
   int max_ctx, num_seqs;
@@ -242,18 +250,18 @@ struct Batch {
   __device__ __forceinline__ Place find(int place, int segs, int n_chunks) const {
     const int target = place / segs;
     const unsigned int owners = __ballot_sync(0xffffffffu, before <= target && target < before + mine);
-    const int lane = __ffs(owners) - 1;
+    const int lane = max(0, __ffs(owners) - 1);
     Place p;
     int prefix;
     if (num_seqs <= 32 * kAlone) {
       int s = lane_begin, ctx = first_ctx;
       prefix = before;
       if ((threadIdx.x & 31) == lane)
-        while (target >= prefix + places_of(ctx)) {
+        while (target >= prefix + places_of(ctx) && s + 1 < num_seqs) {
           prefix += places_of(ctx);
           ctx = ctx_of(++s);
         }
-      p.seq = __shfl_sync(0xffffffffu, s, lane);
+      p.seq = min(num_seqs - 1, __shfl_sync(0xffffffffu, s, lane));
       p.ctx = __shfl_sync(0xffffffffu, ctx, lane);
       prefix = __shfl_sync(0xffffffffu, prefix, lane);
     } else {
@@ -272,7 +280,7 @@ struct Batch {
         if (past != 0 || base + 32 >= end) {
           const int at = past != 0 ? __ffs(past) - 1 : 0;
           prefix += __shfl_sync(0xffffffffu, upto - n, at);
-          p.seq = base + at;
+          p.seq = min(num_seqs - 1, base + at);
           break;
         }
         prefix += __shfl_sync(0xffffffffu, upto, 31);
@@ -280,10 +288,10 @@ struct Batch {
       }
       p.ctx = ctx_of(p.seq);
     }
-    p.units = units_of(p.ctx);
-    const int places = max(1, places_of(p.ctx)), rest = place - prefix * segs;
-    const int y = rest / places;
-    p.k = rest - y * places;
+    p.units = max(1, units_of(p.ctx));
+    const int rest = max(0, place - prefix * segs);
+    const int y = min(segs - 1, rest / (p.units + 1));
+    p.k = min(p.units, rest - y * (p.units + 1));
     p.head = n_chunks == 1 ? y : y / n_chunks;
     p.chunk = y - p.head * n_chunks;
     return p;
@@ -416,9 +424,10 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
     if (++x.head < p.Hkv) return;
     x.head = 0;
     do {
-      x.ctx = ctx_of(++x.seq);
-    } while (x.ctx == 0);
-    x.units = units_of(x.ctx);
+      x.seq = min(x.seq + 1, p.num_seqs - 1);
+      x.ctx = ctx_of(x.seq);
+    } while (x.ctx == 0 && x.seq < p.num_seqs - 1);
+    x.units = max(1, units_of(x.ctx));
   };
   const bool copies = warp == kWarps;
   int phys_lane = -1;  // of the copying warp: physical block of block lane % 8 of a batch's unit lane / 8; -1: none

@@ -12,7 +12,8 @@
 // owns the 8 pairs 8 j .. 8 j + 7 of every head it visits (two 16-byte loads,
 // two 16-byte stores), so its cosines and sines stay in registers; `lanes`
 // such sets of threads share the heads.  Its loads run three or four heads ahead,
-// through shared memory, and start before the angles are formed.
+// through shared memory, and start before the angles are formed.  Rates are at the
+// constants below and at the kernels.
 #include <cuda_bf16.h>
 
 #include "fp4.cuh"

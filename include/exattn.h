@@ -28,7 +28,11 @@
  *     (callers usually pass 1/sqrt(d)).
  *   - stream is a cudaStream_t (NULL = legacy default stream).  Every call
  *     is asynchronous on that stream: validation happens on the host before
- *     anything is enqueued; nothing synchronises.
+ *     anything is enqueued; nothing synchronises.  attn_rope_axes and the
+ *     calls of the 4-bit cache are programmatic dependent launches: they wait
+ *     for the kernel before them on the stream, so one of the caller's own
+ *     that lets its dependents in before it ends must first have waited for
+ *     what came before it (plain launches need no care).
  *   - Ownership: the caller owns every buffer.  The library allocates no
  *     device memory per call; it keeps one 4-byte device status word per
  *     GPU (a static device variable) and a host-side cache of TMA tensor
@@ -388,7 +392,8 @@ int attn_cache_read_fp4(const void* kv_cache, const int32_t* seq_ids, const int3
  * values that the cache stands for.  q, out [num_seqs, Hq, d] bf16, lse
  * [num_seqs, Hq] fp32 or NULL, block_table, ctx_lens and their checks on the
  * device as attn_decode_paged; keys and values enter exactly, the weights are
- * rounded to fp16.  ctx_len 0 gives out = 0, lse = -inf.  scale, k_scale and
+ * rounded to fp16.  ctx_len 0 gives out = 0, lse = -inf.  out overlaps no
+ * input, and ctx_lens keep their values while the call runs.  scale, k_scale and
  * v_scale are finite and > 0, and so is 2 scale k_scale in fp32
  * (EXATTN_ERR_INVALID_ARG).
  *   workspace: attn_decode_fp4_workspace_bytes(...) bytes, 16-byte aligned, its
