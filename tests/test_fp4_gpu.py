@@ -729,3 +729,83 @@ def test_append_captured_and_replayed(env):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(v, ex.attn_cache_read_fp4(other, t[3], t[4], tbl)[1] * 2)
+
+
+def test_rows_and_blocks_past_32_bits(env):
+    """Heads 2^31 elements apart, and blocks whose bytes pass 2^32."""
+    torch, ex, dev = env
+    T, H, d, far = 21, 2, 128, 1 << 31
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    x = to_dev(synth.normal_bf16(580, 1, (T, H, d)), dev)
+    big = torch.zeros(far + T * d, device=dev, dtype=torch.bfloat16)
+    wide = big.as_strided((T, H, d), (d, far, 1))
+    wide.copy_(x)
+    at = torch.arange(T, device=dev, dtype=torch.int32)
+    want, _ = ex.attn_rope_axes(x[None].transpose(1, 2), x[None].transpose(1, 2), at[None], (64,))
+    got, same = ex.attn_rope_axes(wide[None].transpose(1, 2), x[None].transpose(1, 2), at[None], (64,))
+    assert torch.equal(got, want) and torch.equal(same, want)
+
+    blocks = (1 << 32) // (H * 18 * d) + 4
+    seq = torch.zeros(T, device=dev, dtype=torch.int32)
+    near, ends = (torch.tensor([ids], device=dev, dtype=torch.int32) for ids in ([1, 0], [blocks - 1, blocks - 3]))
+    small, cache = ex.attn_fp4_cache(2, H, d), ex.attn_fp4_cache(blocks, H, d)
+    q = ex.attn_rope_cache_write_fp4(x, x, x, seq, at, at[None], near, small, (64,))
+    ex.attn_rope_cache_write_fp4(x, wide, wide, seq, at, at[None], ends, cache, (64,))
+    with pytest.raises(ex.ExattnError):  # queries over the keys that are yet to be read
+        ex.attn_rope_cache_write_fp4(wide, wide, wide, seq, at, at[None], ends, cache, (64,), q_out=wide)
+    qf = ex.attn_rope_cache_write_fp4(wide, x, x, seq, at, at[None], ends, cache, (64,), q_out=wide)
+    assert qf is wide and torch.equal(wide, q) and torch.equal(q, want[0].transpose(0, 1))
+    assert torch.equal(cache[-1], small[1]) and torch.equal(cache[-3], small[0])
+    assert int(cache[:-3].view(-1)[:1 << 20].max()) == 0 and int(cache[-2].max()) == 0
+    k, v = ex.attn_cache_read_fp4(small, seq, at, near)
+    wide.zero_()
+    kf, vf = ex.attn_cache_read_fp4(cache, seq, at, ends, k_out=wide)
+    assert torch.equal(kf, k) and torch.equal(vf, v)
+    lens = torch.tensor([T], device=dev, dtype=torch.int32)
+    a, b = ex.attn_decode_paged_fp4(q[-1:], small, near, lens), ex.attn_decode_paged_fp4(q[-1:], cache, ends, lens)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert ex.attn_get_device_status() == 0
+
+
+def test_first_calls_of_a_process_may_be_captured(env):
+    """The kernels load and the device state is set up inside a capture, too."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from exact_attention_40_gb300 import exattn as ex
+dev = torch.device("cuda:0")
+T, Hq, Hkv, d, S = 40, 8, 2, 128, 2
+g = torch.Generator(device=dev).manual_seed(1)
+q, k, v = (torch.randn(T, h, d, device=dev, generator=g).bfloat16() for h in (Hq, Hkv, Hkv))
+seq = torch.zeros(T, device=dev, dtype=torch.int32)
+at = torch.arange(T, device=dev, dtype=torch.int32)
+blocks = 700
+table = torch.arange(S * blocks, device=dev, dtype=torch.int32).view(S, blocks)
+lens = torch.tensor([T, 0], device=dev, dtype=torch.int32)
+cache = ex.attn_fp4_cache(S * blocks, Hkv, d)
+
+def run():
+    a = ex.attn_rope_axes(q[None].transpose(1, 2), k[None].transpose(1, 2), at[None], (64,))
+    b = ex.attn_rope_cache_write_fp4(q, k, v, seq, at, at[None], table, cache, (64,))
+    c = ex.attn_cache_read_fp4(cache, seq, at, table)
+    e = ex.attn_decode_paged_fp4(b[:S], cache, table, lens)          # split and merge
+    f = ex.attn_decode_paged_fp4(b[:S], cache, table[:, :100].contiguous(), lens)  # a cluster for each segment
+    return [*a, b, *c, *e, *f]
+
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+for x, y in zip(got, run()):
+    assert torch.equal(x, y)
+assert ex.attn_get_device_status() == 0
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
