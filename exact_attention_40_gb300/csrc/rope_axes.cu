@@ -49,14 +49,19 @@ __device__ __forceinline__ const uint4* row_of(const HeadView& v, long long b, l
 }
 
 // Cosines and sines of the tile's tokens into cs[token][pair]: pos(token, axis)
-// gives the position.
+// gives the position.  A thread keeps to one pair, and takes its entry of the table by
+// an ordinary load: as an operand of the constant bank it would be served to one
+// lane after the other.
 template <typename Pos>
 __device__ __forceinline__ void tile_angles(float2* cs, const RopeAxesTable& table, int half, int count, Pos pos) {
-  for (int idx = threadIdx.x; idx < count * half; idx += kTileThreads) {
-    const int tok = idx / half, i = idx - tok * half;
-    const long long p = pos(tok, table.axis[i]);
-    cs[idx] = turn_cos_sin(static_cast<unsigned long long>(p) * table.u[i]);
-  }
+  const int per = kTileThreads / half, i = threadIdx.x % half;
+  if (threadIdx.x >= per * half) return;
+  unsigned long long u;
+  uint32_t axis;
+  asm volatile("ld.b64 %0, [%1];" : "=l"(u) : "l"(table.u + i));
+  asm volatile("ld.u8 %0, [%1];" : "=r"(axis) : "l"(table.axis + i));
+  for (int tok = threadIdx.x / half; tok < count; tok += per)
+    cs[tok * half + i] = turn_cos_sin(static_cast<unsigned long long>(static_cast<long long>(pos(tok, axis))) * u);
 }
 
 // A thread's 8 cosines and sines.
@@ -432,7 +437,7 @@ Tile make_tile(int d, long long tokens, int rows, int lanes, int sms) {
   static_assert(RowRing<kFp4Stages>::kBytes + 32 * kTileThreads <= 48 * 1024, "shared memory of the append");
   t.toks = 1;
   while (2 * t.toks * lanes <= slots) t.toks *= 2;
-  while (t.toks > 1 && (tokens + t.toks - 1) / t.toks < sms && 2 * (slots / t.toks) <= rows) t.toks /= 2;
+  while (t.toks > 1 && (tokens + t.toks - 1) / t.toks < 1 * sms && 2 * (slots / t.toks) <= rows) t.toks /= 2;
   t.lanes = slots / t.toks;
   return t;
 }
