@@ -32,8 +32,8 @@
 //   What bounds it: conversions and the multiplications by the scales, which share a
 //   pipe (4 + 4 of them and one mma take 15 cycles of an SM's quarter, each of the
 //   three alone 8), then DRAM.  64 sequences of 8192 tokens, 32 heads over 8 of 128:
-//   105.8 us = 5.72 TB/s; the copies alone take 94.  64 sequences of 512 to 8192
-//   tokens with the merge 62.4 us = 5.16 TB/s.
+//   106.3 us = 5.69 TB/s; the copies alone take 94.  64 sequences of 512 to 8192
+//   tokens with the merge 62.6 us = 5.14 TB/s.
 //   Small calls (few segments, none long) take a cluster of 8 CTAs for each
 //   segment instead, which take its units in turn and merge through distributed
 //   shared memory: one launch and no workspace (six of up to 1500 tokens 3.9 us).

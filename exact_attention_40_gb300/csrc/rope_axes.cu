@@ -27,10 +27,10 @@ namespace {
 constexpr int kTileThreads = 256;
 // Measured choices (heads of a token in flight together, rows of a thread in the ring
 // with the one at hand, CTAs an SM).  Rotation of 8 x 4096 tokens, 32 + 32 heads of 128:
-// 155 us with 8 lanes, 4 or 5 stages and 4 CTAs, 157 with 4 lanes, 166 with 5 CTAs of 3
-// stages, 157 with two rows in registers and no ring.  Append of 16,384 tokens, 32 + 2 * 8
-// heads: 58 us with 4 lanes, 5 stages and 3 CTAs, 59 with 4 stages, 63 with 4 CTAs, 67
-// with 8 lanes, 61 with 2, 67 without the ring.
+// 156 us = 6.88 TB/s with 8 lanes, 4 or 5 stages and 4 CTAs, 157 with 4 lanes, 166 with
+// 5 CTAs of 3 stages, 157 with two rows in registers and no ring.  Append of 16,384
+// tokens, 32 + 2 * 8 heads: 56.6 us = 6.26 TB/s with 4 lanes, 5 stages and 3 CTAs; 1 us more
+// with 4 stages, 4 with 4 CTAs, 9 with 8 lanes, 3 with 2, 9 without the ring.
 constexpr int kRopeLanes = 8;
 constexpr int kRopeStages = 4;  // rows of a thread on their way, and the one at hand
 constexpr int kFp4Lanes = 4;
