@@ -706,6 +706,44 @@ def test_calls_that_follow_each_other_wait_for_what_they_use(env, S, ctx, Hq, Hk
     assert ex.attn_get_device_status() == 0
 
 
+def test_calls_after_an_event_of_another_stream(env):
+    """A call behind a kernel of its own stream and an event of another waits for both,
+    and the other stream, behind an event after it, overwrites its inputs no sooner."""
+    torch, ex, dev = env
+    d, Hq, Hkv, S = 128, 8, 2, 6
+    qs = [to_dev(synth.normal_bf16(590 + i, 1, (S, Hq, d)), dev) for i in range(12)]
+    _, cache, table, lens = decode_case(589, [3000, 5, 700, 129, 0, 64], Hq, Hkv, d)
+    cache, table, lens = (to_dev(x, dev) for x in (cache, table, lens))
+    at = torch.arange(S, device=dev, dtype=torch.int32)[None]
+    none = qs[0][:, :0]
+    want = []
+    for q in qs:
+        turned, _ = ex.attn_rope_axes(q[None].transpose(1, 2), none[None].transpose(1, 2), at, (64,))
+        torch.cuda.synchronize()
+        want.append(ex.attn_decode_paged_fp4(turned[0].transpose(0, 1).contiguous(), cache, table, lens)[0])
+        torch.cuda.synchronize()
+    busy = torch.randn(4096, 4096, device=dev)
+    side, main = torch.cuda.Stream(), torch.cuda.current_stream()
+    x, y = torch.zeros_like(qs[0]), torch.zeros_like(qs[0])
+    side.wait_stream(main)
+    got = []
+    for q in qs:
+        with torch.cuda.stream(side):
+            busy = (busy @ busy).clamp(-1, 1)  # the copy comes late
+            x.copy_(q)
+        ex.attn_rope_axes(y[None].transpose(1, 2), none[None].transpose(1, 2), at, (64,), q_out=y[None].transpose(1, 2))
+        main.wait_stream(side)
+        ex.attn_rope_axes(x[None].transpose(1, 2), none[None].transpose(1, 2), at, (64,), q_out=y[None].transpose(1, 2))
+        side.wait_stream(main)
+        got.append(ex.attn_decode_paged_fp4(y, cache, table, lens)[0])
+        with torch.cuda.stream(side):
+            x.fill_(float("nan"))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert ex.attn_get_device_status() == 0
+
+
 def test_append_captured_and_replayed(env):
     torch, ex, dev = env
     d, Hkv = 128, 2
