@@ -782,7 +782,10 @@ cudaError_t launch_bwd_d(const BwdArgs& a, const DeviceGuard& g, cudaStream_t st
     const long long units = static_cast<long long>(pk.n_tiles) * pk.n_bh;
     const long long grid = units < sms ? units : sms;
     // programmatic dependent launches: each may start while the launch
-    // before it finishes, and waits for it where it reads its results
+    // before it finishes, and waits for it where it reads its results.  The dK/dV
+    // pass waits at its first streamed tile, which every unit has where there are
+    // queries; without any nothing in it would wait, and what comes before
+    // it is not the dQ pass but some other call: then it is an ordinary launch.
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -792,7 +795,7 @@ cudaError_t launch_bwd_d(const BwdArgs& a, const DeviceGuard& g, cudaStream_t st
     cfg.dynamicSmemBytes = smem_kv;
     cfg.stream = stream;
     cfg.attrs = pdl;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.Nq > 0 ? 1 : 0;
     e = cudaLaunchKernelEx(&cfg, bwd_tc_kernel<D, true>, *a.tm_k128, *a.tm_v128, *a.tm_q64, *a.tm_do64,
                            *a.tm_k128, *a.tm_k128, *a.tm_ldp, pk);
     if (e != cudaSuccess) return e;
