@@ -184,8 +184,10 @@ __device__ __forceinline__ long long find_block(const Fp4Slots& at, long long n,
 // see those ties.  They come from the correctly rounded reciprocal r by one
 // step: q = x r, q + (x - q y) r with fused multiply-adds is x / y correctly
 // rounded (Markstein, IBM Journal of Research and Development 34, 1990).
-// That holds while nothing over- or underflows; the rare rest takes the
-// division itself.
+// Written as q - (q y - x) r it also keeps the sign of a zero x, as the
+// division does: the residual of an exact quotient is +0, and adding +0 to -0
+// would lose it.  That holds while nothing over- or underflows; the rare rest takes
+// the division itself.
 struct Quantiser {
   float g, six_g, inv_six_g;
   bool plain;  // 6 g and its reciprocal are of an ordinary size
@@ -219,7 +221,7 @@ struct Quantiser {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const float q0 = __fmul_rn(x[e], r);
-        q[e] = __fmaf_rn(__fmaf_rn(-q0, y, x[e]), r, q0);
+        q[e] = __fmaf_rn(__fmaf_rn(q0, y, -x[e]), -r, q0);
       }
     } else {
 #pragma unroll
