@@ -25,10 +25,13 @@
 //   into the score's factor.  Both products sum over their inner index
 //   in any order, so which column or token an mma index stands for is free: it
 //   is chosen so that a lane reads its codes as one vector each, from one or two
-//   scale groups.  Weights are rounded to fp16 for the second product, at most
-//   2^-11 relative (the output is rounded to bf16, 2^-8); their sums are fp32 and
-//   take them unrounded (a second sum, of the rounded weights, cost 1 to 2% of the
-//   time and changed no digit that bf16 keeps).
+//   scale groups.  Weights are rounded to fp16 for the second product.  They are
+//   taken 2^7 times as large as the softmax's, so that their largest lies between 2^7
+//   and 2^15: fp16 then rounds those above 2^-21 of the reference by at most 2^-11
+//   relative (the output is rounded to bf16, 2^-8), the smaller ones by at most
+//   2^-32 of the reference, which many tokens beside one that dominates do not add up
+//   to anything.  Their sums are fp32 and take them unrounded (a second sum, of the
+//   rounded weights, cost 1 to 2% of the time).
 //   What bounds it: conversions and the multiplications by the scales, which share a
 //   pipe (4 + 4 of them and one mma take 15 cycles of an SM's quarter, each of the
 //   three alone 8), then DRAM.  64 sequences of 8192 tokens, 32 heads over 8 of 128:
@@ -61,6 +64,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kWhole = static_cast<int>(0x80000000u);
 constexpr float kNoScore = -3.0e38f;     // below any score; -inf would give inf - inf
+// Weights are 2^(score - reference), the reference kLift below the running maximum that it
+// was taken from, and a new one taken once a score passes it by more than kMost: fp16
+// holds weights of up to 2^15.
+constexpr float kLift = 7.f;
+constexpr float kMost = 15.f;
 
 struct Fp4SplitParams {
   const __nv_bfloat16* q;
@@ -151,7 +159,7 @@ struct Fp4Smem {
   uint64_t full[kStages];        // a unit's copies have landed
   uint64_t empty[kStages];       // the four warps have used it
   int present[kStages];          // bits of its blocks that were copied, kWhole where all are and are full
-  float wm[2][kWarps][8 * NT];   // per-warp running max (log2 units)
+  float wm[2][kWarps][8 * NT];   // per-warp reference (log2 units)
   float wl[2][kWarps][8 * NT];   // per-warp sum of the weights
 };
 
@@ -729,9 +737,8 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
           __syncwarp();  // the lanes together again for the next mma
         }
         // Exponents relative to the reference m.  It follows the running maximum
-        // only when a score passes it by more than 8 (weights up to 2^8 fit fp16
-        // and the fp32 sums), which is rare after the first blocks: most pairs pay
-        // one vote.
+        // only when that has grown by more than kMost - kLift, which is rare after the
+        // first blocks: most pairs pay one vote.
         float x[2][NT][4];
         float most = -INFINITY;
 #pragma unroll
@@ -744,7 +751,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
               x[b][nt][y + 1] = fmaf(c[b][nt][y + 1], factor[nt][1], -m[nt][1]);
               most = max3f(most, x[b][nt][y], x[b][nt][y + 1]);
             }
-        if (__any_sync(0xffffffffu, most > 8.f)) {
+        if (__any_sync(0xffffffffu, most > kMost)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -753,7 +760,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-              const float mn = fmaxf(m[nt][j], top * factor[nt][j]);
+              const float mn = fmaxf(m[nt][j], fmaf(top, factor[nt][j], -kLift));
               const float alpha = ex2_approx(m[nt][j] - mn);
               m[nt][j] = mn;
               l[nt][j] *= alpha;

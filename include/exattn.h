@@ -391,8 +391,9 @@ int attn_cache_read_fp4(const void* kv_cache, const int32_t* seq_ids, const int3
  * One-token decode over the 4-bit cache: attn_decode_paged on the keys and
  * values that the cache stands for.  q, out [num_seqs, Hq, d] bf16, lse
  * [num_seqs, Hq] fp32 or NULL, block_table, ctx_lens and their checks on the
- * device as attn_decode_paged; keys and values enter exactly, the weights are
- * rounded to fp16.  ctx_len 0 gives out = 0, lse = -inf.  out overlaps no
+ * device as attn_decode_paged; keys and values enter exactly, a weight is
+ * rounded by at most 2^-11 of itself or 2^-32 of the largest, whichever is more.
+ * ctx_len 0 gives out = 0, lse = -inf.  out overlaps no
  * input, and ctx_lens keep their values while the call runs.  scale, k_scale and
  * v_scale are finite and > 0, and so is 2 scale k_scale in fp32
  * (EXATTN_ERR_INVALID_ARG).
