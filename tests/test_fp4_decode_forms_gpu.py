@@ -58,6 +58,48 @@ def run(env, q, cache, table, lens, d, scale, k_scale=1.0, v_scale=1.0, rows=Non
     return out, lse
 
 
+def shared_pages(lens, pages):
+    """A block table over few pages that the sequences share, each in an order of its own."""
+    most = int((lens.max() + 15) // 16)
+    s, b = np.meshgrid(np.arange(len(lens)), np.arange(most), indexing="ij")
+    table = ((s * 37 + b * (2 * (s % 13) + 1)) % pages).astype(np.int32)
+    return np.where(b * 16 < lens[:, None], table, -1).astype(np.int32)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("S,Hq,Hkv,hi", [
+    (64, 32, 8, 2500),    # 512 segments of up to 8 rows
+    (64, 64, 8, 900),     # all 8 of them used
+    (40, 96, 8, 1500),    # 320 segments of 12 rows, 304 CTAs
+    (30, 160, 8, 700),    # 20 rows a KV head: two chunks of 16, the second of 4
+    (120, 40, 1, 1000),   # one KV head, three chunks
+    (160, 17, 1, 1200),   # a second chunk of one row
+    (460, 2, 1, 1300),    # just above one wave of segments
+])
+def test_more_segments_than_ctas(env, d, S, Hq, Hkv, hi):
+    """Segments that go on in further CTAs are then found in the list that the split
+    kernel writes.  Lengths from 0 to hi, most of them short."""
+    group = Hq // Hkv
+    rows = 8 if group <= 8 else 16
+    assert S * Hkv * -(-group // rows) > 152 * (3 if rows == 8 else 2)
+    lens = np.floor(synth.uniform01(630 + S, S) ** 2 * (hi + 1)).astype(np.int32)
+    lens[[0, S // 2, S - 1]] = 0
+    lens[1] = hi
+    cache = ref.random_cache(631, 150, Hkv, d, 0.01, 0.003)
+    q = synth.normal_bf16(632, 0, (S, Hq, d))
+    some = np.unique(np.concatenate([[0, 1, S // 2, S - 1], np.argsort(lens)[-4:], np.arange(2, S, max(1, S // 12))]))
+    table = shared_pages(lens, 150)
+    args = (q, cache, table, lens, d, d ** -0.5, 0.01, 0.003)
+    out, lse = run(env, *args, rows=some)
+    # every row, also those not compared above: a sequence alone gives nearly the same
+    torch, ex, dev = env
+    for s in range(0, S, max(1, S // 30)):
+        one, one_lse = ex.attn_decode_paged_fp4(to_dev(q[s:s + 1], dev), to_dev(cache, dev), to_dev(table[s:s + 1], dev),
+                                                to_dev(lens[s:s + 1], dev), scale=d ** -0.5, k_scale=0.01, v_scale=0.003)
+        assert (one - out[s]).abs().max() <= 2.0 ** -6 * out[s].abs().max() + 1e-6
+        assert torch.allclose(one_lse[0], lse[s], rtol=0, atol=1e-4)
+
+
 @pytest.mark.parametrize("bits", [20, 27, 30])
 @pytest.mark.parametrize("place", [0, 31])
 @pytest.mark.parametrize("d,S,n,Hq", [(64, 1, 128, 1), (128, 3, 1000, 8), (64, 2, 20000, 12), (128, 500, 1500, 2)])
