@@ -17,7 +17,7 @@
 #include <array>
 #include <cmath>
 #include <cstdarg>
-#include <initializer_list>
+#include <optional>
 
 #include "../../include/exattn.h"
 
@@ -101,57 +101,65 @@ struct Sections {
   }
 };
 
-// A new contiguous tensor, straight from the CUDA allocator (through the
-// operators' dispatcher it takes half a microsecond more).
-Tensor fresh(c10::Device device, at::IntArrayRef shape, at::ScalarType type) {
-  return at::detail::empty_cuda(shape, type, device, std::nullopt);
-}
+// Where a call runs: the tensors' device, and the given stream or that device's current
+// one.  While it exists they are the current device and stream, so that what the call
+// allocates belongs to the stream that uses it: out of the caller's current stream's
+// memory it could be a block whose last use there is still to come.
+struct Target {
+  c10::Device device;
+  c10::cuda::CUDAGuard guard;
+  c10::cuda::CUDAStream callers;  // the caller's current stream
+  cudaStream_t handle;
+  c10::cuda::OptionalCUDAStreamGuard on;
 
-// The output `o`, or a new contiguous tensor where it is None.
-Tensor output(PyObject* o, const char* name, c10::Device device, at::IntArrayRef shape, at::ScalarType type,
-              bool contiguous) {
-  if (o == Py_None) return fresh(device, shape, type);
-  const Tensor& t = tensor(o, name, static_cast<int64_t>(shape.size()), type);
-  check(t, name, device, shape, contiguous);
-  return t;
-}
-
-// Runs call(stream) on the device with the given stream, or its current one.
-// `made`: the tensors this call uses, of which those it allocated belong to the
-// current stream; on another one the allocator is told of it, so that a
-// tensor that is dropped at once (the workspace is) is not handed out again while
-// the kernels run.
-template <typename Call>
-void launch(const char* name, c10::Device device, PyObject* stream, std::initializer_list<const Tensor*> made,
-            Call call) {
-  const c10::cuda::CUDAGuard guard(device);
-  const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(device.index());
-  cudaStream_t handle = current.stream();
-  if (stream != Py_None) {
+  Target(c10::Device d, PyObject* stream)
+      : device(d), guard(d), callers(c10::cuda::getCurrentCUDAStream(d.index())), handle(callers.stream()) {
+    if (stream == Py_None) return;
     PyObject* raw = PyObject_GetAttrString(stream, "cuda_stream");
     if (raw == nullptr) throw python_error();
     handle = static_cast<cudaStream_t>(PyLong_AsVoidPtr(raw));
     Py_DECREF(raw);
     if (handle == nullptr && PyErr_Occurred()) throw python_error();
-    if (handle != current.stream())
-      for (const Tensor* t : made)
-        if (t->defined() && t->numel() > 0)
-          c10::cuda::CUDACachingAllocator::recordStream(t->storage().data_ptr(),
-                                                        c10::cuda::getStreamFromExternal(handle, device.index()));
+    if (handle != callers.stream()) on.reset_stream(c10::cuda::getStreamFromExternal(handle, d.index()));
   }
-  int rc;
-  Py_BEGIN_ALLOW_THREADS
-  rc = call(static_cast<void*>(handle));
-  Py_END_ALLOW_THREADS
-  if (rc != EXATTN_OK) {
-    PyObject* e = PyObject_CallFunction(g_error, "si", name, rc);
-    if (e != nullptr) {
-      PyErr_SetObject(g_error, e);
-      Py_DECREF(e);
+
+  // A new contiguous tensor, straight from the CUDA allocator (through the
+  // operators' dispatcher it takes half a microsecond more).
+  Tensor fresh(at::IntArrayRef shape, at::ScalarType type) const {
+    return at::detail::empty_cuda(shape, type, device, std::nullopt);
+  }
+
+  // The output `o`, or a new contiguous tensor where it is None.  The caller will go on
+  // with that on its own stream: the allocator is told, for when it is dropped.
+  Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, bool contiguous) const {
+    if (o == Py_None) {
+      const Tensor t = fresh(shape, type);
+      if (handle != callers.stream() && t.numel() > 0)
+        c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), callers);
+      return t;
     }
-    throw python_error();
+    const Tensor& t = tensor(o, name, static_cast<int64_t>(shape.size()), type);
+    check(t, name, device, shape, contiguous);
+    return t;
   }
-}
+
+  // Runs call(stream), without the interpreter's lock.
+  template <typename Call>
+  void launch(const char* name, Call call) const {
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = call(static_cast<void*>(handle));
+    Py_END_ALLOW_THREADS
+    if (rc != EXATTN_OK) {
+      PyObject* e = PyObject_CallFunction(g_error, "si", name, rc);
+      if (e != nullptr) {
+        PyErr_SetObject(g_error, e);
+        Py_DECREF(e);
+      }
+      throw python_error();
+    }
+  }
+};
 
 void need_args(Py_ssize_t got, Py_ssize_t want) {
   if (got != want) fail(PyExc_TypeError, "expected %zd arguments, got %zd", want, got);
@@ -180,8 +188,9 @@ PyObject* rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (pos.device() != device || pos.size(0) != sections.count || pos.size(-1) != N || (batched && pos.size(1) != B))
     fail(PyExc_ValueError, "positions must be [%d, %lld, %lld] or [%d, %lld] on the tensors' device", sections.count,
          static_cast<long long>(B), static_cast<long long>(N), sections.count, static_cast<long long>(N));
-  const Tensor qo = output(a[7], "q_out", device, q.sizes(), at::kBFloat16, false);
-  const Tensor ko = output(a[8], "k_out", device, k.sizes(), at::kBFloat16, false);
+  const Target on(device, a[9]);
+  const Tensor qo = on.output(a[7], "q_out", q.sizes(), at::kBFloat16, false);
+  const Tensor ko = on.output(a[8], "k_out", k.sizes(), at::kBFloat16, false);
   const int64_t strides[15] = {q.stride(0),  q.stride(1),  q.stride(2),  k.stride(0),  k.stride(1),
                                k.stride(2),  qo.stride(0), qo.stride(1), qo.stride(2), ko.stride(0),
                                ko.stride(1), ko.stride(2), pos.stride(0), batched ? pos.stride(1) : 0, pos.stride(-1)};
@@ -189,7 +198,7 @@ PyObject* rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int per_axis = truth(a[5]), inverse = truth(a[6]);
   const int iB = narrow(B, "B"), iHq = narrow(Hq, "Hq"), iHkv = narrow(Hkv, "Hkv"), iN = narrow(N, "N"),
             id = narrow(d, "d");
-  launch("attn_rope_axes", device, a[9], {&qo, &ko}, [&](void* s) {
+  on.launch("attn_rope_axes", [&](void* s) {
     return attn_rope_axes(q.const_data_ptr(), k.const_data_ptr(), qo.data_ptr(), ko.data_ptr(), ints(pos), strides,
                           sections.size, sections.count, iB, iHq, iHkv, iN, id, base, per_axis, inverse, s);
   });
@@ -236,7 +245,8 @@ PyObject* rope_cache_write_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& slots = indexes(a[4], "slots", c.device, {T});
   const Tensor& positions = indexes(a[5], "positions", c.device, {sections.count, T});
   const Tensor& table = indexes(a[6], "block_table", c.device, {-1, -1});
-  const Tensor qo = output(a[13], "q_out", c.device, q.sizes(), at::kBFloat16, false);
+  const Target on(c.device, a[14]);
+  const Tensor qo = on.output(a[13], "q_out", q.sizes(), at::kBFloat16, false);
   const int64_t strides[9] = {q.stride(0), q.stride(1),  k.stride(0),  k.stride(1), v.stride(0),
                               v.stride(1), qo.stride(0), qo.stride(1), T};
   const float base = static_cast<float>(number(a[9])), k_scale = static_cast<float>(number(a[11])),
@@ -244,7 +254,7 @@ PyObject* rope_cache_write_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int per_axis = truth(a[10]);
   const int iT = narrow(T, "num_tokens"), iHq = narrow(Hq, "Hq"), S = narrow(table.size(0), "num_seqs"),
             mb = narrow(table.size(1), "max_blocks_per_seq");
-  launch("attn_rope_cache_write_fp4", c.device, a[14], {&qo}, [&](void* s) {
+  on.launch("attn_rope_cache_write_fp4", [&](void* s) {
     return attn_rope_cache_write_fp4(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), qo.data_ptr(),
                                      ints(seq_ids), ints(slots), ints(positions), ints(table), c.t.data_ptr(), strides,
                                      sections.size, sections.count, iT, iHq, c.Hkv, c.d, S, c.num_blocks, mb, base,
@@ -264,13 +274,14 @@ PyObject* cache_read_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& slots = indexes(a[2], "slots", c.device, {T});
   const Tensor& table = indexes(a[3], "block_table", c.device, {-1, -1});
   const std::array<int64_t, 3> shape = {T, c.Hkv, c.d};
-  const Tensor ko = output(a[6], "k_out", c.device, shape, at::kBFloat16, false);
-  const Tensor vo = output(a[7], "v_out", c.device, shape, at::kBFloat16, false);
+  const Target on(c.device, a[8]);
+  const Tensor ko = on.output(a[6], "k_out", shape, at::kBFloat16, false);
+  const Tensor vo = on.output(a[7], "v_out", shape, at::kBFloat16, false);
   const int64_t strides[4] = {ko.stride(0), ko.stride(1), vo.stride(0), vo.stride(1)};
   const float k_scale = static_cast<float>(number(a[4])), v_scale = static_cast<float>(number(a[5]));
   const int iT = narrow(T, "num_tokens"), S = narrow(table.size(0), "num_seqs"),
             mb = narrow(table.size(1), "max_blocks_per_seq");
-  launch("attn_cache_read_fp4", c.device, a[8], {&ko, &vo}, [&](void* s) {
+  on.launch("attn_cache_read_fp4", [&](void* s) {
     return attn_cache_read_fp4(c.t.const_data_ptr(), ints(seq_ids), ints(slots), ints(table), ko.data_ptr(),
                                vo.data_ptr(), strides, iT, c.Hkv, c.d, S, c.num_blocks, mb, k_scale, v_scale, s);
   });
@@ -290,15 +301,16 @@ PyObject* decode_paged_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& ctx_lens = indexes(a[3], "ctx_lens", c.device, {S});
   const float scale = static_cast<float>(a[4] == Py_None ? 1.0 / std::sqrt(static_cast<double>(c.d)) : number(a[4]));
   const float k_scale = static_cast<float>(number(a[5])), v_scale = static_cast<float>(number(a[6]));
-  const Tensor out = output(a[7], "out", c.device, q.sizes(), at::kBFloat16, true);
+  const Target on(c.device, a[11]);
+  const Tensor out = on.output(a[7], "out", q.sizes(), at::kBFloat16, true);
   Tensor lse;
-  if (a[8] != Py_None || truth(a[10])) lse = output(a[8], "lse", c.device, {S, Hq}, at::kFloat, true);
+  if (a[8] != Py_None || truth(a[10])) lse = on.output(a[8], "lse", {S, Hq}, at::kFloat, true);
   const int iS = narrow(S, "num_seqs"), iHq = narrow(Hq, "Hq"), mb = narrow(table.size(1), "max_blocks_per_seq");
   Tensor workspace;
   size_t bytes = 0;
   if (a[9] == Py_None) {
     bytes = attn_decode_fp4_workspace_bytes(iS, iHq, c.Hkv, c.d, mb);
-    if (bytes > 0) workspace = fresh(c.device, {static_cast<int64_t>(bytes)}, at::kByte);
+    if (bytes > 0) workspace = on.fresh({static_cast<int64_t>(bytes)}, at::kByte);
   } else {
     if (!THPVariable_Check(a[9])) fail(PyExc_TypeError, "workspace must be a torch.Tensor");
     workspace = THPVariable_Unpack(a[9]);
@@ -306,7 +318,7 @@ PyObject* decode_paged_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
       fail(PyExc_ValueError, "workspace must be contiguous on the tensors' device");
     bytes = static_cast<size_t>(workspace.numel()) * workspace.element_size();
   }
-  launch("attn_decode_paged_fp4", c.device, a[11], {&out, &lse, &workspace}, [&](void* s) {
+  on.launch("attn_decode_paged_fp4", [&](void* s) {
     return attn_decode_paged_fp4(q.const_data_ptr(), c.t.const_data_ptr(), ints(table), ints(ctx_lens), out.data_ptr(),
                                  lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, iS, iHq, c.Hkv, c.d,
                                  c.num_blocks, mb, scale, k_scale, v_scale,

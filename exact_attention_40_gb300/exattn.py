@@ -9,10 +9,12 @@ Importing this module loads the library and raises if it has not been
 built (``python -m exact_attention_40_gb300.build``) -- there is no
 fallback path.
 
-The functions carry the C names.  ``attn_fwd`` and ``attn_decode_paged``
-take torch tensors, allocate outputs when none are given, and raise
-``ExattnError`` on a non-zero status.  ``lib`` is the raw ctypes handle for
-callers (and tests) that pass pointers themselves.
+The functions carry the C names.  They take torch tensors, allocate outputs
+and workspaces that are not given, and raise ``ExattnError`` on a non-zero
+status.  They run on ``stream``, by default the current one: on another it is
+the caller's part to have that wait for the inputs, and the current one for
+the outputs, as for any torch operation there.  ``lib`` is the raw ctypes handle
+for callers (and tests) that pass pointers themselves.
 """
 from __future__ import annotations
 
