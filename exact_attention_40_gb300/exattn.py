@@ -125,6 +125,21 @@ def _on_device(t):
     return torch.cuda.device(t.device)
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor for a call on `stream` (None: the current one).  On another stream it
+    belongs to that one, since a block of the current stream's memory may have uses there
+    still to come, and the allocator is told that the current one goes on with it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if stream != current:
+        t.record_stream(current)
+    return t
+
+
 def _check_tensor(name, t, dtype, ndim):
     import torch
     if not isinstance(t, torch.Tensor):
@@ -155,11 +170,11 @@ def attn_fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     else:
         _check_tensor("out", out, torch.bfloat16, 4)
     if lse is None and return_lse:
-        lse = torch.empty((B, Hq, Nq), device=q.device, dtype=torch.float32)
+        lse = _empty((B, Hq, Nq), torch.float32, q.device, stream)
     elif lse is not None:
         _check_tensor("lse", lse, torch.float32, 3)
     with _on_device(q):
@@ -192,12 +207,12 @@ def attn_decode_paged(q, k_cache, v_cache, block_table, ctx_lens, scale: float |
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((S, Hq), device=q.device, dtype=torch.float32)
+        lse = _empty((S, Hq), torch.float32, q.device, stream)
     if workspace is None:  # (the library checks a given workspace's size)
         need = attn_decode_workspace_bytes(S, Hq, d, max_blocks, bs)
-        workspace = torch.empty(max(need, 16), device=q.device, dtype=torch.uint8)
+        workspace = _empty(max(need, 16), torch.uint8, q.device, stream)
     with _on_device(q):
         rc = lib.attn_decode_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                    block_table.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(),
@@ -225,11 +240,11 @@ def attn_add_rms_norm(x, residual, weight, eps: float = 1e-6, out=None, residual
         raise ValueError("shape mismatch: x %s residual %s weight %s"
                          % (tuple(x.shape), tuple(residual.shape), tuple(weight.shape)))
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, x.dtype, x.device, stream)
     else:
         _check_tensor("out", out, torch.bfloat16, 2)
     if residual_out is None:
-        residual_out = torch.empty_like(x)
+        residual_out = _empty(x.shape, x.dtype, x.device, stream)
     else:
         _check_tensor("residual_out", residual_out, torch.bfloat16, 2)
     if tuple(out.shape) != (T, D) or tuple(residual_out.shape) != (T, D):
@@ -362,12 +377,12 @@ def attn_bwd(q, k, v, out, dout, lse, causal: bool = False, scale: float | None 
         raise ValueError("shape mismatch")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty(k.shape, k.dtype, k.device, stream) if dk is None else dk
+    dv = _empty(v.shape, v.dtype, v.device, stream) if dv is None else dv
     need = int(lib.attn_bwd_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), device=q.device, dtype=torch.uint8)
+        workspace = _empty(max(need, 16), torch.uint8, q.device, stream)
     with _on_device(q):
         rc = lib.attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(),
                           lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Nq,

@@ -54,7 +54,34 @@ def read(torch, ex, dev):
     return [640 * 2 * 64 * 2] * 2, lambda stream: ex.attn_cache_read_fp4(cache, seq, at, table, stream=stream)
 
 
-CALLS = [decode_fp4, rope, append, read]
+def forward(torch, ex, dev):
+    q = to_dev(synth.normal_bf16(644, 0, (1, 4, 300, 64)), dev)
+    return [q.numel() * 2, 4 * 300 * 4], lambda stream: ex.attn_fwd(q, q, q, causal=True, stream=stream)
+
+
+def backward(torch, ex, dev):
+    q = to_dev(synth.normal_bf16(645, 0, (1, 4, 300, 64)), dev)
+    k = q[:, :2].contiguous()
+    out, lse = ex.attn_fwd(q, k, k)
+    sizes = [q.numel() * 2, k.numel() * 2, k.numel() * 2, ex.lib.attn_bwd_workspace_bytes(1, 4, 2, 300, 300, 64)]
+    return sizes, lambda stream: ex.attn_bwd(q, k, k, out, q, lse, stream=stream)
+
+
+def decode(torch, ex, dev):
+    lens = torch.tensor([20000, 3], device=dev, dtype=torch.int32)
+    cache = to_dev(synth.normal_bf16(646, 0, (64, 1, 16, 128)), dev)
+    table = (torch.arange(2 * 1250, device=dev, dtype=torch.int32) % 64).view(2, 1250)
+    q = to_dev(synth.normal_bf16(646, 1, (2, 8, 128)), dev)
+    sizes = [ex.attn_decode_workspace_bytes(2, 8, 128, 1250), q.numel() * 2, 2 * 8 * 4]
+    return sizes, lambda stream: ex.attn_decode_paged(q, cache, cache, table, lens, stream=stream)
+
+
+def norm(torch, ex, dev):
+    x = to_dev(synth.normal_bf16(647, 0, (64, 512)), dev)
+    return [x.numel() * 2] * 2, lambda stream: ex.attn_add_rms_norm(x, x, x[0], stream=stream)
+
+
+CALLS = [decode_fp4, rope, append, read, forward, backward, decode, norm]
 
 
 @pytest.mark.parametrize("make", CALLS)
