@@ -399,7 +399,11 @@ _native = None  # _binding, the compiled half, once a call needs it
 def _load_native():
     global _native
     import torch  # noqa: F401  (its libraries have to be in the process first)
-    from . import _binding
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise ImportError("_binding.so, which this call needs, is not built for this torch and Python (%s); "
+                          "run `python -m exact_attention_40_gb300.build`" % e) from e
     _binding.set_error(ExattnError)
     _native = _binding
     return _binding
