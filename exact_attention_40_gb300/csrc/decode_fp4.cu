@@ -121,6 +121,15 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
+// c0, c1 times f[0], f[1], rounded, and their distances x0, x1 from m[0], m[1].  (Packed,
+// so that the products cost no more than the one fused operation for each score.)
+__device__ __forceinline__ void scores_and_distances(float& c0, float& c1, const float (&f)[2], const float (&m)[2],
+                                                     float& x0, float& x1) {
+  const uint64_t p = f2_mul(f2_pack(c0, c1), f2_pack(f[0], f[1]));
+  f2_unpack(p, c0, c1);
+  f2_unpack(f2_sub(p, f2_pack(m[0], m[1])), x0, x1);
+}
+
 // Loads from shared memory at addr + kOff (the offset is part of the instruction).
 template <int kOff, int W>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[W]) {
@@ -738,7 +747,10 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
         }
         // Exponents relative to the reference m.  It follows the running maximum
         // only when that has grown by more than kMost - kLift, which is rare after the
-        // first blocks: most pairs pay one vote.
+        // first blocks: most pairs pay one vote.  A score is rounded before m is taken
+        // from it, as it was when it gave m: in one fused operation the largest
+        // itself would lie off by the rounding, which passes all that fp16 holds once
+        // scores come to 2^28.
         float x[2][NT][4];
         float most = -INFINITY;
 #pragma unroll
@@ -747,8 +759,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int y = 0; y < 4; y += 2) {
-              x[b][nt][y] = fmaf(c[b][nt][y], factor[nt][0], -m[nt][0]);
-              x[b][nt][y + 1] = fmaf(c[b][nt][y + 1], factor[nt][1], -m[nt][1]);
+              scores_and_distances(c[b][nt][y], c[b][nt][y + 1], factor[nt], m[nt], x[b][nt][y], x[b][nt][y + 1]);
               most = max3f(most, x[b][nt][y], x[b][nt][y + 1]);
             }
         if (__any_sync(0xffffffffu, most > kMost)) {
@@ -760,7 +771,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-              const float mn = fmaxf(m[nt][j], fmaf(top, factor[nt][j], -kLift));
+              const float mn = fmaxf(m[nt][j], top - kLift);
               const float alpha = ex2_approx(m[nt][j] - mn);
               m[nt][j] = mn;
               l[nt][j] *= alpha;
@@ -771,8 +782,8 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
               }
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
-                x[b][nt][j] = fmaf(c[b][nt][j], factor[nt][j], -mn);
-                x[b][nt][2 + j] = fmaf(c[b][nt][2 + j], factor[nt][j], -mn);
+                x[b][nt][j] = c[b][nt][j] - mn;
+                x[b][nt][2 + j] = c[b][nt][2 + j] - mn;
               }
             }
         }

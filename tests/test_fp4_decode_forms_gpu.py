@@ -120,3 +120,35 @@ def test_weights_far_below_the_largest_are_not_lost(env, bits, place, d, S, n, H
     table = np.tile(np.arange(blocks, dtype=np.int32), (S, 1))
     lens = np.full(S, n, np.int32)
     run(env, synth.f32_to_bf16_bits(f), cache, table, lens, d, bits * np.log(2.0) / 6, rows=np.arange(min(S, 3)))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bits", [20, 28, 34, 60])
+@pytest.mark.parametrize("lens,Hq", [([900, 31, 1], 4), ([128, 100], 16), ([9000, 0, 300], 20)])
+def test_scores_beyond_fp32_resolution(env, d, bits, lens, Hq):
+    """Scores of about 2^bits and more: all the weight falls to the largest, and the output is its
+    token's value.  (Where the largest two are closer than fp32's rounding of the sums of d
+    products, 2^-18 of the largest, either may have it.)"""
+    torch, ex, dev = env
+    lens = np.asarray(lens, np.int32)
+    table, nb = synth.paged_layout(lens, 16, 650)
+    cache = ref.random_cache(650, nb, 1, d)
+    q = synth.normal_bf16(651, 0, (len(lens), Hq, d))
+    scale = 2.0 ** bits / d ** 0.5
+    out, lse = ex.attn_decode_paged_fp4(to_dev(q, dev), to_dev(cache, dev), to_dev(table, dev), to_dev(lens, dev), scale=scale)
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    f = synth.bf16_bits_to_f32(q).astype(np.float64)
+    for s, n in enumerate(lens):
+        if n == 0:
+            continue
+        k, v = (x.transpose(0, 2, 1, 3).reshape(-1, d)[:n] for x in
+                ref.cache_values(cache[table[s, :(n + 15) // 16]], d, 1.0, 1.0))
+        x = f[s] @ k.T * scale
+        for h in range(Hq):
+            big = np.abs(x[h]).max()
+            assert abs(lse[s, h] - x[h].max()) <= 2.0 ** -18 * big
+            near = x[h] >= x[h].max() - 2.0 ** -18 * big - 25.0
+            lo, hi = v[near].min(0), v[near].max(0)  # a mean of these
+            assert (out[s, h] >= lo - 2.0 ** -8 * np.abs(lo) - 1e-9 * n).all()
+            assert (out[s, h] <= hi + 2.0 ** -8 * np.abs(hi) + 1e-9 * n).all()
+    assert ex.attn_get_device_status() == 0
