@@ -900,20 +900,20 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
         o.w += wt * a.w;
       }
       // a share all of whose scores are -inf, or whose blocks are all missing, sees nothing
-      const float scale = L == 0.f ? 0.f : __fdividef(p.v_scale, L);
+      // (v_scale on its own: over the sum of the weights it could lose its bits)
+      const float inv = L == 0.f ? 0.f : __fdividef(1.f, L);
+      o = make_float4(o.x * inv * p.v_scale, o.y * inv * p.v_scale, o.z * inv * p.v_scale, o.w * inv * p.v_scale);
       const float ls = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
       if constexpr (kCluster) {
-        *reinterpret_cast<float4*>(cluster_o + r * D + col) =
-            make_float4(o.x * scale, o.y * scale, o.z * scale, o.w * scale);
+        *reinterpret_cast<float4*>(cluster_o + r * D + col) = o;
         if (col == 0) cluster_lse[r] = ls;
       } else if (starts && ends) {
         *reinterpret_cast<uint2*>(p.out + (row0 + r) * D + col) =
-            make_uint2(pack_bf16x2(o.x * scale, o.y * scale), pack_bf16x2(o.z * scale, o.w * scale));
+            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
         if (p.lse != nullptr && col == 0) p.lse[row0 + r] = ls;
       } else {
         const size_t row = static_cast<size_t>(2 * cta + (starts ? 1 : 0)) * kRows + r;
-        *reinterpret_cast<float4*>(p.ws_o + row * D + col) =
-            make_float4(o.x * scale, o.y * scale, o.z * scale, o.w * scale);
+        *reinterpret_cast<float4*>(p.ws_o + row * D + col) = o;
         if (col == 0) p.ws_lse[row] = ls;
       }
     }

@@ -152,3 +152,16 @@ def test_scores_beyond_fp32_resolution(env, d, bits, lens, Hq):
             assert (out[s, h] >= lo - 2.0 ** -8 * np.abs(lo) - 1e-9 * n).all()
             assert (out[s, h] <= hi + 2.0 ** -8 * np.abs(hi) + 1e-9 * n).all()
     assert ex.attn_get_device_status() == 0
+
+
+@pytest.mark.parametrize("v_scale", [2e-38, 1e35])
+@pytest.mark.parametrize("S,n,Hq", [(2, 3000, 4), (2, 100, 9), (1, 70000, 12), (460, 20000, 1)])
+def test_value_scales_near_the_ends_of_fp32(env, v_scale, S, n, Hq):
+    """Flat scores, so that the sum of the weights is as large as it gets beside them."""
+    lens = np.full(S, n, np.int32)
+    lens[S // 2] = n - 9
+    cache = ref.random_cache(660, 300, 1, 64)
+    ref.split(cache, 64)[3][...] |= 0x40  # scales of 2 and more
+    q = np.zeros((S, Hq, 64), np.uint16)
+    some = np.unique([0, S // 2, S - 1])
+    run(env, q, cache, shared_pages(lens, 300), lens, 64, 0.125, v_scale=v_scale, rows=some)
