@@ -32,11 +32,14 @@
 //   2^-32 of the reference, which many tokens beside one that dominates do not add up
 //   to anything.  Their sums are fp32 and take them unrounded (a second sum, of the
 //   rounded weights, cost 1 to 2% of the time).
-//   What bounds it: conversions and the multiplications by the scales, which share a
-//   pipe (4 + 4 of them and one mma take 15 cycles of an SM's quarter, each of the
-//   three alone 8), then DRAM.  64 sequences of 8192 tokens, 32 heads over 8 of 128:
-//   106.3 us = 5.69 TB/s; the copies alone take 94.  64 sequences of 512 to 8192
-//   tokens with the merge 62.6 us = 5.14 TB/s.
+//   What bounds it at d = 128 with up to 8 heads: conversions and the multiplications
+//   by the scales, which share a pipe (4 + 4 of them and one mma take 15 cycles of an
+//   SM's quarter, each of the three alone 8), then DRAM.  64 sequences of 8192 tokens,
+//   32 heads over 8 of 128: 106.4 us = 5.68 TB/s; the copies alone take 94.  64 sequences
+//   of 512 to 8192 tokens with the merge 62.7 us = 5.13 TB/s.  At d = 64 (64 heads over 8,
+//   the same lengths: 44.8 us = 3.59 TB/s) and with 16 rows (32 sequences, 96 heads over
+//   8: 54.3 us = 2.97 TB/s) no unit is full: the chain of products, vote, exponentials,
+//   transposes and products of few warps is what takes the time.
 //   Small calls (few segments, none long) take a cluster of 8 CTAs for each
 //   segment instead, which take its units in turn and merge through distributed
 //   shared memory: one launch and no workspace (six of up to 1500 tokens 3.9 us).

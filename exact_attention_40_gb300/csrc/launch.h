@@ -210,7 +210,8 @@ constexpr int kFp4MaxCtas = kFp4Sms * 3;  // no grid of the batch's shares is la
 // Three of four computing warps, though registers and shared memory would hold
 // four at d = 64: a batch of 64 x 8192 tokens takes 67.4 us with three, 73.1 with
 // four and 78.2 with two (d = 128, where four would spill: 106, 132 and 109).  Two for
-// 16 heads, whose accumulators fill the registers.
+// 16 heads, whose accumulators fill the registers: 168 of them at d = 128, with four
+// words spilled in the form for small calls and none in the other.
 constexpr __host__ __device__ int fp4_decode_ctas(int rows) { return rows > 8 ? 2 : 3; }
 
 constexpr int kFp4ClusterCtas = 8;      // CTAs of a segment in a small call (the portable cluster size)

@@ -2,8 +2,10 @@
 //
 // Pair i of d/2 turns by position[axis(i)] * theta_i.  u_i = theta_i / (2 pi)
 // is held as a 64-bit fixed-point fraction of a turn (formed on the host in
-// fp64), so the angle in turns is one integer product modulo 2^64: exact for
-// any position, negative ones too.  The angle is brought to |x| <= pi/4 and the
+// fp64), so the angle in turns is one integer product modulo 2^64, for negative
+// positions too, and its reduction loses nothing.  What is left is u's own rounding,
+// some 1e-15 relative and 2^-65 absolute: beyond 10^7 radians it moves an angle by
+// about half an fp32 unit.  The angle is brought to |x| <= pi/4 and the
 // sine and cosine are Taylor sums whose three largest terms are kept with their
 // rounding errors, so that the last rounding gives the nearest fp32 number but for
 // 3 in 10,000 (14 in 1,000 with two such terms).  The 4-bit cache needs that: a key

@@ -302,7 +302,8 @@ int attn_rope_cache_write(void* q, const void* k, const void* v, const int32_t* 
  * inverse != 0 turns the other way, which is the gradient: with the same
  * positions it takes the gradients of the outputs to those of the inputs.
  * Angles are reduced modulo a turn exactly (64-bit fixed point, any int32
- * position), the rotation is in fp32, one rounding to bf16.
+ * position; the frequencies are fp64's, 1e-15 relative), the rotation is in fp32,
+ * one rounding to bf16.
  *   q, q_out [B, Hq, N, d], k, k_out [B, Hkv, N, d] bf16 by their strides, d
  *            contiguous; q_out may be q and k_out k (with the same strides, in
  *            place), no other overlap (an output at the other input's or output's
@@ -393,10 +394,9 @@ int attn_cache_read_fp4(const void* kv_cache, const int32_t* seq_ids, const int3
  * [num_seqs, Hq] fp32 or NULL, block_table, ctx_lens and their checks on the
  * device as attn_decode_paged; keys and values enter exactly, a weight is
  * rounded by at most 2^-11 of itself or 2^-32 of the largest, whichever is more.
- * ctx_len 0 gives out = 0, lse = -inf.  out overlaps no
- * input, and ctx_lens keep their values while the call runs.  scale, k_scale and
- * v_scale are finite and > 0, and so is 2 scale k_scale in fp32
- * (EXATTN_ERR_INVALID_ARG).
+ * ctx_len 0 gives out = 0, lse = -inf.  out overlaps no input, and ctx_lens keep
+ * their values while the call runs.  scale, k_scale and v_scale are finite and > 0,
+ * and so is 2 scale k_scale in fp32 (EXATTN_ERR_INVALID_ARG).
  *   workspace: attn_decode_fp4_workspace_bytes(...) bytes, 16-byte aligned, its
  *   contents clobbered; NULL where that is 0 (also for invalid arguments).
  *   Calls whose executions overlap need one each.
