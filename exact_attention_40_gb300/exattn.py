@@ -130,13 +130,15 @@ def _empty(shape, dtype, device, stream):
     belongs to that one, since a block of the current stream's memory may have uses there
     still to come, and the allocator is told that the current one goes on with it."""
     import torch
-    if stream is None:
+    current = None if stream is None else torch.cuda.current_stream(device)
+    if stream is None or stream.cuda_stream == current.cuda_stream:
         return torch.empty(shape, dtype=dtype, device=device)
-    current = torch.cuda.current_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):  # any object with the handle will do
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device) if stream.cuda_stream \
+            else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
-    if stream != current:
-        t.record_stream(current)
+    t.record_stream(current)
     return t
 
 

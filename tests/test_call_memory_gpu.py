@@ -130,3 +130,20 @@ def test_outputs_dropped_on_the_current_stream_are_not_handed_out_before_their_u
                     torch.full((n,), 0xFF, device=dev, dtype=torch.uint8)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(copies, want))
+
+
+@pytest.mark.parametrize("make", CALLS)
+def test_a_stream_is_any_object_with_its_handle(env, make):
+    """The default stream among them, from a stream that is current instead."""
+    from types import SimpleNamespace
+    torch, ex, dev = env
+    _, call = make(torch, ex, dev)
+    want = [x.clone() for x in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = call(SimpleNamespace(cuda_stream=side.cuda_stream))
+    with torch.cuda.stream(side):
+        back = call(SimpleNamespace(cuda_stream=torch.cuda.default_stream().cuda_stream))
+    torch.cuda.synchronize()
+    for a, b, c in zip(got, back, want):
+        assert torch.equal(a, c) and torch.equal(b, c)
