@@ -20,7 +20,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libexattn.so")
 SOURCES = ["api.cu", "prefill.cu", "decode.cu", "norm.cu", "rope.cu", "backward.cu", "rope_axes.cu",
-           "decode_fp4.cu"]
+           "decode_fp4.cu", "cache_fp8.cu", "decode_fp8.cu"]
 BINDING = os.path.join(HERE, "_binding.so")
 BINDING_KEY = os.path.join(HERE, "_build", "binding.key")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "exattn.h")

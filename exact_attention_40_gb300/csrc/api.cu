@@ -691,8 +691,8 @@ bool same_view(const exattn::HeadView& a, const exattn::HeadView& b) {
   return a.batch == b.batch && a.head == b.head && a.token == b.token;
 }
 
-// Sizes that the 4-bit cache calls share.
-int fp4_sizes(int Hkv, int d, int num_blocks, int num_seqs, int max_blocks_per_seq) {
+// Sizes that the calls on a quantised cache share.
+int quantised_sizes(int Hkv, int d, int num_blocks, int num_seqs, int max_blocks_per_seq) {
   if (Hkv < 1 || num_blocks < 1 || num_seqs < 1 || max_blocks_per_seq < 1) return EXATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return EXATTN_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(max_blocks_per_seq) * exattn::kDecodeBlockSize > (1 << 30)) return EXATTN_ERR_UNSUPPORTED;
@@ -703,6 +703,38 @@ int status_word(unsigned int** status) {
   std::lock_guard<std::mutex> lock(g_mu);
   int dev;
   return device_state(&dev, status);
+}
+
+// Checks the arguments that the reads of the quantised caches share and fills in where
+// their tokens and outputs lie.
+int read_arguments(const void* kv_cache, const int32_t* seq_ids, const int32_t* slots, const int32_t* block_table,
+                   void* k_out, void* v_out, const int64_t* strides, int num_tokens, int Hkv, int d, int num_seqs,
+                   int num_blocks, int max_blocks_per_seq, bool good_scales, exattn::HeadView* k_view,
+                   exattn::HeadView* v_view, exattn::PagedSlots* at) {
+  if (num_tokens < 0 || strides == nullptr) return EXATTN_ERR_INVALID_ARG;
+  int rc = quantised_sizes(Hkv, d, num_blocks, num_seqs, max_blocks_per_seq);
+  if (rc != EXATTN_OK) return rc;
+  if (Hkv > 65535) return EXATTN_ERR_UNSUPPORTED;
+  if (!good_scales) return EXATTN_ERR_INVALID_ARG;
+  if (num_tokens == 0) return EXATTN_OK;
+  if (kv_cache == nullptr || seq_ids == nullptr || slots == nullptr || block_table == nullptr || k_out == nullptr ||
+      v_out == nullptr || k_out == v_out)
+    return EXATTN_ERR_INVALID_ARG;
+  if (!aligned16(kv_cache) || !aligned16(k_out) || !aligned16(v_out) || !aligned4(seq_ids) || !aligned4(slots) ||
+      !aligned4(block_table))
+    return EXATTN_ERR_ALIGNMENT;
+  if ((rc = head_view(k_out, 0, strides[1], strides[0], 1, Hkv, num_tokens, d, true, k_view)) != EXATTN_OK ||
+      (rc = head_view(v_out, 0, strides[3], strides[2], 1, Hkv, num_tokens, d, true, v_view)) != EXATTN_OK)
+    return rc;
+  if ((rc = status_word(&at->status)) != EXATTN_OK) return rc;
+  at->seq_ids = seq_ids;
+  at->slots = slots;
+  at->block_table = block_table;
+  at->num_tokens = num_tokens;
+  at->num_seqs = num_seqs;
+  at->num_blocks = num_blocks;
+  at->max_blocks_per_seq = max_blocks_per_seq;
+  return EXATTN_OK;
 }
 
 }  // namespace
@@ -762,7 +794,7 @@ int attn_rope_cache_write_fp4(const void* q, const void* k, const void* v, void*
                               int max_blocks_per_seq, float base, int per_axis, float k_scale, float v_scale,
                               void* stream) {
   if (num_tokens < 0 || Hq < 0 || strides == nullptr) return EXATTN_ERR_INVALID_ARG;
-  int rc = fp4_sizes(Hkv, d, num_blocks, num_seqs, max_blocks_per_seq);
+  int rc = quantised_sizes(Hkv, d, num_blocks, num_seqs, max_blocks_per_seq);
   if (rc != EXATTN_OK) return rc;
   if (Hq > 65535 || Hkv > 65535) return EXATTN_ERR_UNSUPPORTED;
   if (!good_scale(k_scale) || !good_scale(v_scale)) return EXATTN_ERR_INVALID_ARG;
@@ -810,31 +842,12 @@ int attn_cache_read_fp4(const void* kv_cache, const int32_t* seq_ids, const int3
                         const int32_t* block_table, void* k_out, void* v_out, const int64_t* strides, int num_tokens,
                         int Hkv, int d, int num_seqs, int num_blocks, int max_blocks_per_seq, float k_scale,
                         float v_scale, void* stream) {
-  if (num_tokens < 0 || strides == nullptr) return EXATTN_ERR_INVALID_ARG;
-  int rc = fp4_sizes(Hkv, d, num_blocks, num_seqs, max_blocks_per_seq);
-  if (rc != EXATTN_OK) return rc;
-  if (Hkv > 65535) return EXATTN_ERR_UNSUPPORTED;
-  if (!good_scale(k_scale) || !good_scale(v_scale)) return EXATTN_ERR_INVALID_ARG;
-  if (num_tokens == 0) return EXATTN_OK;
-  if (kv_cache == nullptr || seq_ids == nullptr || slots == nullptr || block_table == nullptr || k_out == nullptr ||
-      v_out == nullptr || k_out == v_out)
-    return EXATTN_ERR_INVALID_ARG;
-  if (!aligned16(kv_cache) || !aligned16(k_out) || !aligned16(v_out) || !aligned4(seq_ids) || !aligned4(slots) ||
-      !aligned4(block_table))
-    return EXATTN_ERR_ALIGNMENT;
   exattn::ReadFp4Args a;
-  if ((rc = head_view(k_out, 0, strides[1], strides[0], 1, Hkv, num_tokens, d, true, &a.k_out)) != EXATTN_OK ||
-      (rc = head_view(v_out, 0, strides[3], strides[2], 1, Hkv, num_tokens, d, true, &a.v_out)) != EXATTN_OK)
-    return rc;
-  if ((rc = status_word(&a.at.status)) != EXATTN_OK) return rc;
+  const int rc = read_arguments(kv_cache, seq_ids, slots, block_table, k_out, v_out, strides, num_tokens, Hkv, d,
+                                num_seqs, num_blocks, max_blocks_per_seq, good_scale(k_scale) && good_scale(v_scale),
+                                &a.k_out, &a.v_out, &a.at);
+  if (rc != EXATTN_OK || num_tokens == 0) return rc;
   a.kv_cache = kv_cache;
-  a.at.seq_ids = seq_ids;
-  a.at.slots = slots;
-  a.at.block_table = block_table;
-  a.at.num_tokens = num_tokens;
-  a.at.num_seqs = num_seqs;
-  a.at.num_blocks = num_blocks;
-  a.at.max_blocks_per_seq = max_blocks_per_seq;
   a.Hkv = Hkv;
   a.d = d;
   a.k_scale = k_scale;
@@ -845,7 +858,7 @@ int attn_cache_read_fp4(const void* kv_cache, const int32_t* seq_ids, const int3
 
 size_t attn_decode_fp4_workspace_bytes(int num_seqs, int Hq, int Hkv, int d, int max_blocks_per_seq) {
   if (num_seqs < 1 || num_seqs > 65535 || Hq < 1 || Hq > 65535 || Hkv < 1 || Hq % Hkv != 0 ||
-      fp4_sizes(Hkv, d, 1, 1, max_blocks_per_seq) != EXATTN_OK)
+      quantised_sizes(Hkv, d, 1, 1, max_blocks_per_seq) != EXATTN_OK)
     return 0;
   const exattn::Fp4Plan plan(num_seqs, Hkv, Hq / Hkv, max_blocks_per_seq);
   return plan.fits ? plan.bytes(d) : 0;
@@ -856,7 +869,7 @@ int attn_decode_paged_fp4(const void* q, const void* kv_cache, const int32_t* bl
                           int max_blocks_per_seq, float scale, float k_scale, float v_scale, void* workspace,
                           size_t workspace_bytes, void* stream) {
   if (num_seqs < 0 || Hq < 1) return EXATTN_ERR_INVALID_ARG;
-  int rc = fp4_sizes(Hkv, d, num_blocks, 1, max_blocks_per_seq);
+  int rc = quantised_sizes(Hkv, d, num_blocks, 1, max_blocks_per_seq);
   if (rc != EXATTN_OK) return rc;
   if (Hq % Hkv != 0 || !good_scale(scale) || !good_scale(k_scale) || !good_scale(v_scale) ||
       !good_scale(static_cast<float>(2.0 * scale * k_scale)))
@@ -881,6 +894,112 @@ int attn_decode_paged_fp4(const void* q, const void* kv_cache, const int32_t* bl
                                 workspace, plan, num_seqs, Hq, Hkv, d, num_blocks, max_blocks_per_seq,
                                 scale, k_scale, v_scale};
   return exattn::launch_decode_fp4(a, g, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXATTN_OK
+                                                                                           : EXATTN_ERR_CUDA;
+}
+
+size_t attn_fp8_cache_bytes(int num_blocks, int Hkv, int d) {
+  if (num_blocks < 1 || Hkv < 1 || (d != 64 && d != 128)) return 0;
+  return static_cast<size_t>(num_blocks) * Hkv * (32 * d + 32);
+}
+
+int attn_rope_cache_write_fp8(const void* q, const void* k, const void* v, void* q_out, const int32_t* token_starts,
+                              const int32_t* ctx_lens, const int32_t* positions, const int32_t* block_table,
+                              void* kv_cache, const int64_t* strides, const int* sections, int num_axes,
+                              int num_tokens, int Hq, int Hkv, int d, int num_seqs, int num_blocks,
+                              int max_blocks_per_seq, float base, int per_axis, void* stream) {
+  if (num_tokens < 0 || Hq < 0 || strides == nullptr) return EXATTN_ERR_INVALID_ARG;
+  int rc = quantised_sizes(Hkv, d, num_blocks, num_seqs, max_blocks_per_seq);
+  if (rc != EXATTN_OK) return rc;
+  if (Hq > 65535 || Hkv > 65535 || num_seqs > 65535) return EXATTN_ERR_UNSUPPORTED;
+  exattn::RopeAxesTable table;
+  if ((rc = rope_table(sections, num_axes, d, base, per_axis, &table)) != EXATTN_OK) return rc;
+  if (token_starts == nullptr && num_tokens != num_seqs) return EXATTN_ERR_INVALID_ARG;
+  if (num_tokens == 0) return EXATTN_OK;
+  if ((Hq > 0 && (q == nullptr || q_out == nullptr)) || k == nullptr || v == nullptr || ctx_lens == nullptr ||
+      positions == nullptr || block_table == nullptr || kv_cache == nullptr ||
+      (Hq > 0 && (q_out == k || q_out == v)))
+    return EXATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) || !aligned16(kv_cache) ||
+      !aligned4(token_starts) || !aligned4(ctx_lens) || !aligned4(positions) || !aligned4(block_table))
+    return EXATTN_ERR_ALIGNMENT;
+  exattn::RopeFp8Args a;
+  const int64_t* s = strides;
+  if ((rc = head_view(q, 0, s[1], s[0], 1, Hq, num_tokens, d, false, &a.q)) != EXATTN_OK ||
+      (rc = head_view(k, 0, s[3], s[2], 1, Hkv, num_tokens, d, false, &a.k)) != EXATTN_OK ||
+      (rc = head_view(v, 0, s[5], s[4], 1, Hkv, num_tokens, d, false, &a.v)) != EXATTN_OK ||
+      (rc = head_view(q_out, 0, s[7], s[6], 1, Hq, num_tokens, d, true, &a.q_out)) != EXATTN_OK)
+    return rc;
+  if (Hq > 0 && q == q_out && !same_view(a.q, a.q_out)) return EXATTN_ERR_INVALID_ARG;
+  a.positions = positions;
+  a.pos_axis = s[8];
+  if (a.pos_axis < 0) return EXATTN_ERR_INVALID_ARG;
+  if ((rc = status_word(&a.status)) != EXATTN_OK) return rc;
+  a.token_starts = token_starts;
+  a.ctx_lens = ctx_lens;
+  a.block_table = block_table;
+  a.kv_cache = kv_cache;
+  a.num_tokens = num_tokens;
+  a.num_seqs = num_seqs;
+  a.num_blocks = num_blocks;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  return exattn::launch_rope_cache_write_fp8(a, table, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? EXATTN_OK
+             : EXATTN_ERR_CUDA;
+}
+
+int attn_cache_read_fp8(const void* kv_cache, const int32_t* seq_ids, const int32_t* slots,
+                        const int32_t* block_table, void* k_out, void* v_out, const int64_t* strides, int num_tokens,
+                        int Hkv, int d, int num_seqs, int num_blocks, int max_blocks_per_seq, void* stream) {
+  exattn::ReadFp8Args a;
+  const int rc = read_arguments(kv_cache, seq_ids, slots, block_table, k_out, v_out, strides, num_tokens, Hkv, d,
+                                num_seqs, num_blocks, max_blocks_per_seq, true, &a.k_out, &a.v_out, &a.at);
+  if (rc != EXATTN_OK || num_tokens == 0) return rc;
+  a.kv_cache = kv_cache;
+  a.Hkv = Hkv;
+  a.d = d;
+  return exattn::launch_cache_read_fp8(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXATTN_OK
+                                                                                            : EXATTN_ERR_CUDA;
+}
+
+size_t attn_decode_fp8_workspace_bytes(int num_seqs, int num_queries, int Hq, int Hkv, int d, int max_blocks_per_seq) {
+  if (num_seqs < 1 || num_seqs > 65535 || num_queries < 1 || num_queries > exattn::kFp8MaxQueries || Hq < 1 ||
+      Hq > 65535 || Hkv < 1 || Hq % Hkv != 0 || quantised_sizes(Hkv, d, 1, 1, max_blocks_per_seq) != EXATTN_OK)
+    return 0;
+  const exattn::Fp8Plan plan(num_seqs, Hkv, num_queries * (Hq / Hkv), max_blocks_per_seq, d);
+  return plan.fits ? plan.bytes(d) : 0;
+}
+
+int attn_decode_paged_fp8(const void* q, const void* kv_cache, const int32_t* block_table, const int32_t* ctx_lens,
+                          void* out, float* lse, int num_seqs, int num_queries, int Hq, int Hkv, int d, int num_blocks,
+                          int max_blocks_per_seq, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (num_seqs < 0 || num_queries < 1 || Hq < 1) return EXATTN_ERR_INVALID_ARG;
+  int rc = quantised_sizes(Hkv, d, num_blocks, 1, max_blocks_per_seq);
+  if (rc != EXATTN_OK) return rc;
+  if (Hq % Hkv != 0 || !good_scale(scale) || !good_scale(2.f * scale)) return EXATTN_ERR_INVALID_ARG;
+  if (num_seqs > 65535 || num_queries > exattn::kFp8MaxQueries || Hq > 65535 ||
+      static_cast<int64_t>(num_seqs) * num_queries * Hq > 0x7FFFFFFF)
+    return EXATTN_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return EXATTN_OK;
+  if (q == nullptr || kv_cache == nullptr || block_table == nullptr || ctx_lens == nullptr || out == nullptr)
+    return EXATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(out) || !aligned4(block_table) || !aligned4(ctx_lens) ||
+      !aligned4(lse))
+    return EXATTN_ERR_ALIGNMENT;
+  const exattn::Fp8Plan plan(num_seqs, Hkv, num_queries * (Hq / Hkv), max_blocks_per_seq, d);
+  if (!plan.fits) return EXATTN_ERR_UNSUPPORTED;
+  const size_t need = plan.bytes(d);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EXATTN_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return EXATTN_ERR_ALIGNMENT;
+  exattn::DeviceGuard g;
+  if ((rc = status_word(&g.status)) != EXATTN_OK) return rc;
+  g.wait_ns = wait_budget_ns();
+  const exattn::DecodeFp8Args a{q,           kv_cache, block_table, ctx_lens, out,        lse,
+                                workspace,   plan,     num_seqs,    num_queries, Hq, Hkv, d, num_blocks,
+                                max_blocks_per_seq, scale};
+  return exattn::launch_decode_fp8(a, g, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXATTN_OK
                                                                                            : EXATTN_ERR_CUDA;
 }
 

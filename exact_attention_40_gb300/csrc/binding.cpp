@@ -1,4 +1,4 @@
-// Compiled half of the Python binding, for the calls around the 4-bit cache and
+// Compiled half of the Python binding, for the calls around the 4-bit and 8-bit caches and
 // multi-axis rotary positions: it checks the tensors, allocates outputs,
 // and calls the C ABI (include/exattn.h) on the tensors' device and stream.
 //
@@ -206,19 +206,28 @@ PyObject* rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// The cache and block table that the 4-bit calls share.
+// A quantised cache, whose spans are `per` d + `more` bytes.
 struct Cache {
   const Tensor& t;
   c10::Device device;
   int num_blocks, Hkv, d;
-  explicit Cache(PyObject* o) : t(tensor(o, "kv_cache", 3, at::kByte)), device(cuda_device(t, "kv_cache")) {
-    if (t.size(2) % 18 != 0 || !t.is_contiguous())
-      fail(PyExc_ValueError, "kv_cache must be contiguous [num_blocks, Hkv, 18 d], got [%lld, %lld, %lld]",
-           static_cast<long long>(t.size(0)), static_cast<long long>(t.size(1)), static_cast<long long>(t.size(2)));
+  Cache(PyObject* o, int per, int more) : t(tensor(o, "kv_cache", 3, at::kByte)), device(cuda_device(t, "kv_cache")) {
+    if (t.size(2) < more || (t.size(2) - more) % per != 0 || !t.is_contiguous())
+      fail(PyExc_ValueError, "kv_cache must be contiguous [num_blocks, Hkv, %d d%s], got [%lld, %lld, %lld]", per,
+           more > 0 ? " + 32" : "", static_cast<long long>(t.size(0)), static_cast<long long>(t.size(1)),
+           static_cast<long long>(t.size(2)));
     num_blocks = narrow(t.size(0), "num_blocks");
     Hkv = narrow(t.size(1), "Hkv");
-    d = narrow(t.size(2) / 18, "d");
+    d = narrow((t.size(2) - more) / per, "d");
   }
+};
+
+struct Fp4Cache : Cache {
+  explicit Fp4Cache(PyObject* o) : Cache(o, 18, 0) {}
+};
+
+struct Fp8Cache : Cache {
+  explicit Fp8Cache(PyObject* o) : Cache(o, 32, 32) {}
 };
 
 // A contiguous int32 tensor.
@@ -232,7 +241,7 @@ const Tensor& indexes(PyObject* o, const char* name, c10::Device device, at::Int
 PyObject* rope_cache_write_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   need_args(n, 15);
-  const Cache c(a[7]);
+  const Fp4Cache c(a[7]);
   const Tensor& q = tensor(a[0], "q", 3, at::kBFloat16);
   const Tensor& k = tensor(a[1], "k", 3, at::kBFloat16);
   const Tensor& v = tensor(a[2], "v", 3, at::kBFloat16);
@@ -268,7 +277,7 @@ PyObject* rope_cache_write_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* cache_read_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   need_args(n, 9);
-  const Cache c(a[0]);
+  const Fp4Cache c(a[0]);
   const Tensor& seq_ids = indexes(a[1], "seq_ids", c.device, {-1});
   const int64_t T = seq_ids.size(0);
   const Tensor& slots = indexes(a[2], "slots", c.device, {T});
@@ -289,11 +298,21 @@ PyObject* cache_read_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A workspace that the caller gave, and its size.
+Tensor given_workspace(PyObject* o, c10::Device device, size_t* bytes) {
+  if (!THPVariable_Check(o)) fail(PyExc_TypeError, "workspace must be a torch.Tensor");
+  const Tensor& t = THPVariable_Unpack(o);
+  if (t.device() != device || !t.is_contiguous())
+    fail(PyExc_ValueError, "workspace must be contiguous on the tensors' device");
+  *bytes = static_cast<size_t>(t.numel()) * t.element_size();
+  return t;
+}
+
 // (q, kv_cache, block_table, ctx_lens, scale, k_scale, v_scale, out, lse, workspace, return_lse, stream)
 PyObject* decode_paged_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   need_args(n, 12);
-  const Cache c(a[1]);
+  const Fp4Cache c(a[1]);
   const Tensor& q = tensor(a[0], "q", 3, at::kBFloat16);
   const int64_t S = q.size(0), Hq = q.size(1);
   check(q, "q", c.device, {S, Hq, c.d}, true);
@@ -312,17 +331,117 @@ PyObject* decode_paged_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     bytes = attn_decode_fp4_workspace_bytes(iS, iHq, c.Hkv, c.d, mb);
     if (bytes > 0) workspace = on.fresh({static_cast<int64_t>(bytes)}, at::kByte);
   } else {
-    if (!THPVariable_Check(a[9])) fail(PyExc_TypeError, "workspace must be a torch.Tensor");
-    workspace = THPVariable_Unpack(a[9]);
-    if (workspace.device() != c.device || !workspace.is_contiguous())
-      fail(PyExc_ValueError, "workspace must be contiguous on the tensors' device");
-    bytes = static_cast<size_t>(workspace.numel()) * workspace.element_size();
+    workspace = given_workspace(a[9], c.device, &bytes);
   }
   on.launch("attn_decode_paged_fp4", [&](void* s) {
     return attn_decode_paged_fp4(q.const_data_ptr(), c.t.const_data_ptr(), ints(table), ints(ctx_lens), out.data_ptr(),
                                  lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, iS, iHq, c.Hkv, c.d,
                                  c.num_blocks, mb, scale, k_scale, v_scale,
                                  workspace.defined() ? workspace.data_ptr() : nullptr, bytes, s);
+  });
+  return pair(out, lse);
+  END_HANDLE_TH_ERRORS
+}
+
+// (q, k, v, token_starts, ctx_lens, positions, block_table, kv_cache, sections, base, per_axis, q_out, stream)
+PyObject* rope_cache_write_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  need_args(n, 13);
+  const Fp8Cache c(a[7]);
+  const Tensor& q = tensor(a[0], "q", 3, at::kBFloat16);
+  const Tensor& k = tensor(a[1], "k", 3, at::kBFloat16);
+  const Tensor& v = tensor(a[2], "v", 3, at::kBFloat16);
+  const int64_t T = q.size(0), Hq = q.size(1);
+  check(q, "q", c.device, {T, Hq, c.d}, false);
+  check(k, "k", c.device, {T, c.Hkv, c.d}, false);
+  check(v, "v", c.device, {T, c.Hkv, c.d}, false);
+  const Sections sections(a[8]);
+  const Tensor& table = indexes(a[6], "block_table", c.device, {-1, -1});
+  const int64_t S = table.size(0);
+  const Tensor& ctx_lens = indexes(a[4], "ctx_lens", c.device, {S});
+  const int32_t* starts = nullptr;
+  if (a[3] != Py_None) {
+    starts = ints(indexes(a[3], "token_starts", c.device, {S + 1}));
+  } else if (T != S) {
+    fail(PyExc_ValueError, "without token_starts each of the %lld sequences has one token, got %lld",
+         static_cast<long long>(S), static_cast<long long>(T));
+  }
+  const Tensor& positions = indexes(a[5], "positions", c.device, {sections.count, T});
+  const Target on(c.device, a[12]);
+  const Tensor qo = on.output(a[11], "q_out", q.sizes(), at::kBFloat16, false);
+  const int64_t strides[9] = {q.stride(0), q.stride(1),  k.stride(0),  k.stride(1), v.stride(0),
+                              v.stride(1), qo.stride(0), qo.stride(1), T};
+  const float base = static_cast<float>(number(a[9]));
+  const int per_axis = truth(a[10]);
+  const int iT = narrow(T, "num_tokens"), iHq = narrow(Hq, "Hq"), iS = narrow(S, "num_seqs"),
+            mb = narrow(table.size(1), "max_blocks_per_seq");
+  on.launch("attn_rope_cache_write_fp8", [&](void* s) {
+    return attn_rope_cache_write_fp8(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), qo.data_ptr(), starts,
+                                     ints(ctx_lens), ints(positions), ints(table), c.t.data_ptr(), strides,
+                                     sections.size, sections.count, iT, iHq, c.Hkv, c.d, iS, c.num_blocks, mb, base,
+                                     per_axis, s);
+  });
+  return THPVariable_Wrap(qo);
+  END_HANDLE_TH_ERRORS
+}
+
+// (kv_cache, seq_ids, slots, block_table, k_out, v_out, stream)
+PyObject* cache_read_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  need_args(n, 7);
+  const Fp8Cache c(a[0]);
+  const Tensor& seq_ids = indexes(a[1], "seq_ids", c.device, {-1});
+  const int64_t T = seq_ids.size(0);
+  const Tensor& slots = indexes(a[2], "slots", c.device, {T});
+  const Tensor& table = indexes(a[3], "block_table", c.device, {-1, -1});
+  const std::array<int64_t, 3> shape = {T, c.Hkv, c.d};
+  const Target on(c.device, a[6]);
+  const Tensor ko = on.output(a[4], "k_out", shape, at::kBFloat16, false);
+  const Tensor vo = on.output(a[5], "v_out", shape, at::kBFloat16, false);
+  const int64_t strides[4] = {ko.stride(0), ko.stride(1), vo.stride(0), vo.stride(1)};
+  const int iT = narrow(T, "num_tokens"), S = narrow(table.size(0), "num_seqs"),
+            mb = narrow(table.size(1), "max_blocks_per_seq");
+  on.launch("attn_cache_read_fp8", [&](void* s) {
+    return attn_cache_read_fp8(c.t.const_data_ptr(), ints(seq_ids), ints(slots), ints(table), ko.data_ptr(),
+                               vo.data_ptr(), strides, iT, c.Hkv, c.d, S, c.num_blocks, mb, s);
+  });
+  return pair(ko, vo);
+  END_HANDLE_TH_ERRORS
+}
+
+// (q, kv_cache, block_table, ctx_lens, scale, out, lse, workspace, return_lse, stream)
+PyObject* decode_paged_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  need_args(n, 10);
+  const Fp8Cache c(a[1]);
+  const bool many = THPVariable_Check(a[0]) && THPVariable_Unpack(a[0]).dim() == 4;
+  const Tensor& q = tensor(a[0], "q", many ? 4 : 3, at::kBFloat16);
+  const int64_t S = q.size(0), N = many ? q.size(1) : 1, Hq = q.size(-2);
+  if (q.size(-1) != c.d)
+    fail(PyExc_ValueError, "q's heads have %lld columns, the cache's %d", static_cast<long long>(q.size(-1)), c.d);
+  check(q, "q", c.device, {}, true);
+  const Tensor& table = indexes(a[2], "block_table", c.device, {S, -1});
+  const Tensor& ctx_lens = indexes(a[3], "ctx_lens", c.device, {S});
+  const float scale = static_cast<float>(a[4] == Py_None ? 1.0 / std::sqrt(static_cast<double>(c.d)) : number(a[4]));
+  const Target on(c.device, a[9]);
+  const Tensor out = on.output(a[5], "out", q.sizes(), at::kBFloat16, true);
+  Tensor lse;
+  if (a[6] != Py_None || truth(a[8])) lse = on.output(a[6], "lse", q.sizes().slice(0, q.dim() - 1), at::kFloat, true);
+  const int iS = narrow(S, "num_seqs"), iN = narrow(N, "num_queries"), iHq = narrow(Hq, "Hq"),
+            mb = narrow(table.size(1), "max_blocks_per_seq");
+  size_t bytes = 0;
+  Tensor workspace;
+  if (a[7] == Py_None) {
+    bytes = attn_decode_fp8_workspace_bytes(iS, iN, iHq, c.Hkv, c.d, mb);
+    if (bytes > 0) workspace = on.fresh({static_cast<int64_t>(bytes)}, at::kByte);
+  } else {
+    workspace = given_workspace(a[7], c.device, &bytes);
+  }
+  on.launch("attn_decode_paged_fp8", [&](void* s) {
+    return attn_decode_paged_fp8(q.const_data_ptr(), c.t.const_data_ptr(), ints(table), ints(ctx_lens), out.data_ptr(),
+                                 lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, iS, iN, iHq, c.Hkv, c.d,
+                                 c.num_blocks, mb, scale, workspace.defined() ? workspace.data_ptr() : nullptr, bytes,
+                                 s);
   });
   return pair(out, lse);
   END_HANDLE_TH_ERRORS
@@ -338,6 +457,9 @@ PyMethodDef kMethods[] = {
     {"rope_cache_write_fp4", reinterpret_cast<PyCFunction>(rope_cache_write_fp4), METH_FASTCALL, nullptr},
     {"cache_read_fp4", reinterpret_cast<PyCFunction>(cache_read_fp4), METH_FASTCALL, nullptr},
     {"decode_paged_fp4", reinterpret_cast<PyCFunction>(decode_paged_fp4), METH_FASTCALL, nullptr},
+    {"rope_cache_write_fp8", reinterpret_cast<PyCFunction>(rope_cache_write_fp8), METH_FASTCALL, nullptr},
+    {"cache_read_fp8", reinterpret_cast<PyCFunction>(cache_read_fp8), METH_FASTCALL, nullptr},
+    {"decode_paged_fp8", reinterpret_cast<PyCFunction>(decode_paged_fp8), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -48,6 +48,7 @@
 
 #include <type_traits>
 
+#include "decode_shares.cuh"
 #include "fp4.cuh"
 #include "launch.h"
 #include "ptx.cuh"
@@ -58,27 +59,27 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;       // that compute; one warp more copies
 constexpr int kCtaThreads = kThreads + 32;
-constexpr int kMergeThreads = 256;
 constexpr int kStages = 3;  // units in flight
 constexpr int kBlk = kDecodeBlockSize;
 constexpr int kUnit = kFp4UnitBlocks;
 static_assert(kUnit == 2 * kWarps, "a pair of blocks per warp");
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kWhole = static_cast<int>(0x80000000u);
-constexpr float kNoScore = -3.0e38f;     // below any score; -inf would give inf - inf
 // Weights are 2^(score - reference), the reference kLift below the running maximum that it
 // was taken from, and a new one taken once a score passes it by more than kMost: fp16
 // holds weights of up to 2^15.
 constexpr float kLift = 7.f;
 constexpr float kMost = 15.f;
 
+using Batch = BatchOf<kUnit>;
+
+__device__ __forceinline__ int units_of(int ctx) { return exattn::units_of<kUnit>(ctx); }
+
 struct Fp4SplitParams {
   const __nv_bfloat16* q;
   const uint8_t* cache;
   const int32_t* block_table;
   const int32_t* ctx_lens;
-  Fp4Joint* joints;  // one per CTA: its last segment, where others go on with it; or NULL
+  SegmentJoint* joints;  // one per CTA: its last segment, where others go on with it; or NULL
   float* ws_o;    // [2 * ctas][rows][d]
   float* ws_lse;  // [2 * ctas][rows]
   __nv_bfloat16* out;
@@ -89,79 +90,6 @@ struct Fp4SplitParams {
   float scale_log2;       // scale * k_scale * log2 e
   float v_scale;
 };
-
-__device__ __forceinline__ int clamp_ctx(int n, int max_ctx, unsigned int* status) {
-  if (n < 0 || n > max_ctx) {
-    atomicOr(status, 2u);  // EXATTN_DEVICE_BOUNDS_BIT
-    n = n < 0 ? 0 : max_ctx;
-  }
-  return n;
-}
-
-__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The same product without a sum before it.
-__device__ __forceinline__ void mma_f16_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                                    uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%10, %10, %10, %10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-// Transposes an 8x8 matrix of 16-bit elements held one row per four lanes.
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
-// c0, c1 times f[0], f[1], rounded, and their distances x0, x1 from m[0], m[1].  (Packed,
-// so that the products cost no more than the one fused operation for each score.)
-__device__ __forceinline__ void scores_and_distances(float& c0, float& c1, const float (&f)[2], const float (&m)[2],
-                                                     float& x0, float& x1) {
-  const uint64_t p = f2_mul(f2_pack(c0, c1), f2_pack(f[0], f[1]));
-  f2_unpack(p, c0, c1);
-  f2_unpack(f2_sub(p, f2_pack(m[0], m[1])), x0, x1);
-}
-
-// Loads from shared memory at addr + kOff (the offset is part of the instruction).
-template <int kOff, int W>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[W]) {
-  if constexpr (W == 4) {
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4 + %5];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(addr), "n"(kOff));
-  } else if constexpr (W == 2) {
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2 + %3];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr), "n"(kOff));
-  } else {
-    asm volatile("ld.shared.b32 %0, [%1 + %2];" : "=r"(w[0]) : "r"(addr), "n"(kOff));
-  }
-}
-
-template <int kOff>
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1 + %2];" : "=r"(v) : "r"(addr), "n"(kOff));
-  return v;
-}
-
-template <int kOff>
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint32_t v;
-  asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1 + %2];\n\tcvt.u32.u16 %0, h;\n\t}"
-               : "=r"(v)
-               : "r"(addr), "n"(kOff));
-  return v;
-}
 
 template <int D, int NT>
 struct Fp4Smem {
@@ -181,186 +109,6 @@ __device__ __forceinline__ void compute_barrier() {
   asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
 
-// Equal contiguous shares of `total` places for `parts` CTAs, the first
-// total % parts of them one larger.  (The host keeps totals below 2^31.)
-struct Shares {
-  int base, extra, parts;
-  __device__ __forceinline__ Shares(int total, int n) : base(total / n), extra(total % n), parts(n) {}
-  __device__ __forceinline__ int begin(int c) const { return c * base + min(c, extra); }
-  __device__ __forceinline__ int owner(int place) const {
-    const int large = extra * (base + 1);
-    const int c = place < large ? place / (base + 1) : extra + (place - large) / max(1, base);
-    return max(0, min(parts - 1, c));
-  }
-};
-
-// A place in the numbering of all segments: unit k of `units` of segment (seq, head,
-// chunk), or (k == units) the place that stands for the segment's end.
-struct Place {
-  int seq, head, chunk, k, units, ctx;
-};
-
-__device__ __forceinline__ int units_of(int ctx) { return (ctx + kUnit * kBlk - 1) / (kUnit * kBlk); }
-
-// Places of a segment: its units and one for its end, whose merge and change of
-// queries take a CTA 2400 cycles, about what a unit does (2100).  (With units alone the
-// CTAs that got the short sequences of a batch were the last to finish: 128 sequences
-// of 1 to 2000 tokens took 45.8 us, 38.4 with the ends counted.)
-__device__ __forceinline__ int places_of(int ctx) { return units_of(ctx) + (ctx > 0 ? 1 : 0); }
-
-// Sums over the sequences that a warp forms from ctx_lens, each lane holding those of a
-// contiguous range of them.  In a large batch the warp reads 32 neighbours together: with
-// every lane reading its own range, no two of a load's addresses share a line, and 4096
-// sequences took each CTA 40 us before its first copy.  (Lengths are read more than
-// once; if another stream changes them meanwhile the result is undefined, but every
-// place that comes out is clamped to one that exists.)
-struct Batch {
-  const int32_t* ctx_lens;
-  int max_ctx, num_seqs;
-  int range;                     // sequences per lane; a multiple of 32 where the warp reads them together
-  int lane_begin, before, mine;  // this lane's first sequence, the places before it, in its range
-  int first_ctx;                 // of its first sequence (small batches)
-  int per_segment;               // places of all sequences (of one segment of each)
-
-  static constexpr int kAlone = 4;  // longest range that a lane reads by itself
-
-  // Clamped without a word: whoever handles the sequence reports it.
-  __device__ __forceinline__ int ctx_of(int s) const { return max(0, min(max_ctx, __ldg(ctx_lens + s))); }
-  __device__ __forceinline__ int places_at(int s, int end) const { return s < end ? places_of(ctx_of(s)) : 0; }
-
-  __device__ __forceinline__ Batch(const int32_t* lens, int seqs, int longest) {
-    ctx_lens = lens;
-    num_seqs = seqs;
-    max_ctx = longest;
-    const int lane = threadIdx.x & 31;
-    const bool alone = seqs <= 32 * kAlone;
-    range = alone ? (seqs + 31) / 32 : (seqs + 1023) / 1024 * 32;
-    lane_begin = min(seqs, lane * range);
-    first_ctx = mine = 0;
-    if (alone) {
-      const int end = min(seqs, lane_begin + range);
-      if (lane_begin < end) first_ctx = ctx_of(lane_begin);
-      mine = places_of(first_ctx);
-#pragma unroll
-      for (int i = 1; i < kAlone; ++i) mine += places_at(lane_begin + i, end);
-    } else {
-      const int groups = (seqs + 31) / 32, per_lane = range / 32;
-      int owner = 0, left = per_lane;
-#pragma unroll 8
-      for (int i = 0; i < groups; ++i) {
-        const int sum = __reduce_add_sync(0xffffffffu, places_at(32 * i + lane, seqs));
-        if (lane == owner) mine += sum;
-        if (--left == 0) {
-          left = per_lane;
-          ++owner;
-        }
-      }
-    }
-    int upto = mine;  // inclusive sum over the lanes
-#pragma unroll
-    for (int x = 1; x < 32; x *= 2) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, x);
-      if (lane >= x) upto += v;
-    }
-    per_segment = __shfl_sync(0xffffffffu, upto, 31);
-    before = upto - mine;
-  }
-
-  // The unit or end at a place (below per_segment * segs); whole warp, same place.
-  __device__ __forceinline__ Place find(int place, int segs, int n_chunks) const {
-    const int target = place / segs;
-    const unsigned int owners = __ballot_sync(0xffffffffu, before <= target && target < before + mine);
-    const int lane = max(0, __ffs(owners) - 1);
-    Place p;
-    int prefix;
-    if (num_seqs <= 32 * kAlone) {
-      int s = lane_begin, ctx = first_ctx;
-      prefix = before;
-      if ((threadIdx.x & 31) == lane)
-        while (target >= prefix + places_of(ctx) && s + 1 < num_seqs) {
-          prefix += places_of(ctx);
-          ctx = ctx_of(++s);
-        }
-      p.seq = min(num_seqs - 1, __shfl_sync(0xffffffffu, s, lane));
-      p.ctx = __shfl_sync(0xffffffffu, ctx, lane);
-      prefix = __shfl_sync(0xffffffffu, prefix, lane);
-    } else {
-      const int end = min(num_seqs, (lane + 1) * range);
-      int base = lane * range;
-      prefix = __shfl_sync(0xffffffffu, before, lane);
-      while (true) {  // 32 sequences at a time; one of the range has the place
-        const int n = places_at(base + (threadIdx.x & 31), end);
-        int upto = n;
-#pragma unroll
-        for (int x = 1; x < 32; x *= 2) {
-          const int v = __shfl_up_sync(0xffffffffu, upto, x);
-          if ((threadIdx.x & 31) >= x) upto += v;
-        }
-        const unsigned int past = __ballot_sync(0xffffffffu, target < prefix + upto);
-        if (past != 0 || base + 32 >= end) {
-          const int at = past != 0 ? __ffs(past) - 1 : 0;
-          prefix += __shfl_sync(0xffffffffu, upto - n, at);
-          p.seq = min(num_seqs - 1, base + at);
-          break;
-        }
-        prefix += __shfl_sync(0xffffffffu, upto, 31);
-        base += 32;
-      }
-      p.ctx = ctx_of(p.seq);
-    }
-    p.units = max(1, units_of(p.ctx));
-    const int rest = max(0, place - prefix * segs);
-    const int y = min(segs - 1, rest / (p.units + 1));
-    p.k = min(p.units, rest - y * (p.units + 1));
-    p.head = n_chunks == 1 ? y : y / n_chunks;
-    p.chunk = y - p.head * n_chunks;
-    return p;
-  }
-
-  // The places before a sequence, per segment; whole warp, same s.
-  __device__ __forceinline__ int before_seq(int s) const {
-    const int lane = s / range;
-    int prefix = before, ctx = first_ctx;
-    if (num_seqs <= 32 * kAlone) {
-      if ((threadIdx.x & 31) == lane)
-        for (int i = lane_begin; i < s; ctx = ctx_of(++i)) prefix += places_of(ctx);
-      return __shfl_sync(0xffffffffu, prefix, lane);
-    }
-    int sum = 0;
-    for (int i = lane * range + (threadIdx.x & 31); i < s; i += 32) sum += places_of(ctx_of(i));
-    return __shfl_sync(0xffffffffu, prefix, lane) + __reduce_add_sync(0xffffffffu, sum);
-  }
-};
-
-// Waits for every thread of the cluster; shared memory written before is seen after.
-// Not the .aligned form: that needs the warp's lanes together, and after a loop
-// that some of them left early nothing says they are.
-__device__ __forceinline__ void cluster_barrier() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// Loads from the shared memory of the cluster's CTA `rank`, at an address of one's own.
-__device__ __forceinline__ float4 cluster_load4(const void* own, uint32_t rank) {
-  float4 v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
-      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
-      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-      : "r"(smem_u32(own)), "r"(rank)
-      : "memory");
-  return v;
-}
-
-__device__ __forceinline__ float cluster_load(const void* own, uint32_t rank) {
-  float v;
-  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-               : "=f"(v)
-               : "r"(smem_u32(own)), "r"(rank)
-               : "memory");
-  return v;
-}
-
 template <int D, int NT, bool kCluster>
 __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_fp4_split_kernel(const Fp4SplitParams p) {
   using Span = Fp4Span<D>;
@@ -370,7 +118,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
   constexpr int kMTiles = D / 16;    // mma row tiles of O^T
   constexpr int kKeyWords = D / 32;  // 32-bit words of a lane's key codes per token
   constexpr int kValWords = D / 64;  // ... value codes
-  constexpr int kStep = kCluster ? kFp4ClusterCtas : 1;  // from a CTA's unit to its next
+  constexpr int kStep = kCluster ? kSplitClusterCtas : 1;  // from a CTA's unit to its next
 
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
@@ -419,7 +167,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
   Place at;             // the next unit to compute
   int left;             // units (in a cluster) or places of this CTA that are not yet computed
   int joint_parts = 0;  // CTAs after this one that its last segment goes on in (warp 0)
-  const uint32_t rank = kCluster ? cta % kFp4ClusterCtas : 0;
+  const uint32_t rank = kCluster ? cta % kSplitClusterCtas : 0;
   // Sequences without a cached token: o = 0, lse = -inf.  A lane looks at one, the
   // warp clears what is found.  (Every sequence's length passes here once, so that
   // one out of range is reported.)
@@ -459,8 +207,8 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
   if constexpr (kCluster) {
     // Every 8th unit, so that the table entries and queries need not wait for the
     // context length: the three loads are in flight together.
-    static_assert(kFp4ClusterUnits / kFp4ClusterCtas <= 32 / kUnit, "one batch of table entries");
-    const int seg = cta / kFp4ClusterCtas;
+    static_assert(kFp4ClusterUnits / kSplitClusterCtas <= 32 / kUnit, "one batch of table entries");
+    const int seg = cta / kSplitClusterCtas;
     at.seq = seg / segs;
     at.head = seg % segs / p.n_chunks;
     at.chunk = seg % p.n_chunks;
@@ -923,7 +671,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
     if (left == 0) {
       // the only segment that can go on into further CTAs is the last
       if (!kCluster && p.joints != nullptr && starts && !ends && threadIdx.x == 0)
-        p.joints[cta] = Fp4Joint{cta, joint_parts, static_cast<int>(row0), rows_here};
+        p.joints[cta] = SegmentJoint{cta, joint_parts, static_cast<int>(row0), rows_here};
       break;
     }
     buf ^= 1;
@@ -934,23 +682,23 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
     const int rows_here = rows_of(at);
     const size_t row0 = row_of(at);
     cluster_barrier();
-    for (int idx = threadIdx.x * kFp4ClusterCtas + rank; idx < rows_here * (D / 4); idx += kThreads * kFp4ClusterCtas) {
+    for (int idx = threadIdx.x * kSplitClusterCtas + rank; idx < rows_here * (D / 4); idx += kThreads * kSplitClusterCtas) {
       const int r = idx / (D / 4), col = idx % (D / 4) * 4;
-      float ls[kFp4ClusterCtas];
-      float4 part[kFp4ClusterCtas];
+      float ls[kSplitClusterCtas];
+      float4 part[kSplitClusterCtas];
 #pragma unroll
-      for (int i = 0; i < kFp4ClusterCtas; ++i) {
+      for (int i = 0; i < kSplitClusterCtas; ++i) {
         ls[i] = cluster_load(cluster_lse + r, i);
         part[i] = cluster_load4(cluster_o + r * D + col, i);
       }
       float M = ls[0];
 #pragma unroll
-      for (int i = 1; i < kFp4ClusterCtas; ++i) M = max_nan(M, ls[i]);
+      for (int i = 1; i < kSplitClusterCtas; ++i) M = max_nan(M, ls[i]);
       const float ref = M == -INFINITY ? 0.f : M;
       float W = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < kFp4ClusterCtas; ++i) {
+      for (int i = 0; i < kSplitClusterCtas; ++i) {
         const float w = ex2_approx((ls[i] - ref) * kLog2e);
         W += w;
         o.x = fmaf(w, part[i].x, o.x);
@@ -969,121 +717,9 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
   }
 }
 
-struct Fp4CombineParams {
-  const Fp4Joint* joints;  // one per CTA of the split kernel, or NULL (kFind): one CTA row per segment
-  const int32_t* ctx_lens;
-  const float* ws_o;
-  const float* ws_lse;
-  __nv_bfloat16* out;
-  float* lse;
-  int num_seqs, Hq, segs, n_chunks, group, max_blocks_per_seq, ctas;
-  int rows;  // query heads per segment, at most
-};
-
-// One CTA per (row, segment that several CTAs share): its partial outputs O_i
-// lie in the second place of the CTA where it starts and the first places of
-// the `more` that follow; L = log sum_i exp(lse_i), o = sum_i exp(lse_i - L) O_i.
-// Where segments are few (kFind) it finds them from ctx_lens, while the split kernel
-// still runs; else it reads what that wrote down.  Registers: with 40, not 64, where it
-// reads (64 sequences of 512 to 8192 tokens 62.7 us, 63.7); with 48 where it finds: 66
-// would leave it no room beside a split kernel for 16 heads (32 sequences of 96 heads
-// 59.7 us, 55.4 with 48), and fewer slow the search (one of 8000 tokens 8.4 us with 66,
-// 8.8 with 48, 9.1 with 40).  The weights are formed once, one
-// per thread; D/4 threads take four columns each of every kTeams-th partial output,
-// the first ones' loads on their way before the weights are known.
 template <int D, bool kFind>
-__global__ void __launch_bounds__(kMergeThreads, kFind ? 5 : 6) decode_fp4_combine_kernel(const Fp4CombineParams p) {
-  constexpr int kTeams = kMergeThreads / (D / 4);
-  constexpr int kMergeWarps = kMergeThreads / 32;
-  constexpr int kEarly = 3;
-  __shared__ float weight[kFp4MaxCtas];
-  __shared__ float top[kMergeWarps], sum[kMergeWarps];
-  __shared__ float4 part[kTeams][D / 4];
-  __shared__ Fp4Joint found;
-  const int r = blockIdx.x;
-  if constexpr (kFind) {
-    if (threadIdx.x < 32) {
-      const Batch seqs(p.ctx_lens, p.num_seqs, p.max_blocks_per_seq * kBlk);
-      const Shares shares(seqs.per_segment * p.segs, p.ctas);
-      const int seq = blockIdx.y / p.segs, y = blockIdx.y % p.segs;
-      const int ctx = seqs.ctx_of(seq), units = units_of(ctx);
-      const int unit = seqs.before_seq(seq) * p.segs + y * places_of(ctx);  // the place of its first
-      if (threadIdx.x == 0) {
-        found.cta = units > 0 ? shares.owner(unit) : 0;
-        found.more = units > 0 ? shares.owner(unit + units - 1) - found.cta : 0;
-        found.row = seq * p.Hq + y / p.n_chunks * p.group + y % p.n_chunks * p.rows;
-        found.rows = min(p.rows, p.group - y % p.n_chunks * p.rows);
-      }
-    }
-    __syncthreads();
-  }
-  cudaGridDependencySynchronize();  // launched while the split kernel runs, after all before that had ended
-  const Fp4Joint joint = kFind ? found : p.joints[blockIdx.y];
-  if (joint.more == 0 || r >= joint.rows) return;
-  const int used = joint.more + 1;
-  auto place = [&](int i) { return static_cast<size_t>(2 * (joint.cta + i) + (i == 0 ? 1 : 0)) * p.rows + r; };
-  const int col = threadIdx.x % (D / 4), team = threadIdx.x / (D / 4);
-  auto part_of = [&](int s) { return reinterpret_cast<const float4*>(p.ws_o + place(s) * D)[col]; };
-  float4 early[kEarly];
-#pragma unroll
-  for (int i = 0; i < kEarly; ++i)
-    early[i] = team + i * kTeams < used ? part_of(team + i * kTeams) : make_float4(0.f, 0.f, 0.f, 0.f);
-  float M = -INFINITY;
-  for (int s = threadIdx.x; s < used; s += kMergeThreads) {
-    const float ls = p.ws_lse[place(s)];
-    weight[s] = ls;
-    M = max_nan(M, ls);
-  }
-#pragma unroll
-  for (int x = 1; x < 32; x *= 2) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, x));
-  if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = M;
-  __syncthreads();
-  M = top[0];
-#pragma unroll
-  for (int w = 1; w < kMergeWarps; ++w) M = max_nan(M, top[w]);
-  const float ref = M == -INFINITY ? 0.f : M;  // all weights 0 where no part sees anything
-  float W = 0.f;
-  for (int s = threadIdx.x; s < used; s += kMergeThreads) {
-    const float w = ex2_approx((weight[s] - ref) * kLog2e);
-    weight[s] = w;
-    W += w;
-  }
-#pragma unroll
-  for (int x = 1; x < 32; x *= 2) W += __shfl_xor_sync(0xffffffffu, W, x);
-  if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = W;
-  __syncthreads();
-  W = 0.f;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) W += sum[w];
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float w, const float4& a) {
-    o.x = fmaf(w, a.x, o.x);
-    o.y = fmaf(w, a.y, o.y);
-    o.z = fmaf(w, a.z, o.z);
-    o.w = fmaf(w, a.w, o.w);
-  };
-#pragma unroll
-  for (int i = 0; i < kEarly; ++i)
-    if (team + i * kTeams < used) add(weight[team + i * kTeams], early[i]);
-#pragma unroll 4
-  for (int s = team + kEarly * kTeams; s < used; s += kTeams) add(weight[s], part_of(s));
-  part[team][col] = o;
-  __syncthreads();
-  if (threadIdx.x < D / 4) {
-#pragma unroll
-    for (int x = 1; x < kTeams; ++x) {
-      const float4 a = part[x][col];
-      o.x += a.x;
-      o.y += a.y;
-      o.z += a.z;
-      o.w += a.w;
-    }
-    const float inv = W == 0.f ? 0.f : 1.f / W;
-    const size_t row = static_cast<size_t>(joint.row) + r;
-    reinterpret_cast<uint2*>(p.out + row * D)[col] =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (p.lse != nullptr && col == 0) p.lse[row] = W == 0.f ? -INFINITY : M + __logf(W);
-  }
+__global__ void __launch_bounds__(kMergeThreads, kFind ? 5 : 6) decode_fp4_combine_kernel(const MergeParams p) {
+  merge_segment<D, kUnit, kFind, false>(p);
 }
 
 template <int D, int NT, bool kCluster>
@@ -1094,7 +730,7 @@ cudaError_t launch_split(const Fp4SplitParams& sp, int ctas, cudaStream_t stream
                                   static_cast<int>(smem), smem_set);
   if (e != cudaSuccess) return e;
   return launch_overlapped(decode_fp4_split_kernel<D, NT, kCluster>, ctas, kCtaThreads, smem, stream,
-                           kCluster ? kFp4ClusterCtas : 1, sp);
+                           kCluster ? kSplitClusterCtas : 1, sp);
 }
 
 template <int D>
@@ -1106,7 +742,7 @@ cudaError_t launch_d(const DecodeFp4Args& a, const DeviceGuard& g, cudaStream_t 
   sp.block_table = a.block_table;
   sp.ctx_lens = a.ctx_lens;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  sp.joints = plan.joints > 0 ? reinterpret_cast<Fp4Joint*>(ws) : nullptr;
+  sp.joints = plan.joints > 0 ? reinterpret_cast<SegmentJoint*>(ws) : nullptr;
   sp.ws_o = reinterpret_cast<float*>(ws + plan.joint_bytes());
   sp.ws_lse = reinterpret_cast<float*>(ws + plan.joint_bytes() + plan.part_bytes(D));
   sp.out = static_cast<__nv_bfloat16*>(a.out);
@@ -1129,7 +765,7 @@ cudaError_t launch_d(const DecodeFp4Args& a, const DeviceGuard& g, cudaStream_t 
                                        : launch_split<D, 2, false>(sp, plan.ctas, stream);
   if (e != cudaSuccess || !plan.shared) return e;
 
-  Fp4CombineParams cp;
+  MergeParams cp;
   cp.joints = sp.joints;
   cp.ctx_lens = a.ctx_lens;
   cp.ws_o = sp.ws_o;
@@ -1141,6 +777,7 @@ cudaError_t launch_d(const DecodeFp4Args& a, const DeviceGuard& g, cudaStream_t 
   cp.segs = a.Hkv * plan.chunks;
   cp.n_chunks = plan.chunks;
   cp.group = sp.group;
+  cp.queries = 1;
   cp.max_blocks_per_seq = a.max_blocks_per_seq;
   cp.ctas = plan.ctas;
   cp.rows = plan.rows;

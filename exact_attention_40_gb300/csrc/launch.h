@@ -170,8 +170,8 @@ struct RopeAxesArgs {
 
 cudaError_t launch_rope_axes(const RopeAxesArgs& a, const RopeAxesTable& table, cudaStream_t stream);
 
-// Where the tokens of the 4-bit cache calls lie.
-struct Fp4Slots {
+// Where the tokens of a call on a quantised cache lie.
+struct PagedSlots {
   const int32_t* seq_ids;      // [num_tokens]
   const int32_t* slots;        // [num_tokens]: token index within its sequence
   const int32_t* block_table;  // [num_seqs, max_blocks_per_seq]
@@ -185,7 +185,7 @@ struct RopeFp4Args {
   const int32_t* positions;
   long long pos_axis;       // stride between axes, in elements
   void* kv_cache;           // [num_blocks, Hkv, 18 d]
-  Fp4Slots at;
+  PagedSlots at;
   int Hq, Hkv, d;
   float k_scale, v_scale;
 };
@@ -195,16 +195,92 @@ cudaError_t launch_rope_cache_write_fp4(const RopeFp4Args& a, const RopeAxesTabl
 struct ReadFp4Args {
   const void* kv_cache;
   HeadView k_out, v_out;  // batch stride unused
-  Fp4Slots at;
+  PagedSlots at;
   int Hkv, d;
   float k_scale, v_scale;
 };
 
 cudaError_t launch_cache_read_fp4(const ReadFp4Args& a, cudaStream_t stream);
 
+struct RopeFp8Args {
+  HeadView q, k, v, q_out;      // batch stride unused
+  const int32_t* token_starts;  // [num_seqs + 1], or NULL: one token for each sequence
+  const int32_t* ctx_lens;      // [num_seqs], the new tokens among them
+  const int32_t* positions;
+  long long pos_axis;           // stride between axes, in elements
+  const int32_t* block_table;   // [num_seqs, max_blocks_per_seq]
+  void* kv_cache;               // [num_blocks, Hkv, 32 d + 32]
+  unsigned int* status;         // device status word
+  int num_tokens, num_seqs, num_blocks, max_blocks_per_seq, Hq, Hkv, d;
+};
+
+cudaError_t launch_rope_cache_write_fp8(const RopeFp8Args& a, const RopeAxesTable& table, cudaStream_t stream);
+
+struct ReadFp8Args {
+  const void* kv_cache;
+  HeadView k_out, v_out;  // batch stride unused
+  PagedSlots at;
+  int Hkv, d;
+};
+
+cudaError_t launch_cache_read_fp8(const ReadFp8Args& a, cudaStream_t stream);
+
+constexpr int kSplitSms = 152;
+constexpr int kSplitMaxCtas = kSplitSms * 3;  // no grid of a batch's shares is larger
+constexpr int kSplitClusterCtas = 8;          // CTAs of a segment in a small call (the portable cluster size)
+constexpr int kSplitClusterTokens = 4096;     // of the longest segment of a small call
+
+// A segment (the columns, in chunks of `rows`, that read one KV head of one sequence: the
+// query heads that share it, of each query token) that starts in CTA `cta` and goes on
+// through `more` further CTAs.
+struct SegmentJoint {
+  int cta, more;
+  int row;   // its first row of the output; with several query tokens, of its first column of all chunks
+  int rows;  // and how many; with several query tokens packed with the first one's number
+  static __host__ __device__ int pack(int rows, int first) { return first << 8 | rows; }
+  __host__ __device__ int columns() const { return rows & 255; }
+  __host__ __device__ int first() const { return rows >> 8; }
+};
+
+// How a decode over a quantised cache divides a call.  By the call's sizes alone, so that
+// the workspace can be sized on any host and a captured graph stays good.
+struct SplitPlan {
+  int rows;               // columns per segment: 8 of an mma, or 16 where there are more
+  int chunks;             // segments per KV head
+  int ctas;               // shares: one wave, but no more than there can be places
+  int joints;             // entries of the list of shared segments; 0 where the merge finds them itself
+  bool cluster;           // a cluster of CTAs for each segment
+  bool shared;            // whether a segment's partial outputs can lie in several CTAs' workspace
+  bool fits;              // the numbers of the work's places fit 32 bits
+  // columns: query heads of a KV head, of all query tokens; unit_blocks: blocks in a unit of
+  // work; per_sm: CTAs that share an SM, with segments of 8 columns and of 16
+  SplitPlan(int num_seqs, int Hkv, int columns, int max_blocks_per_seq, int unit_blocks, int per_sm8, int per_sm16) {
+    rows = columns <= 8 ? 8 : 16;
+    chunks = (columns + rows - 1) / rows;
+    const long long segments = static_cast<long long>(num_seqs) * Hkv * chunks;
+    const long long units = segments * ((max_blocks_per_seq + unit_blocks - 1) / unit_blocks);
+    const int wave = kSplitSms * (rows > 8 ? per_sm16 : per_sm8);
+    const bool split = units > segments;
+    // (with a place more for each segment's end, which a CTA may get alone, where that
+    // leaves every other CTA a single unit)
+    const long long shares = split ? units + segments : units;
+    ctas = static_cast<int>(shares < wave ? shares : wave);
+    cluster = split && segments * kSplitClusterCtas <= wave &&
+              units * unit_blocks * kDecodeBlockSize <= segments * kSplitClusterTokens;
+    if (cluster) ctas = static_cast<int>(segments * kSplitClusterCtas);
+    shared = split && !cluster;
+    joints = shared && segments > ctas ? ctas : 0;
+    fits = units + segments <= 0x7FFFFFFF;  // the places of units and of segments' ends
+  }
+  size_t joint_bytes() const { return sizeof(SegmentJoint) * joints; }
+  size_t part_bytes(int d) const { return sizeof(float) * 2 * ctas * rows * d; }
+  // of the workspace: joints, partial outputs, their log-sum-exp
+  size_t bytes(int d) const {
+    return shared ? joint_bytes() + part_bytes(d) + sizeof(float) * 2 * ctas * rows : 0;
+  }
+};
+
 constexpr int kFp4UnitBlocks = 8;       // blocks in a unit of the 4-bit decode's work
-constexpr int kFp4Sms = 152;
-constexpr int kFp4MaxCtas = kFp4Sms * 3;  // no grid of the batch's shares is larger
 
 // CTAs of the 4-bit decode that share an SM, for segments of `rows` query heads.
 // Three of four computing warps, though registers and shared memory would hold
@@ -214,50 +290,11 @@ constexpr int kFp4MaxCtas = kFp4Sms * 3;  // no grid of the batch's shares is la
 // words spilled in the form for small calls and none in the other.
 constexpr __host__ __device__ int fp4_decode_ctas(int rows) { return rows > 8 ? 2 : 3; }
 
-constexpr int kFp4ClusterCtas = 8;      // CTAs of a segment in a small call (the portable cluster size)
-constexpr int kFp4ClusterUnits = 32;    // units of the longest segment of a small call
+constexpr int kFp4ClusterUnits = kSplitClusterTokens / (kFp4UnitBlocks * kDecodeBlockSize);
 
-// A segment (the query heads of one sequence that share a KV head, in chunks
-// of `rows`) that starts in CTA `cta` and goes on through `more` further CTAs.
-struct Fp4Joint {
-  int cta, more;
-  int row;   // its first row of the output
-  int rows;  // and how many
-};
-
-// How the 4-bit decode divides a call.  By the call's sizes alone, so that the
-// workspace can be sized on any host and a captured graph stays good.
-struct Fp4Plan {
-  int rows;               // query heads per segment: 8 columns of an mma, or 16 for larger groups
-  int chunks;             // segments per KV head
-  int ctas;               // shares: one wave, but no more than there can be places
-  int joints;             // entries of the list of shared segments; 0 where the merge finds them itself
-  bool cluster;           // a cluster of CTAs for each segment
-  bool shared;            // whether a segment's partial outputs can lie in several CTAs' workspace
-  bool fits;              // the numbers of the work's places fit 32 bits
-  Fp4Plan(int num_seqs, int Hkv, int group, int max_blocks_per_seq) {
-    rows = group <= 8 ? 8 : 16;
-    chunks = (group + rows - 1) / rows;
-    const long long segments = static_cast<long long>(num_seqs) * Hkv * chunks;
-    const long long units = segments * ((max_blocks_per_seq + kFp4UnitBlocks - 1) / kFp4UnitBlocks);
-    const int wave = kFp4Sms * fp4_decode_ctas(rows);
-    const bool split = units > segments;
-    // (with a place more for each segment's end, which a CTA may get alone, where that
-    // leaves every other CTA a single unit)
-    const long long shares = split ? units + segments : units;
-    ctas = static_cast<int>(shares < wave ? shares : wave);
-    cluster = split && segments * kFp4ClusterCtas <= wave && units <= segments * kFp4ClusterUnits;
-    if (cluster) ctas = static_cast<int>(segments * kFp4ClusterCtas);
-    shared = split && !cluster;
-    joints = shared && segments > ctas ? ctas : 0;
-    fits = units + segments <= 0x7FFFFFFF;  // the places of units and of segments' ends
-  }
-  size_t joint_bytes() const { return sizeof(Fp4Joint) * joints; }
-  size_t part_bytes(int d) const { return sizeof(float) * 2 * ctas * rows * d; }
-  // of the workspace: joints, partial outputs, their log-sum-exp
-  size_t bytes(int d) const {
-    return shared ? joint_bytes() + part_bytes(d) + sizeof(float) * 2 * ctas * rows : 0;
-  }
+struct Fp4Plan : SplitPlan {
+  Fp4Plan(int num_seqs, int Hkv, int group, int max_blocks_per_seq)
+      : SplitPlan(num_seqs, Hkv, group, max_blocks_per_seq, kFp4UnitBlocks, fp4_decode_ctas(8), fp4_decode_ctas(16)) {}
 };
 
 struct DecodeFp4Args {
@@ -274,6 +311,36 @@ struct DecodeFp4Args {
 };
 
 cudaError_t launch_decode_fp4(const DecodeFp4Args& a, const DeviceGuard& g, cudaStream_t stream);
+
+// Blocks in a unit of the 8-bit decode's work, 16.5 KB of them: one for each computing
+// warp, two for heads of 64.
+constexpr __host__ __device__ int fp8_unit_blocks(int d) { return d == 128 ? 4 : 8; }
+
+// CTAs of the 8-bit decode that share an SM, for segments of `rows` columns.
+constexpr __host__ __device__ int fp8_decode_ctas(int rows) { return rows > 8 ? 2 : 3; }
+
+constexpr int kFp8MaxQueries = 16;  // query tokens of a sequence in one call
+
+struct Fp8Plan : SplitPlan {
+  Fp8Plan(int num_seqs, int Hkv, int columns, int max_blocks_per_seq, int d)
+      : SplitPlan(num_seqs, Hkv, columns, max_blocks_per_seq, fp8_unit_blocks(d), fp8_decode_ctas(8),
+                  fp8_decode_ctas(16)) {}
+};
+
+struct DecodeFp8Args {
+  const void* q;  // [num_seqs, queries, Hq, d]
+  const void* kv_cache;
+  const int32_t* block_table;
+  const int32_t* ctx_lens;
+  void* out;
+  float* lse;
+  void* workspace;  // joints, then partial outputs [2 ctas][rows][d] and their lse
+  Fp8Plan plan;
+  int num_seqs, queries, Hq, Hkv, d, num_blocks, max_blocks_per_seq;
+  float scale;
+};
+
+cudaError_t launch_decode_fp8(const DecodeFp8Args& a, const DeviceGuard& g, cudaStream_t stream);
 
 struct BwdArgs {
   // tensor maps (3-D views (d, rows, planes), 64-column boxes, 128-byte

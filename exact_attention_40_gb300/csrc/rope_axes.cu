@@ -19,12 +19,12 @@
 #include "fp4.cuh"
 #include "launch.h"
 #include "ptx.cuh"
+#include "rope_rows.cuh"
 #include "rotary.cuh"
 
 namespace exattn {
 namespace {
 
-constexpr int kTileThreads = 256;
 // Measured choices (heads of a token in flight together, rows of a thread in the ring
 // with the one at hand, CTAs an SM).  Rotation of 8 x 4096 tokens, 32 + 32 heads of 128:
 // 156 us = 6.88 TB/s with 8 lanes, 4 or 5 stages and 4 CTAs, 157 with 4 lanes, 166 with
@@ -36,17 +36,6 @@ constexpr int kRopeStages = 4;  // rows of a thread on their way, and the one at
 constexpr int kFp4Lanes = 4;
 constexpr int kFp4Stages = 5;
 constexpr int kReadLanes = 4;  // of the read
-
-// How a CTA's threads cover tokens and heads.
-struct Tile {
-  int per_tok;  // threads per token: d / 16
-  int toks;     // tokens per CTA
-  int lanes;    // threads that share a (token, j)
-};
-
-__device__ __forceinline__ const uint4* row_of(const HeadView& v, long long b, long long h, long long n) {
-  return static_cast<const uint4*>(v.ptr) + b * v.batch + h * v.head + n * v.token;
-}
 
 // Cosines and sines of the tile's tokens into cs[token][pair]: pos(token, axis)
 // gives the position.  A thread keeps to one pair, and takes its entry of the table by
@@ -63,35 +52,6 @@ __device__ __forceinline__ void tile_angles(float2* cs, const RopeAxesTable& tab
   for (int tok = threadIdx.x / half; tok < count; tok += per)
     cs[tok * half + i] = turn_cos_sin(static_cast<unsigned long long>(static_cast<long long>(pos(tok, axis))) * u);
 }
-
-// A thread's 8 cosines and sines.
-struct Turn8 {
-  float c[8], s[8];
-  __device__ __forceinline__ void load(const float2* cs, float sign) {
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      const float4 x = *reinterpret_cast<const float4*>(cs + e);
-      c[e] = x.x;
-      s[e] = sign * x.y;
-      c[e + 1] = x.z;
-      s[e + 1] = sign * x.w;
-    }
-  }
-  // The turned pairs of the vectors (lo, hi).  Products are rounded before they are
-  // added, so that the fp32 result, and with it every 4-bit code, is the one
-  // that the definition's plain fp32 operations give.  (Packed f32x2
-  // operations do not keep that: their products end up fused into the sums.)
-  __device__ __forceinline__ void turn(const uint4 lo, const uint4 hi, float (&ya)[8], float (&yb)[8]) const {
-    float a[8], b[8];
-    unpack_bf16x8(lo, a);
-    unpack_bf16x8(hi, b);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      ya[e] = __fsub_rn(__fmul_rn(a[e], c[e]), __fmul_rn(b[e], s[e]));
-      yb[e] = __fadd_rn(__fmul_rn(b[e], c[e]), __fmul_rn(a[e], s[e]));
-    }
-  }
-};
 
 // Two 16-byte vectors of one row.
 struct Vecs {
@@ -166,15 +126,6 @@ __global__ void __launch_bounds__(kTileThreads, 4) rope_axes_kernel(const RopeAx
     to[0] = pack_bf16x8(ya);
     to[apart] = pack_bf16x8(yb);
   }
-}
-
-// Span index (block * Hkv) and offset of a token in the cache, or -1.
-__device__ __forceinline__ long long find_block(const Fp4Slots& at, long long n, int* off) {
-  const int seq = at.seq_ids[n], slot = at.slots[n];
-  *off = slot & 15;
-  if (seq < 0 || seq >= at.num_seqs || slot < 0 || slot / 16 >= at.max_blocks_per_seq) return -1;
-  const int blk = at.block_table[static_cast<long long>(seq) * at.max_blocks_per_seq + slot / 16];
-  return blk >= 0 && blk < at.num_blocks ? blk : -1;
 }
 
 // Quantises groups of one tensor with fp32 scale g.
@@ -424,31 +375,11 @@ __global__ void __launch_bounds__(kTileThreads, 8) cache_read_fp4_kernel(const R
   }
 }
 
-// A tile of as many tokens as the threads hold with `lanes` heads of each walked at
-// once: fewer where a token has fewer rows, so that a thread gets `each` of them (2 + 2
-// heads of 64, 258,842 tokens: 69 us with four, 95 with one), but no fewer than `least`.
-// Halved while there are fewer than two CTAs an SM and a token still has rows for the
-// threads that frees (3 x 1001 tokens of 16 heads: 4.2 us; 4.5 with one, 5.5 with four).
-Tile make_tile(int d, long long tokens, int rows, int lanes, int each, int least, int sms) {
-  Tile t;
-  t.per_tok = d / 16;
-  const int slots = kTileThreads / t.per_tok;
-  while (lanes > least && each * lanes > rows) lanes /= 2;
-  // A ring and the cosines and sines, 4 d bytes a token and so 64 for each of its d/16
-  // threads, divided by the lanes: within the 48 KB that a launch has without asking (an
-  // append has two lanes or more).
-  static_assert(RowRing<kRopeStages>::kBytes + 64 * kTileThreads <= 48 * 1024, "shared memory of the rotation");
-  static_assert(RowRing<kFp4Stages>::kBytes + 32 * kTileThreads <= 48 * 1024, "shared memory of the append");
-  t.toks = 1;
-  while (2 * t.toks * lanes <= slots) t.toks *= 2;
-  while (t.toks > 1 && (tokens + t.toks - 1) / t.toks < 2 * sms && 2 * (slots / t.toks) <= rows) t.toks /= 2;
-  t.lanes = slots / t.toks;
-  return t;
-}
-
-unsigned int tiles(const Tile& t, long long tokens) {
-  return static_cast<unsigned int>((tokens + t.toks - 1) / t.toks);
-}
+// A ring and the cosines and sines, 4 d bytes a token and so 64 for each of its d/16
+// threads, divided by the lanes: within the 48 KB that a launch has without asking (an
+// append has two lanes or more).
+static_assert(RowRing<kRopeStages>::kBytes + 64 * kTileThreads <= 48 * 1024, "shared memory of the rotation");
+static_assert(RowRing<kFp4Stages>::kBytes + 32 * kTileThreads <= 48 * 1024, "shared memory of the append");
 
 }  // namespace
 

@@ -2,7 +2,7 @@
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels behind the C ABI.  PyTorch supplies device memory and the stream.
-The calls of the 4-bit cache and of multi-axis rotary positions, which a
+The calls of the 4-bit and 8-bit caches and of multi-axis rotary positions, which a
 serving step makes with a few tokens, marshal theirs in a compiled module
 (csrc/binding.cpp) instead of ctypes.
 Importing this module loads the library and raises if it has not been
@@ -83,6 +83,16 @@ lib.attn_decode_fp4_workspace_bytes.argtypes = [_I, _I, _I, _I, _I]
 lib.attn_decode_fp4_workspace_bytes.restype = _SZ
 lib.attn_decode_paged_fp4.argtypes = [_P] * 6 + [_I] * 6 + [_F, _F, _F, _P, _SZ, _P]
 lib.attn_decode_paged_fp4.restype = _I
+lib.attn_fp8_cache_bytes.argtypes = [_I, _I, _I]
+lib.attn_fp8_cache_bytes.restype = _SZ
+lib.attn_rope_cache_write_fp8.argtypes = [_P] * 9 + [_P, _P] + [_I] * 8 + [_F, _I, _P]
+lib.attn_rope_cache_write_fp8.restype = _I
+lib.attn_cache_read_fp8.argtypes = [_P] * 7 + [_I] * 6 + [_P]
+lib.attn_cache_read_fp8.restype = _I
+lib.attn_decode_fp8_workspace_bytes.argtypes = [_I] * 6
+lib.attn_decode_fp8_workspace_bytes.restype = _SZ
+lib.attn_decode_paged_fp8.argtypes = [_P] * 6 + [_I] * 7 + [_F, _P, _SZ, _P]
+lib.attn_decode_paged_fp8.restype = _I
 lib.attn_shutdown.argtypes = []
 lib.attn_shutdown.restype = None
 
@@ -470,6 +480,55 @@ def attn_decode_paged_fp4(q, kv_cache, block_table, ctx_lens, scale: float | Non
     Returns (out [S,Hq,d] bf16, lse [S,Hq] fp32 or None)."""
     return (_native or _load_native()).decode_paged_fp4(q, kv_cache, block_table, ctx_lens, scale, k_scale, v_scale, out,
                                                         lse, workspace, return_lse, stream)
+
+
+def attn_fp8_cache(num_blocks: int, Hkv: int, d: int, device="cuda"):
+    """An empty (zeroed) 8-bit paged cache: uint8 [num_blocks, Hkv, 32 d + 32]."""
+    import torch
+    if lib.attn_fp8_cache_bytes(num_blocks, Hkv, d) == 0:
+        raise ValueError("no 8-bit cache of %d blocks, %d heads of %d" % (num_blocks, Hkv, d))
+    return torch.zeros((num_blocks, Hkv, 32 * d + 32), device=device, dtype=torch.uint8)
+
+
+def attn_rope_cache_write_fp8(q, k, v, token_starts, ctx_lens, positions, block_table, kv_cache, sections,
+                              base: float = 500000.0, per_axis: bool = False, q_out=None, stream=None):
+    """Rotates new tokens' queries and keys by their positions and appends the
+    rotated keys and the values to the 8-bit cache.  q [T,Hq,d], k, v [T,Hkv,d]
+    bf16, any strides with d contiguous; token_starts int32 [S+1]: sequence s has
+    the call's tokens token_starts[s] .. token_starts[s+1] - 1, or None where each
+    has one; ctx_lens int32 [S]: tokens of each sequence, the new ones included
+    (they take its last places); positions int32 [axes,T]; block_table int32
+    [S,max_blocks]; sections, base, per_axis as attn_rope_axes.  q_out may be q.
+
+    Returns q_out, the rotated queries (contiguous where not given).  Rows that
+    belong to no sequence are left as they are."""
+    return (_native or _load_native()).rope_cache_write_fp8(q, k, v, token_starts, ctx_lens, positions, block_table,
+                                                            kv_cache, sections, base, per_axis, q_out, stream)
+
+
+def attn_cache_read_fp8(kv_cache, seq_ids, slots, block_table, k_out=None, v_out=None, stream=None):
+    """Tokens of the 8-bit cache as bf16: token i is place slots[i] of sequence
+    seq_ids[i].  k_out, v_out [T,Hkv,d], any strides with d contiguous (a
+    [Hkv,N,d] tensor's transpose takes one sequence for attn_fwd).
+
+    Returns (k_out, v_out), contiguous where not given."""
+    return (_native or _load_native()).cache_read_fp8(kv_cache, seq_ids, slots, block_table, k_out, v_out, stream)
+
+
+def attn_decode_fp8_workspace_bytes(num_seqs, num_queries, Hq, Hkv, d, max_blocks_per_seq) -> int:
+    return int(lib.attn_decode_fp8_workspace_bytes(num_seqs, num_queries, Hq, Hkv, d, max_blocks_per_seq))
+
+
+def attn_decode_paged_fp8(q, kv_cache, block_table, ctx_lens, scale: float | None = None, out=None, lse=None,
+                          workspace=None, return_lse: bool = True, stream=None):
+    """Decode over the 8-bit cache.  q [S,Hq,d] bf16: the last token of each
+    sequence; or [S,n,Hq,d]: its last n tokens (at most 16), each of which sees
+    the context up to itself.  kv_cache uint8 [num_blocks,Hkv,32 d+32];
+    block_table int32 [S,max_blocks]; ctx_lens int32 [S].
+
+    Returns (out like q, lse like q without d, fp32, or None)."""
+    return (_native or _load_native()).decode_paged_fp8(q, kv_cache, block_table, ctx_lens, scale, out, lse, workspace,
+                                                        return_lse, stream)
 
 
 def attn_get_device_status(stream=None) -> int:

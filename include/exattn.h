@@ -29,7 +29,7 @@
  *   - stream is a cudaStream_t (NULL = legacy default stream).  Every call
  *     is asynchronous on that stream: validation happens on the host before
  *     anything is enqueued; nothing synchronises.  attn_rope_axes and the
- *     calls of the 4-bit cache are programmatic dependent launches: they wait
+ *     calls of the 4-bit and 8-bit caches are programmatic dependent launches: they wait
  *     for the kernel before them on the stream, so one of the caller's own
  *     that lets its dependents in before it ends must first have waited for
  *     what came before it (plain launches need no care).
@@ -410,6 +410,96 @@ int attn_decode_paged_fp4(const void* q, const void* kv_cache, const int32_t* bl
                           void* out, float* lse, int num_seqs, int Hq, int Hkv, int d, int num_blocks,
                           int max_blocks_per_seq, float scale, float k_scale, float v_scale, void* workspace,
                           size_t workspace_bytes, void* stream);
+
+/*
+ * The 8-bit paged cache.  A value is code * scale: code an e4m3 number, scale a power
+ * of two (2^-117 .. 2^119), one for the keys and one for the values of each block of
+ * 16 tokens of a KV head.  8.06 bits a value, and nothing to calibrate.
+ *   kv_cache [num_blocks, Hkv, 32 d + 32] bytes, 16-byte aligned: one block of 16
+ *   tokens of one KV head is one span,
+ *     key codes    16 d bytes
+ *     value codes  16 d bytes
+ *     key scale, value scale (fp32), 24 unused bytes
+ *   Column c of token n is byte n d + 16 ((c / 16) ^ turn(n)) + c % 16 of its codes,
+ *   turn(n) = n % 8 for d = 128 and n / 2 % 4 for d = 64.
+ * A scale is the smallest in that range with which the block's largest finite magnitude
+ * is at most 448 of it.  It grows with the tokens that are added; the codes already there
+ * are then brought to the larger scale (rounded once more, which changes those that
+ * fall below 2^-6 of it).  A call that writes a block's place 0 starts its scales anew
+ * from its own tokens, so that a block's memory can be given to another sequence: what
+ * the block's other places held is void then.  Elements that are not finite are stored
+ * and read back as NaN.  A cache starts as zeros.
+ * attn_fp8_cache_bytes: its size (0 for invalid arguments).  d is 64 or 128 for
+ * every call on it.
+ */
+size_t attn_fp8_cache_bytes(int num_blocks, int Hkv, int d);
+
+/*
+ * Append to the 8-bit cache: rotates the new tokens' queries and keys (as
+ * attn_rope_axes, positions by axis, frequencies by sections, base, per_axis)
+ * and stores the rotated keys and the values at the end of their sequences:
+ *   code = e4m3(x / scale)   rounded to nearest, ties to even.
+ * The keys are the fp32 results of the rotation, not rounded to bf16 before.
+ *   q, q_out  [num_tokens, Hq, d] bf16 by strides; q_out may be q, and overlaps
+ *             nothing else.  Hq may be 0.
+ *   k, v      [num_tokens, Hkv, d] bf16 by strides
+ *   token_starts int32 [num_seqs + 1]: sequence s has the call's tokens token_starts[s] ..
+ *             token_starts[s + 1] - 1, any number of them.  NULL: one token for each
+ *             sequence (num_tokens == num_seqs).
+ *   ctx_lens  int32 [num_seqs]: tokens of each sequence, the new ones included (as
+ *             attn_decode_paged_fp8 takes them): sequence s's new tokens take its last places
+ *   positions int32 [num_axes][num_tokens]
+ *   block_table int32 [num_seqs, max_blocks_per_seq] (as attn_decode_paged)
+ *   strides   host array of 9, in elements: q (token, head), k, v, q_out, axis
+ *             of positions; rules as attn_rope_axes
+ * Rows of the call that belong to no sequence (before token_starts[0], from
+ * token_starts[num_seqs] on) are neither read nor written.  Two sequences must not have
+ * new tokens in one block.  Tokens whose places or table entries lie outside the table or
+ * the cache are rotated in q_out but store nothing, and set EXATTN_DEVICE_BOUNDS_BIT.
+ * token_starts that decrease or leave 0 .. num_tokens set it too, and nothing is written.
+ * num_seqs <= 65535; num_tokens >= 0 (0 launches nothing).  One launch on `stream`,
+ * asynchronous, deterministic; the call can be captured into a CUDA graph, whose replays
+ * follow the contents of token_starts and ctx_lens.
+ */
+int attn_rope_cache_write_fp8(const void* q, const void* k, const void* v, void* q_out, const int32_t* token_starts,
+                              const int32_t* ctx_lens, const int32_t* positions, const int32_t* block_table,
+                              void* kv_cache, const int64_t* strides, const int* sections, int num_axes,
+                              int num_tokens, int Hq, int Hkv, int d, int num_seqs, int num_blocks,
+                              int max_blocks_per_seq, float base, int per_axis, void* stream);
+
+/*
+ * Reads tokens of the 8-bit cache back as bf16 (code * scale, exact while normal):
+ * arguments and rules as attn_cache_read_fp4, without its scales.
+ */
+int attn_cache_read_fp8(const void* kv_cache, const int32_t* seq_ids, const int32_t* slots,
+                        const int32_t* block_table, void* k_out, void* v_out, const int64_t* strides, int num_tokens,
+                        int Hkv, int d, int num_seqs, int num_blocks, int max_blocks_per_seq, void* stream);
+
+/*
+ * Decode over the 8-bit cache: attn_decode_paged on the keys and values that the cache
+ * stands for, for one query token of each sequence or for the last num_queries tokens of
+ * each (drafted ones that are checked together): query i sees the tokens before
+ * ctx_len - (num_queries - 1 - i), so the last sees all of them.
+ *   q, out [num_seqs, num_queries, Hq, d] bf16, lse [num_seqs, num_queries, Hq] fp32 or
+ *   NULL; block_table, ctx_lens and their checks on the device as attn_decode_paged
+ * Keys and values enter exactly; a weight is rounded by at most 2^-11 of itself or
+ * 2^-32 of the largest product of a weight and its block's value scale, whichever is
+ * more.  A query that sees no token gets out = 0, lse = -inf.  What a query does not see
+ * has no part in its output, NaN included.  out overlaps no input, and
+ * ctx_lens keep their values while the call runs.  scale and 2 scale are finite and > 0;
+ * 1 <= num_queries <= 16.
+ *   workspace: attn_decode_fp8_workspace_bytes(...) bytes, 16-byte aligned, its
+ *   contents clobbered; NULL where that is 0 (also for invalid arguments).
+ *   Calls whose executions overlap need one each.
+ * One or two launches on `stream` (the second merges the splits of a sequence,
+ * a programmatic dependent launch), asynchronous, deterministic; it can be
+ * captured into a CUDA graph.  A bounded wait that runs out sets
+ * EXATTN_DEVICE_TIMEOUT_BIT.
+ */
+size_t attn_decode_fp8_workspace_bytes(int num_seqs, int num_queries, int Hq, int Hkv, int d, int max_blocks_per_seq);
+int attn_decode_paged_fp8(const void* q, const void* kv_cache, const int32_t* block_table, const int32_t* ctx_lens,
+                          void* out, float* lse, int num_seqs, int num_queries, int Hq, int Hkv, int d, int num_blocks,
+                          int max_blocks_per_seq, float scale, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Synchronises `stream`, then reads and clears the status word of the
