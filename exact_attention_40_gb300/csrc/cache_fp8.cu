@@ -11,15 +11,18 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
-constexpr int kAppendCtas = 2;  // that share an SM
+constexpr int kAppendCtas = 3;    // that share an SM
+constexpr int kAppendStages = 2;  // heads of a warp on their way, and the one at hand
+constexpr long long kAppendSmall = 8 << 20;  // bytes of rows of a small call
 constexpr int kBlk = kDecodeBlockSize;
 constexpr int kReadLanes = 4;
 
-// New tokens of one sequence that fall into one block: `count` of them from the call's
-// token `token` on, at places `place` and following.
+// Rows of the call that are handled together: new tokens of one sequence that fall into
+// one block, or (kSingle) one token each of neighbouring sequences.
 struct Run {
-  int seq, token, count, place;
-  long long slot;  // of the first
+  int token, count;  // the call's tokens token .. token + count - 1
+  int seq, place;    // of the first
+  long long slot;    // of the first
 };
 
 // The new tokens of a sequence: tokens begin .. end - 1 of the call, the last ones of ctx.
@@ -42,32 +45,81 @@ struct Added {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
-    rope_cache_fp8_kernel(const RopeFp8Args a, const __grid_constant__ RopeAxesTable table, const int splits) {
-  using Span = Fp8Span<D>;
-  constexpr int kHalf = D / 2, kApart = kHalf / 8;  // 16-byte vectors between the halves of a row
-  constexpr int kPerTok = D / 16;                   // lanes per token: 8 pairs each
-  constexpr int kToks = 32 / kPerTok;               // tokens of a warp at once
-  constexpr int kSteps = kBlk / kToks;
-  // Cosines and sines by token, then two pairs (float4) of each lane next to each other:
-  // the lanes of a token read neighbouring vectors.
-  __shared__ float4 angles[kBlk][4][kPerTok];
-  __shared__ int upto[kAppendThreads];       // runs of the sequences of this and earlier threads
-  __shared__ Added added[kAppendThreads];    // where a thread has one sequence
-  __shared__ int warp_sum[kAppendWarps];
+struct AppendSmem {
+  static constexpr int kPerTok = D / 16;              // lanes per token: 8 pairs each
+  static constexpr int kSteps = kBlk * kPerTok / 32;  // rounds of a warp over 16 tokens
+  uint4 ring[kAppendWarps][kAppendStages][kSteps][2][32];  // a lane's two vectors of each round
+  // Of a run: cosines and sines by token, then two pairs (float4) of each lane next to each
+  // other, so that the lanes of a token read neighbouring vectors; and where each token lies.
+  float4 angles[kBlk][4][kPerTok];
+  int block[kBlk], place[kBlk];
+  int upto[kAppendThreads];     // runs of the sequences of this and earlier threads
+  Added added[kAppendThreads];  // where a thread has one sequence
+  int warp_sum[kAppendWarps];
+};
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.4028234663852886e38f; }
+
+// Largest of m and the magnitudes of a and b, NaN where one is.
+__device__ __forceinline__ float max3_nan_abs(float m, float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
+// Brings a block's codes from one scale to a larger one (biased exponents; 0: there was
+// none, and all are 0), but for places first .. first + count - 1.  By `lanes` lanes.
+template <int D>
+__device__ __forceinline__ void rescale(uint8_t* codes, int from, int to, int first, int count, int lane, int lanes) {
+  const int shift = from > 0 ? 127 + from - to : 0;
+  const float factor = shift > 0 ? __uint_as_float(static_cast<uint32_t>(shift) << 23) : 0.f;
+  auto moved = [&](uint32_t w) {
+    uint32_t h0, h1;
+    e4m3x4_to_f16(w, h0, h1);
+    return f32x4_to_e4m3(f16_lo(h0) * factor, f16_hi(h0) * factor, f16_lo(h1) * factor, f16_hi(h1) * factor);
+  };
+#pragma unroll 1
+  for (int v = lane; v < D; v += lanes) {
+    const int place = v / (D / 16);
+    if (place >= first && place < first + count) continue;
+    uint4* at = reinterpret_cast<uint4*>(codes) + v;
+    const uint4 old = *at;
+    *at = make_uint4(moved(old.x), moved(old.y), moved(old.z), moved(old.w));
+  }
+}
+
+// kSingle: each sequence has one token; runs are `tile` of them.
+template <int D, bool kSingle>
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
+    rope_cache_fp8_kernel(const RopeFp8Args a, const __grid_constant__ RopeAxesTable table, const int tile,
+                          const int splits) {
+  using Span = Fp8Span<D>;
+  using Smem = AppendSmem<D>;
+  constexpr int kHalf = D / 2, kApart = kHalf / 8;  // 16-byte vectors between the halves of a row
+  constexpr int kPerTok = Smem::kPerTok, kSteps = Smem::kSteps;
+  constexpr int kToks = 32 / kPerTok;               // tokens of a warp at once
+  constexpr int kAtOnce = kAppendThreads / kHalf;   // tokens whose angles the threads form at once
+  constexpr int kAngles = kBlk / kAtOnce;
+  extern __shared__ __align__(16) uint8_t append_smem[];
+  Smem& sm = *reinterpret_cast<Smem*>(append_smem);
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int j = lane % kPerTok, tok0 = lane / kPerTok;
+  // this thread's pair of the angles
+  const int pair = threadIdx.x % kHalf, angle_tok = threadIdx.x / kHalf;
+  unsigned long long freq;
+  uint32_t axis;
+  asm volatile("ld.b64 %0, [%1];" : "=l"(freq) : "l"(table.u + pair));
+  asm volatile("ld.u8 %0, [%1];" : "=r"(axis) : "l"(table.axis + pair));
   cudaGridDependencySynchronize();
 
-  // ---- the runs: one for each sequence, or counted from token_starts
-  const int per = a.token_starts == nullptr ? 1 : (a.num_seqs + kAppendThreads - 1) / kAppendThreads;
+  // ---- the runs: counted from token_starts, or `tile` sequences each
+  const int per = (a.num_seqs + kAppendThreads - 1) / kAppendThreads;
   auto added_of = [&](int s) {
-    if (a.token_starts == nullptr) return Added{s, s + 1, __ldg(a.ctx_lens + s)};
     return Added{__ldg(a.token_starts + s), __ldg(a.token_starts + s + 1), __ldg(a.ctx_lens + s)};
   };
-  int total = a.num_seqs;
-  if (a.token_starts != nullptr) {
+  int total = (a.num_seqs + tile - 1) / tile;
+  if constexpr (!kSingle) {
     int mine = 0;
     bool bad = false;
     Added x = {0, 0, 0};
@@ -78,14 +130,14 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
       bad |= x.begin < 0 || x.end < x.begin || x.end > a.num_tokens;
       mine += bad ? 0 : x.runs();
     }
-    added[threadIdx.x] = x;
+    sm.added[threadIdx.x] = x;
     int sum = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
       const int v = __shfl_up_sync(0xffffffffu, sum, d);
       if (lane >= d) sum += v;
     }
-    if (lane == 31) warp_sum[warp] = sum;
+    if (lane == 31) sm.warp_sum[warp] = sum;
     // starts that decrease or leave the call could name a token twice: nothing is done then
     if (__syncthreads_or(bad)) {
       if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, 2u);  // EXATTN_DEVICE_BOUNDS_BIT
@@ -94,24 +146,21 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
     total = 0;
 #pragma unroll
     for (int w = 0; w < kAppendWarps; ++w) {
-      if (w < warp) sum += warp_sum[w];
-      total += warp_sum[w];
+      if (w < warp) sum += sm.warp_sum[w];
+      total += sm.warp_sum[w];
     }
-    upto[threadIdx.x] = sum;
+    sm.upto[threadIdx.x] = sum;
     __syncthreads();
   }
   auto find_run = [&](int r) {
-    if (a.token_starts == nullptr) return added_of(r).run(r, 0);
-    int lo = 0, hi = kAppendThreads - 1;  // the first thread with upto > r
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (upto[mid] > r)
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
-    r -= lo > 0 ? upto[lo - 1] : 0;
-    if (per == 1) return added[lo].run(lo, r);
+    if constexpr (kSingle) return Run{r * tile, min(tile, a.num_seqs - r * tile), r * tile, 0, 0};
+    // the first thread with upto > r, by the warp: its warp's place, then its own
+    static_assert(kAppendThreads == 32 * kAppendWarps, "lanes look at every eighth entry");
+    const int eighth = min(31, __popc(__ballot_sync(0xffffffffu, sm.upto[kAppendWarps * lane + kAppendWarps - 1] <= r)));
+    const bool past = lane < kAppendWarps && sm.upto[kAppendWarps * eighth + min(lane, kAppendWarps - 1)] <= r;
+    const int lo = kAppendWarps * eighth + min(kAppendWarps - 1, __popc(__ballot_sync(0xffffffffu, past)));
+    r -= lo > 0 ? sm.upto[lo - 1] : 0;
+    if (per == 1) return sm.added[lo].run(lo, r);
     int s = lo * per;
     Added x = added_of(s);
     while (r >= x.runs() && s + 1 < a.num_seqs) {
@@ -121,169 +170,236 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
     return x.run(s, r);
   };
 
-  // items of a run: key heads, value heads, query heads
+  // ---- units of work: a run and a part of its items, which are key heads, value heads and
+  // query heads in order.  (Runs hold a token each, and have several parts only where they
+  // are fewer than the CTAs: the numbers stay far below 2^31.)
   const int first_value = a.Hkv, first_query = 2 * a.Hkv, items = first_query + a.Hq;
-  // (the grid has no more CTAs than fit at once: total * splits stays far below 2^31, runs
-  // hold a token each and splits are few)
-  for (long long unit = blockIdx.x; unit < static_cast<long long>(total) * splits; unit += gridDim.x) {
-    const Run run = find_run(static_cast<int>(unit / splits));
-    const int part = static_cast<int>(unit % splits);
-    uint4 lo[kSteps], hi[kSteps];
-    auto load = [&](int item) {
-      if (item >= items) return;
-      const HeadView& view = item < first_value ? a.k : item < first_query ? a.v : a.q;
-      const int head = item < first_value ? item : item < first_query ? item - first_value : item - first_query;
+  const int units = total * splits;
+  int unit = blockIdx.x;
+  if (unit >= units) return;
+
+  // Rows on their way into the ring: this warp's items in order, through all units.
+  int to_unit = unit, to_item = unit % splits + splits * warp;
+  Run to = find_run(unit / splits);
+  auto fetch = [&](int stage) {
+    while (to_item >= items) {
+      to_unit += gridDim.x;
+      if (to_unit >= units) break;
+      to = find_run(to_unit / splits);
+      to_item = to_unit % splits + splits * warp;
+    }
+    if (to_unit < units) {
+      const HeadView& view = to_item < first_value ? a.k : to_item < first_query ? a.v : a.q;
+      const int head = to_item - (to_item < first_value ? 0 : to_item < first_query ? first_value : first_query);
+      const uint4* row = row_of(view, 0, head, to.token + tok0) + j;
+      const uint32_t slot = smem_u32(&sm.ring[warp][stage][0][0][lane]);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const int tok = s * kToks + tok0;
-        if (tok < run.count) {
-          const uint4* row = row_of(view, 0, head, run.token + tok) + j;
-          lo[s] = row[0];
-          hi[s] = row[kApart];
-        } else {
-          lo[s] = hi[s] = make_uint4(0u, 0u, 0u, 0u);
+        if (s * kToks + tok0 < to.count) {
+          cp_async16(slot + s * 1024, row, true);
+          cp_async16(slot + s * 1024 + 512, row + kApart, true);
         }
+        row += kToks * view.token;
       }
-    };
-    int item = part + splits * warp;
-    load(item);
-    int blk = -1;
-    if (run.slot >= 0 && run.slot < static_cast<long long>(a.max_blocks_per_seq) * kBlk) {
-      blk = __ldg(a.block_table + static_cast<long long>(run.seq) * a.max_blocks_per_seq + run.slot / kBlk);
-      if (blk >= a.num_blocks) blk = -1;
+      to_item += splits * kAppendWarps;
     }
-    if (blk < 0 && part == 0 && threadIdx.x == 0) atomicOr(a.status, 2u);  // EXATTN_DEVICE_BOUNDS_BIT
-    __syncthreads();  // the angles of the run before are no longer read
-    {
-      constexpr int kAtOnce = kAppendThreads / kHalf;
-      const int pair = threadIdx.x % kHalf;
-      unsigned long long u;
-      uint32_t axis;
-      asm volatile("ld.b64 %0, [%1];" : "=l"(u) : "l"(table.u + pair));
-      asm volatile("ld.u8 %0, [%1];" : "=r"(axis) : "l"(table.axis + pair));
-      for (int tok = threadIdx.x / kHalf; tok < run.count; tok += kAtOnce) {
-        const long long pos = a.positions[axis * a.pos_axis + run.token + tok];
-        reinterpret_cast<float2*>(&angles[tok][pair % 8 / 2][pair / 8])[pair & 1] =
-            turn_cos_sin(static_cast<unsigned long long>(pos) * u);
-      }
-    }
-    __syncthreads();
-    auto turn_of = [&](int tok) {
-      Turn8 t;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float4 v = angles[tok][x][j];
-        t.c[2 * x] = v.x;
-        t.s[2 * x] = v.y;
-        t.c[2 * x + 1] = v.z;
-        t.s[2 * x + 1] = v.w;
-      }
-      return t;
-    };
-    uint8_t* const spans = static_cast<uint8_t*>(a.kv_cache) + static_cast<size_t>(max(blk, 0)) * a.Hkv * Span::kBytes;
-    const bool anew = run.place == 0;
+    cp_async_commit();
+  };
 
-    for (; item < items; item += splits * kAppendWarps) {
-      if (item >= first_query) {
-        // ---- queries: turned and stored
-        uint4* out = const_cast<uint4*>(row_of(a.q_out, 0, item - first_query, run.token)) + j;
-        uint4 to_lo[kSteps], to_hi[kSteps];
+  // What a run needs beside its rows: where thread n's token n lies, the positions of the
+  // tokens whose angles a thread forms.  Asked for while the run before is worked on.
+  int ahead_block = -1, ahead_place = 0;
+  int ahead_pos[kAngles];
+  auto ask = [&](const Run& run) {
+    if (threadIdx.x < run.count) {
+      int seq = run.seq;
+      long long slot = run.slot;
+      ahead_place = run.place + threadIdx.x;
+      if constexpr (kSingle) {
+        seq += threadIdx.x;
+        slot = static_cast<long long>(__ldg(a.ctx_lens + seq)) - 1;
+        ahead_place = static_cast<int>(slot & (kBlk - 1));
+      }
+      ahead_block = -1;
+      if (slot >= 0 && slot < static_cast<long long>(a.max_blocks_per_seq) * kBlk) {
+        ahead_block = __ldg(a.block_table + static_cast<long long>(seq) * a.max_blocks_per_seq + slot / kBlk);
+        if (ahead_block >= a.num_blocks) ahead_block = -1;
+      }
+      if (ahead_block < 0) atomicOr(a.status, 2u);  // EXATTN_DEVICE_BOUNDS_BIT
+    }
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          if (s * kToks >= run.count) break;
-          float ya[8], yb[8];
-          turn_of(s * kToks + tok0).turn(lo[s], hi[s], ya, yb);
-          to_lo[s] = pack_bf16x8(ya);
-          to_hi[s] = pack_bf16x8(yb);
+    for (int i = 0; i < kAngles; ++i) {
+      const int tok = angle_tok + i * kAtOnce;
+      ahead_pos[i] = tok < run.count ? __ldg(a.positions + axis * a.pos_axis + run.token + tok) : 0;
+    }
+  };
+  auto put = [&](const Run& run) {
+    if (threadIdx.x < run.count) {
+      sm.block[threadIdx.x] = ahead_block;
+      sm.place[threadIdx.x] = ahead_place;
+    }
+#pragma unroll
+    for (int i = 0; i < kAngles; ++i) {
+      const int tok = angle_tok + i * kAtOnce;
+      if (tok < run.count)
+        reinterpret_cast<float2*>(&sm.angles[tok][pair % 8 / 2][pair / 8])[pair & 1] =
+            turn_cos_sin(static_cast<unsigned long long>(static_cast<long long>(ahead_pos[i])) * freq);
+    }
+  };
+
+#pragma unroll
+  for (int s = 0; s < kAppendStages - 1; ++s) fetch(s);
+  Run run = find_run(unit / splits);
+  ask(run);
+  int stage = 0, behind = kAppendStages - 1;  // stages of the item at hand, and of the one before it
+  for (;;) {
+    put(run);
+    __syncthreads();  // this run's angles are there
+    const bool more = unit + static_cast<int>(gridDim.x) < units;
+    const Run next = more ? find_run((unit + gridDim.x) / splits) : run;
+    if (more) ask(next);
+    for (int item = unit % splits + splits * warp; item < items; item += splits * kAppendWarps) {
+      const bool value = item >= first_value, query = item >= first_query;
+      const int head = item - (query ? first_query : value ? first_value : 0);
+      cp_async_wait<kAppendStages - 2>();
+      const uint4* const rows = &sm.ring[warp][stage][0][0][lane];  // vector x of round s at rows[64 s + 32 x]
+      fetch(behind);
+      behind = stage;
+      stage = stage + 1 == kAppendStages ? 0 : stage + 1;
+      // A token's 8 low and 8 high columns, turned; `turns` is false for values.
+      auto columns = [&](int s, bool turns, float (&ya)[8], float (&yb)[8]) {
+        const uint4 lo = rows[64 * s], hi = rows[64 * s + 32];
+        if (!turns) {
+          unpack_bf16x8(lo, ya);
+          unpack_bf16x8(hi, yb);
+          return;
         }
-        load(item + splits * kAppendWarps);
+        Turn8 t;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float4 v = sm.angles[s * kToks + tok0][x][j];
+          t.c[2 * x] = v.x;
+          t.s[2 * x] = v.y;
+          t.c[2 * x + 1] = v.z;
+          t.s[2 * x + 1] = v.w;
+        }
+        t.turn(lo, hi, ya, yb);
+      };
+      if (query) {
+        uint4* out = const_cast<uint4*>(row_of(a.q_out, 0, head, run.token + tok0)) + j;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-          const int tok = s * kToks + tok0;
-          if (tok < run.count) {
-            out[tok * a.q_out.token] = to_lo[s];
-            out[tok * a.q_out.token + kApart] = to_hi[s];
+          if (s * kToks + tok0 < run.count) {
+            float ya[8], yb[8];
+            columns(s, true, ya, yb);
+            out[0] = pack_bf16x8(ya);
+            out[kApart] = pack_bf16x8(yb);
           }
+          out += kToks * a.q_out.token;
         }
         continue;
       }
-      // ---- a head's keys or values of the run
-      const bool value = item >= first_value;
-      uint8_t* const span = spans + static_cast<size_t>(value ? item - first_value : item) * Span::kBytes;
-      uint8_t* const codes = span + (value ? Span::kValueCodes : Span::kKeyCodes);
-      uint32_t* const scale = reinterpret_cast<uint32_t*>(span + Span::kScales) + (value ? 1 : 0);
-      const uint32_t before = blk >= 0 && !anew ? *scale : 0u;
-      float y[kSteps][16];
-      float most = 0.f;
+      // ---- a head's keys or values: their largest magnitude, the scale, the codes
+      auto largest = [&](int s, bool all) {  // of a token's columns of this lane; of the finite ones, or NaN where one is
+        float ya[8], yb[8];
+        columns(s, !value, ya, yb);
+        float m = 0.f;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        if (s * kToks < run.count) {
-          float ya[8], yb[8];
-          if (value) {
-            unpack_bf16x8(lo[s], ya);
-            unpack_bf16x8(hi[s], yb);
+        for (int e = 0; e < 8; ++e) {
+          if (all) {
+            m = max3_nan_abs(m, ya[e], yb[e]);
           } else {
-            turn_of(s * kToks + tok0).turn(lo[s], hi[s], ya, yb);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            y[s][e] = ya[e];
-            y[s][8 + e] = yb[e];
-          }
-          const bool real = s * kToks + tok0 < run.count;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {  // (what is not finite becomes NaN, and has no part in the scale)
-            const bool finite = fabsf(y[s][e]) <= 3.4028234663852886e38f;
-            most = fmaxf(most, real && finite ? fabsf(y[s][e]) : 0.f);
-            if (!finite) y[s][e] = __int_as_float(0x7FC00000);
+            m = fmaxf(m, is_finite(ya[e]) ? fabsf(ya[e]) : 0.f);
+            m = fmaxf(m, is_finite(yb[e]) ? fabsf(yb[e]) : 0.f);
           }
         }
-      }
-      load(item + splits * kAppendWarps);
-      most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
-      const int e_before = min(static_cast<int>(before >> 23), 127 + kFp8HighExponent);
-      const int e = max(fp8_scale_exponent(most), e_before);
-      if (blk < 0) continue;
-      const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+        return m;
+      };
+      auto store = [&](int s, float most, bool plain, int block, int place, int first, int count, uint32_t before) {
+        uint8_t* const span = static_cast<uint8_t*>(a.kv_cache) +
+                              (static_cast<size_t>(block) * a.Hkv + head) * Span::kBytes;
+        uint8_t* const codes = span + (value ? Span::kValueCodes : Span::kKeyCodes);
+        const int e_before = min(static_cast<int>(before >> 23), 127 + kFp8HighExponent);
+        const int e = max(fp8_scale_exponent(most), e_before);
+        if (s * kToks + tok0 < run.count) {
+          const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+          float ya[8], yb[8];
+          columns(s, !value, ya, yb);
+          if (!plain) {
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int tok = s * kToks + tok0;
-        if (tok < run.count) {
-          const int place = run.place + tok;
+            for (int x = 0; x < 8; ++x) {
+              if (!is_finite(ya[x])) ya[x] = __int_as_float(0x7FC00000);
+              if (!is_finite(yb[x])) yb[x] = __int_as_float(0x7FC00000);
+            }
+          }
           uint32_t w[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            w[x] = f32x4_to_e4m3(y[s][4 * x] * down, y[s][4 * x + 1] * down, y[s][4 * x + 2] * down,
-                                 y[s][4 * x + 3] * down);
+          for (int x = 0; x < 2; ++x) {
+            w[x] = f32x4_to_e4m3(ya[4 * x] * down, ya[4 * x + 1] * down, ya[4 * x + 2] * down, ya[4 * x + 3] * down);
+            w[2 + x] = f32x4_to_e4m3(yb[4 * x] * down, yb[4 * x + 1] * down, yb[4 * x + 2] * down, yb[4 * x + 3] * down);
+          }
           uint8_t* row = codes + place * Span::kRow + (j & 1) * 8;
           *reinterpret_cast<uint2*>(row + ((j / 2) ^ fp8_turn<D>(place)) * 16) = make_uint2(w[0], w[1]);
           *reinterpret_cast<uint2*>(row + ((j / 2 + D / 32) ^ fp8_turn<D>(place)) * 16) = make_uint2(w[2], w[3]);
         }
-      }
-      if (anew || e > e_before) {
-        if (lane == 0) *scale = static_cast<uint32_t>(e) << 23;
-        if (!anew) {
-          // the block's other codes, at the larger scale
-          const int shift = e_before > 0 ? 127 + e_before - e : 0;
-          const float factor = shift > 0 ? __uint_as_float(static_cast<uint32_t>(shift) << 23) : 0.f;
+        if ((kSingle || s == 0) && e > e_before) {  // the scale, once for a block
+          if (kSingle ? j == 0 : lane == 0)
+            reinterpret_cast<uint32_t*>(span + Span::kScales)[value ? 1 : 0] = static_cast<uint32_t>(e) << 23;
+          if (first > 0) rescale<D>(codes, e_before, e, first, count, kSingle ? j : lane, kSingle ? kPerTok : 32);
+        }
+      };
+      auto scale_of = [&](int block) {
+        return reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.kv_cache) +
+                                                 (static_cast<size_t>(block) * a.Hkv + head) * Span::kBytes +
+                                                 Span::kScales)[value ? 1 : 0];
+      };
+      if constexpr (kSingle) {
 #pragma unroll 1
-          for (int v = lane; v < D; v += 32) {
-            const int place = v / (D / 16);
-            if (place >= run.place && place < run.place + run.count) continue;
-            uint4* at = reinterpret_cast<uint4*>(codes) + v;
-            const uint4 old = *at;
-            auto moved = [&](uint32_t w) {
-              uint32_t h0, h1;
-              e4m3x4_to_f16(w, h0, h1);
-              return f32x4_to_e4m3(f16_lo(h0) * factor, f16_hi(h0) * factor, f16_lo(h1) * factor, f16_hi(h1) * factor);
-            };
-            *at = make_uint4(moved(old.x), moved(old.y), moved(old.z), moved(old.w));
-          }
+        for (int s = 0; s * kToks < run.count; ++s) {
+          const int tok = s * kToks + tok0;
+          const bool real = tok < run.count;
+          const int block = real ? sm.block[tok] : -1, place = real ? sm.place[tok] : 0;
+          const uint32_t before = block >= 0 && place > 0 ? scale_of(block) : 0u;
+          float m = real ? largest(s, true) : 0.f;
+          const bool plain = is_finite(m);
+          if (!plain) m = largest(s, false);
+          __syncwarp();
+#pragma unroll
+          for (int d = 1; d < kPerTok; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+          if (block >= 0) store(s, m, plain, block, place, place, 1, before);
           __syncwarp();
         }
+      } else {
+        const int block = sm.block[0];
+        const uint32_t before = block >= 0 && run.place > 0 ? scale_of(block) : 0u;
+        float m = 0.f;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+          if (s * kToks + tok0 < run.count) m = max_nan(m, largest(s, true));
+        const bool plain = __all_sync(0xffffffffu, is_finite(m));
+        if (!plain) {
+          m = 0.f;
+#pragma unroll 1
+          for (int s = 0; s < kSteps; ++s)
+            if (s * kToks + tok0 < run.count) m = fmaxf(m, largest(s, false));
+          __syncwarp();
+        }
+        m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+        if (block >= 0) {
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s)
+            if (s * kToks < run.count)
+              store(s, m, plain, block, run.place + s * kToks + tok0, run.place, run.count, before);
+        }
+        __syncwarp();
       }
     }
+    if (!more) break;
+    __syncthreads();  // this run's angles are no longer read
+    unit += gridDim.x;
+    run = next;
   }
+  cp_async_wait<0>();
 }
 
 // Read: thread j of a token takes chunk j of the keys and values of every head
@@ -343,22 +459,40 @@ __global__ void __launch_bounds__(kTileThreads, 8) cache_read_fp8_kernel(const R
   }
 }
 
+template <int D, bool kSingle>
+cudaError_t launch_append(const RopeFp8Args& a, const RopeAxesTable& table, int sms, cudaStream_t stream) {
+  const size_t smem = sizeof(AppendSmem<D>);
+  static std::atomic<int> smem_set[64] = {};
+  const cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(rope_cache_fp8_kernel<D, kSingle>),
+                                        static_cast<int>(smem), smem_set);
+  if (e != cudaSuccess) return e;
+  // Small calls take so few CTAs that those of two launches fit on the SMs together, one's
+  // start under the other's end.
+  const int items = a.Hq + 2 * a.Hkv, most = (items + kAppendWarps - 1) / kAppendWarps;  // most: an item for each warp
+  const bool small = static_cast<long long>(a.num_tokens) * items * D * 2 <= kAppendSmall;
+  const int fit = small ? sms * kAppendCtas / 2 : sms * kAppendCtas;
+  int tile = 32 / AppendSmem<D>::kPerTok;  // tokens that a warp's lanes take at once
+  int runs;
+  if (kSingle) {
+    while (tile < kBlk && (a.num_tokens + tile - 1) / tile * most > fit) tile *= 2;
+    runs = (a.num_tokens + tile - 1) / tile;
+  } else {  // about as many as the call can have
+    runs = a.num_tokens / kBlk + (a.num_seqs < a.num_tokens ? a.num_seqs : a.num_tokens);
+  }
+  const int splits = runs * most <= fit ? most : runs < fit ? fit / runs : 1;
+  const int units = runs * splits;
+  return launch_overlapped(rope_cache_fp8_kernel<D, kSingle>, units < sms * kAppendCtas ? units : sms * kAppendCtas,
+                           kAppendThreads, smem, stream, 1, a, table, tile, splits);
+}
+
 }  // namespace
 
 cudaError_t launch_rope_cache_write_fp8(const RopeFp8Args& a, const RopeAxesTable& table, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  // About as many runs as the call can have; where they are fewer than the CTAs that fit at
-  // once, several CTAs share the heads of each, down to one for each warp.
-  const long long few = a.num_seqs < a.num_tokens ? a.num_seqs : a.num_tokens;
-  const long long runs = a.token_starts == nullptr ? a.num_tokens : a.num_tokens / kBlk + few;
-  const int fit = sms * kAppendCtas, most = (a.Hq + 2 * a.Hkv + kAppendWarps - 1) / kAppendWarps;
-  const int wanted = static_cast<int>((fit + runs - 1) / runs);
-  const int splits = wanted < 1 ? 1 : wanted < most ? wanted : most;
-  const long long units = runs * splits;
-  const int grid = static_cast<int>(units < fit ? units : fit);
-  return launch_overlapped(a.d == 64 ? rope_cache_fp8_kernel<64> : rope_cache_fp8_kernel<128>, grid, kAppendThreads, 0,
-                           stream, 1, a, table, splits);
+  if (a.token_starts == nullptr)
+    return a.d == 64 ? launch_append<64, true>(a, table, sms, stream) : launch_append<128, true>(a, table, sms, stream);
+  return a.d == 64 ? launch_append<64, false>(a, table, sms, stream) : launch_append<128, false>(a, table, sms, stream);
 }
 
 cudaError_t launch_cache_read_fp8(const ReadFp8Args& a, cudaStream_t stream) {
