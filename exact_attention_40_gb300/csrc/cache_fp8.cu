@@ -13,7 +13,6 @@ constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
 constexpr int kAppendCtas = 3;    // that share an SM
 constexpr int kAppendStages = 2;  // heads of a warp on their way, and the one at hand
-constexpr long long kAppendSmall = 8 << 20;  // bytes of rows of a small call
 constexpr int kBlk = kDecodeBlockSize;
 constexpr int kReadLanes = 4;
 
@@ -469,8 +468,7 @@ cudaError_t launch_append(const RopeFp8Args& a, const RopeAxesTable& table, int 
   // Small calls take so few CTAs that those of two launches fit on the SMs together, one's
   // start under the other's end.
   const int items = a.Hq + 2 * a.Hkv, most = (items + kAppendWarps - 1) / kAppendWarps;  // most: an item for each warp
-  const bool small = static_cast<long long>(a.num_tokens) * items * D * 2 <= kAppendSmall;
-  const int fit = small ? sms * kAppendCtas / 2 : sms * kAppendCtas;
+  const int fit = sms * kAppendCtas / 2;
   int tile = 32 / AppendSmem<D>::kPerTok;  // tokens that a warp's lanes take at once
   int runs;
   if (kSingle) {
