@@ -70,7 +70,7 @@ constexpr int kWhole = static_cast<int>(0x80000000u);
 constexpr float kLift = 7.f;
 constexpr float kMost = 15.f;
 
-using Batch = BatchOf<kUnit>;
+using Batch = BatchOf<kUnit, 1>;
 
 __device__ __forceinline__ int units_of(int ctx) { return exattn::units_of<kUnit>(ctx); }
 
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp4_decode_ctas(8 * NT)) decode_f
 
 template <int D, bool kFind>
 __global__ void __launch_bounds__(kMergeThreads, kFind ? 5 : 6) decode_fp4_combine_kernel(const MergeParams p) {
-  merge_segment<D, kUnit, kFind, false>(p);
+  merge_segment<D, kUnit, 1, kFind, false>(p);
 }
 
 template <int D, int NT, bool kCluster>

@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
   constexpr int kKeyVecs = D / 64;   // 16-byte vectors of a lane's key codes per token
   constexpr int kValWords = D / 32;  // words of a lane's value codes per token
   constexpr int kUnit = fp8_unit_blocks(D);
+  constexpr int kEnd = fp8_end_units(D, kRows);
   constexpr int kPer = kUnit / kWarps;  // blocks of a unit for each warp
   constexpr int kStages = Smem::kStages;
   constexpr int kStep = kCluster ? kSplitClusterCtas : 1;  // from a CTA's unit to its next
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
     if (copies && blk * kBlk < at.ctx) phys_lane = check(entry);
   } else {
     // ---- this CTA's share; every warp finds it for itself
-    const BatchOf<kUnit> seqs(p.ctx_lens, p.num_seqs, max_ctx);
+    const BatchOf<kUnit, kEnd> seqs(p.ctx_lens, p.num_seqs, max_ctx);
     const Shares shares(seqs.per_segment * segs, gridDim.x);
     const int begin = shares.begin(cta), begin_next = shares.begin(cta + 1);
     left = begin_next - begin;
@@ -194,8 +195,9 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
       return;
     }
     at = seqs.find(begin, segs, p.n_chunks);
-    if (at.k == at.units) {  // the end of a segment that others compute
-      if (--left == 0) {
+    if (at.k >= at.units) {  // the end of a segment that others compute
+      left -= at.units + kEnd - at.k;
+      if (left <= 0) {
         clear_empty();
         return;
       }
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
       e.head = p.cache + static_cast<size_t>(to.head) * Span::kBytes;
       to.k += e.units;
       to_load -= e.units;
-      if (to.k == to.units && to_load > 0) --to_load;
+      if (to.k == to.units) to_load = max(0, to_load - kEnd);
       return e;
     };
     Entries now, next;  // the entries of the next batch are on their way while this one's blocks are copied
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
         // reference is taken from it, as it was when it gave that: in one fused
         // operation the largest itself would lie off by the rounding, which passes all
         // that fp16 holds once scores come to 2^28.
-        float x[kPer][NT][4], y[kPer][NT][4];
+        float x[kPer][NT][4], shift[kPer][NT][2];  // y = x + shift
         auto distances = [&]() {
           float most = -INFINITY;
 #pragma unroll
@@ -489,13 +491,14 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const uint64_t mm = f2_pack(m[nt][0], m[nt][1]);
-              const uint64_t nn = f2_pack(n[nt][0] - value_exp[b], n[nt][1] - value_exp[b]);
 #pragma unroll
-              for (int z = 0; z < 4; z += 2) {
-                const uint64_t s = f2_pack(c[b][nt][z], c[b][nt][z + 1]);
-                f2_unpack(f2_sub(s, mm), x[b][nt][z], x[b][nt][z + 1]);
-                f2_unpack(f2_sub(s, nn), y[b][nt][z], y[b][nt][z + 1]);
-                most = max3f(most, max3f(x[b][nt][z], x[b][nt][z + 1], y[b][nt][z]), y[b][nt][z + 1]);
+              for (int z = 0; z < 4; z += 2)
+                f2_unpack(f2_sub(f2_pack(c[b][nt][z], c[b][nt][z + 1]), mm), x[b][nt][z], x[b][nt][z + 1]);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                shift[b][nt][j] = (m[nt][j] - n[nt][j]) + value_exp[b];
+                const float top = fmaxf(x[b][nt][j], x[b][nt][2 + j]);
+                most = max3f(most, top, top + shift[b][nt][j]);
               }
             }
           return most;
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               l[nt][z & 1] += ex2_approx(x[b][nt][z]);
-              w[z] = ex2_approx(y[b][nt][z]);
+              w[z] = ex2_approx(x[b][nt][z] + shift[b][nt][z & 1]);
             }
             pb[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
             pb[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
@@ -649,45 +652,56 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
                 make_float4(acc[mt][nt][j], acc[mt][nt][2 + j], acc[mt + 1][nt][j], acc[mt + 1][nt][2 + j]);
       }
     left -= n_units;
-    if (!kCluster && ends && left > 0) --left;
+    if (!kCluster && ends) left = max(0, left - kEnd);
     if (left > 0) {  // the next segment's queries arrive during the merge
       next_segment(at);
       load_queries(at);
     }
     compute_barrier();
-    for (int idx = threadIdx.x; idx < rows_here * (D / 4); idx += kThreads) {
-      const int r = idx / (D / 4), col = idx % (D / 4) * 4;
-      float M = kNoScore, N = kNoScore;
+    // A lane forms one row's factors: of each warp's sums, then from the values' reference
+    // back to the weights', in two steps as their distance may pass what fp32's exponents
+    // hold.  A share all of whose scores are -inf, or whose blocks are all missing, sees nothing.
+    const int own = lane % kRows;
+    float M = kNoScore, N = kNoScore, L = 0.f, part[kWarps];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        M = fmaxf(M, sm.wm[buf][w][r]);
-        N = fmaxf(N, sm.wn[buf][w][r]);
-      }
-      float L = 0.f;
+    for (int w = 0; w < kWarps; ++w) {
+      M = fmaxf(M, sm.wm[buf][w][own]);
+      N = fmaxf(N, sm.wn[buf][w][own]);
+    }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      part[w] = ex2_approx(sm.wn[buf][w][own] - N);
+      L += ex2_approx(sm.wm[buf][w][own] - M) * sm.wl[buf][w][own];
+    }
+    const float inv = L == 0.f ? 0.f : __fdividef(1.f, L), half_way = ex2_approx(0.5f * (N - M));
+    const float own_lse = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
+    const bool whole = starts && ends;
+    const int own_row = whole && own < rows_here ? static_cast<int>(row_of(here, own)) : 0;
+    constexpr int kRowLanes = D / 4, kAtOnce = 32 / kRowLanes;  // lanes of a row, rows of a warp
+#pragma unroll 1
+    for (int r0 = warp * kAtOnce; r0 < rows_here; r0 += kWarps * kAtOnce) {
+      const int r = r0 + lane / kRowLanes, col = lane % kRowLanes * 4;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float wt = ex2_approx(sm.wn[buf][w][r] - N);
-        L += ex2_approx(sm.wm[buf][w][r] - M) * sm.wl[buf][w][r];
+        const float wt = __shfl_sync(0xffffffffu, part[w], r);
         const float4 a = *reinterpret_cast<const float4*>(&sm.acc[w][half + r][col]);
         o.x += wt * a.x;
         o.y += wt * a.y;
         o.z += wt * a.z;
         o.w += wt * a.w;
       }
-      // a share all of whose scores are -inf, or whose blocks are all missing, sees nothing
-      // (from the values' reference back to the weights' in two steps: their distance may pass
-      // what fp32's exponents hold)
-      const float inv = L == 0.f ? 0.f : __fdividef(1.f, L);
-      const float half_way = ex2_approx(0.5f * (N - M));
-      auto scaled = [&](float s) { return s * inv * half_way * half_way; };
+      const float by = __shfl_sync(0xffffffffu, inv, r), h = __shfl_sync(0xffffffffu, half_way, r);
+      const float ls = __shfl_sync(0xffffffffu, own_lse, r);
+      const int row_out = __shfl_sync(0xffffffffu, own_row, r);
+      if (r >= rows_here) continue;
+      auto scaled = [&](float x) { return x * by * h * h; };
       o = make_float4(scaled(o.x), scaled(o.y), scaled(o.z), scaled(o.w));
-      const float ls = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
       if constexpr (kCluster) {
         *reinterpret_cast<float4*>(cluster_o + r * D + col) = o;
         if (col == 0) cluster_lse[r] = ls;
-      } else if (starts && ends) {
-        const size_t row = row_of(here, r);
+      } else if (whole) {
+        const size_t row = row_out;
         *reinterpret_cast<uint2*>(p.out + row * D + col) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
         if (p.lse != nullptr && col == 0) p.lse[row] = ls;
       } else {
@@ -696,6 +710,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
         if (col == 0) p.ws_lse[row] = ls;
       }
     }
+    __syncwarp();
     if (left == 0) {
       // the only segment that can go on into further CTAs is the last
       if (!kCluster && p.joints != nullptr && starts && !ends && threadIdx.x == 0)
@@ -745,9 +760,9 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
   }
 }
 
-template <int D, bool kFind>
+template <int D, int NT, bool kFind>
 __global__ void __launch_bounds__(kMergeThreads, kFind ? 5 : 6) decode_fp8_combine_kernel(const MergeParams p) {
-  merge_segment<D, fp8_unit_blocks(D), kFind, true>(p);
+  merge_segment<D, fp8_unit_blocks(D), fp8_end_units(D, 8 * NT), kFind, true>(p);
 }
 
 template <int D, int NT, bool kCluster>
@@ -811,8 +826,10 @@ cudaError_t launch_d(const DecodeFp8Args& a, const DeviceGuard& g, cudaStream_t 
   cp.rows = plan.rows;
   const int columns = a.queries * sp.group;
   const dim3 grid(columns < plan.rows ? columns : plan.rows, plan.joints > 0 ? plan.joints : a.num_seqs * cp.segs);
-  return launch_overlapped(plan.joints > 0 ? decode_fp8_combine_kernel<D, false> : decode_fp8_combine_kernel<D, true>,
-                           grid, kMergeThreads, 0, stream, 1, cp);
+  auto merge = [&](auto kernel) { return launch_overlapped(kernel, grid, kMergeThreads, 0, stream, 1, cp); };
+  if (plan.rows == 8)
+    return plan.joints > 0 ? merge(decode_fp8_combine_kernel<D, 1, false>) : merge(decode_fp8_combine_kernel<D, 1, true>);
+  return plan.joints > 0 ? merge(decode_fp8_combine_kernel<D, 2, false>) : merge(decode_fp8_combine_kernel<D, 2, true>);
 }
 
 }  // namespace

@@ -1,6 +1,7 @@
 // What the paged decode kernels over quantised caches share: how a call's work is
 // divided among the CTAs of one wave, the merge of partial outputs, and the
-// instructions that both use.  kUnit: blocks of 16 tokens in a unit of work.
+// instructions that both use.  kUnit: blocks of 16 tokens in a unit of work; kEnd: units
+// that the end of a segment, its merge and the change of queries, counts for.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -102,7 +103,7 @@ struct Shares {
 };
 
 // A place in the numbering of all segments: unit k of `units` of segment (seq, head,
-// chunk), or (k == units) the place that stands for the segment's end.
+// chunk), or (k >= units) a place that stands for the segment's end.
 struct Place {
   int seq, head, chunk, k, units, ctx;
 };
@@ -112,13 +113,13 @@ __device__ __forceinline__ int units_of(int ctx) {
   return (ctx + kUnit * kDecodeBlockSize - 1) / (kUnit * kDecodeBlockSize);
 }
 
-// Places of a segment: its units and one for its end, whose merge and change of
-// queries take a CTA about what a unit does (4-bit cache: 2400 cycles and 2100; with units
+// Places of a segment: its units and kEnd for its end, whose merge and change of
+// queries take a CTA time too (4-bit cache: 2400 cycles where a unit takes 2100; with units
 // alone the CTAs that got the short sequences of a batch were the last to finish, 128
 // sequences of 1 to 2000 tokens took 45.8 us, 38.4 with the ends counted).
-template <int kUnit>
+template <int kUnit, int kEnd>
 __device__ __forceinline__ int places_of(int ctx) {
-  return units_of<kUnit>(ctx) + (ctx > 0 ? 1 : 0);
+  return units_of<kUnit>(ctx) + (ctx > 0 ? kEnd : 0);
 }
 
 // Sums over the sequences that a warp forms from ctx_lens, each lane holding those of a
@@ -127,7 +128,7 @@ __device__ __forceinline__ int places_of(int ctx) {
 // sequences took each CTA 40 us before its first copy.  (Lengths are read more than
 // once; if another stream changes them meanwhile the result is undefined, but every
 // place that comes out is clamped to one that exists.)
-template <int kUnit>
+template <int kUnit, int kEnd>
 struct BatchOf {
   const int32_t* ctx_lens;
   int max_ctx, num_seqs;
@@ -140,7 +141,7 @@ struct BatchOf {
 
   // Clamped without a word: whoever handles the sequence reports it.
   __device__ __forceinline__ int ctx_of(int s) const { return max(0, min(max_ctx, __ldg(ctx_lens + s))); }
-  __device__ __forceinline__ int places_at(int s, int end) const { return s < end ? places_of<kUnit>(ctx_of(s)) : 0; }
+  __device__ __forceinline__ int places_at(int s, int end) const { return s < end ? places_of<kUnit, kEnd>(ctx_of(s)) : 0; }
 
   __device__ __forceinline__ BatchOf(const int32_t* lens, int seqs, int longest) {
     ctx_lens = lens;
@@ -154,7 +155,7 @@ struct BatchOf {
     if (alone) {
       const int end = min(seqs, lane_begin + range);
       if (lane_begin < end) first_ctx = ctx_of(lane_begin);
-      mine = places_of<kUnit>(first_ctx);
+      mine = places_of<kUnit, kEnd>(first_ctx);
 #pragma unroll
       for (int i = 1; i < kAlone; ++i) mine += places_at(lane_begin + i, end);
     } else {
@@ -191,8 +192,8 @@ struct BatchOf {
       int s = lane_begin, ctx = first_ctx;
       prefix = before;
       if ((threadIdx.x & 31) == lane)
-        while (target >= prefix + places_of<kUnit>(ctx) && s + 1 < num_seqs) {
-          prefix += places_of<kUnit>(ctx);
+        while (target >= prefix + places_of<kUnit, kEnd>(ctx) && s + 1 < num_seqs) {
+          prefix += places_of<kUnit, kEnd>(ctx);
           ctx = ctx_of(++s);
         }
       p.seq = min(num_seqs - 1, __shfl_sync(0xffffffffu, s, lane));
@@ -224,8 +225,8 @@ struct BatchOf {
     }
     p.units = max(1, units_of<kUnit>(p.ctx));
     const int rest = max(0, place - prefix * segs);
-    const int y = min(segs - 1, rest / (p.units + 1));
-    p.k = min(p.units, rest - y * (p.units + 1));
+    const int y = min(segs - 1, rest / (p.units + kEnd));
+    p.k = min(p.units + kEnd - 1, rest - y * (p.units + kEnd));
     p.head = n_chunks == 1 ? y : y / n_chunks;
     p.chunk = y - p.head * n_chunks;
     return p;
@@ -237,11 +238,11 @@ struct BatchOf {
     int prefix = before, ctx = first_ctx;
     if (num_seqs <= 32 * kAlone) {
       if ((threadIdx.x & 31) == lane)
-        for (int i = lane_begin; i < s; ctx = ctx_of(++i)) prefix += places_of<kUnit>(ctx);
+        for (int i = lane_begin; i < s; ctx = ctx_of(++i)) prefix += places_of<kUnit, kEnd>(ctx);
       return __shfl_sync(0xffffffffu, prefix, lane);
     }
     int sum = 0;
-    for (int i = lane * range + (threadIdx.x & 31); i < s; i += 32) sum += places_of<kUnit>(ctx_of(i));
+    for (int i = lane * range + (threadIdx.x & 31); i < s; i += 32) sum += places_of<kUnit, kEnd>(ctx_of(i));
     return __shfl_sync(0xffffffffu, prefix, lane) + __reduce_add_sync(0xffffffffu, sum);
   }
 };
@@ -299,7 +300,7 @@ struct MergeParams {
 // per thread; D/4 threads take four columns each of every kTeams-th partial output,
 // the first ones' loads on their way before the weights are known.
 // kMany: a segment's columns are the heads of several query tokens (SegmentJoint).
-template <int D, int kUnit, bool kFind, bool kMany>
+template <int D, int kUnit, int kEnd, bool kFind, bool kMany>
 __device__ __forceinline__ void merge_segment(const MergeParams& p) {
   constexpr int kTeams = kMergeThreads / (D / 4);
   constexpr int kMergeWarps = kMergeThreads / 32;
@@ -311,11 +312,11 @@ __device__ __forceinline__ void merge_segment(const MergeParams& p) {
   const int r = blockIdx.x;
   if constexpr (kFind) {
     if (threadIdx.x < 32) {
-      const BatchOf<kUnit> seqs(p.ctx_lens, p.num_seqs, p.max_blocks_per_seq * kDecodeBlockSize);
+      const BatchOf<kUnit, kEnd> seqs(p.ctx_lens, p.num_seqs, p.max_blocks_per_seq * kDecodeBlockSize);
       const Shares shares(seqs.per_segment * p.segs, p.ctas);
       const int seq = blockIdx.y / p.segs, y = blockIdx.y % p.segs;
       const int ctx = seqs.ctx_of(seq), units = units_of<kUnit>(ctx);
-      const int unit = seqs.before_seq(seq) * p.segs + y * places_of<kUnit>(ctx);  // the place of its first
+      const int unit = seqs.before_seq(seq) * p.segs + y * places_of<kUnit, kEnd>(ctx);  // the place of its first
       if (threadIdx.x == 0) {
         found.cta = units > 0 ? shares.owner(unit) : 0;
         found.more = units > 0 ? shares.owner(unit + units - 1) - found.cta : 0;

@@ -253,8 +253,10 @@ struct SplitPlan {
   bool shared;            // whether a segment's partial outputs can lie in several CTAs' workspace
   bool fits;              // the numbers of the work's places fit 32 bits
   // columns: query heads of a KV head, of all query tokens; unit_blocks: blocks in a unit of
-  // work; per_sm: CTAs that share an SM, with segments of 8 columns and of 16
-  SplitPlan(int num_seqs, int Hkv, int columns, int max_blocks_per_seq, int unit_blocks, int per_sm8, int per_sm16) {
+  // work; end_units: units that a segment's end counts for; per_sm: CTAs that share an SM,
+  // with segments of 8 columns and of 16
+  SplitPlan(int num_seqs, int Hkv, int columns, int max_blocks_per_seq, int unit_blocks, int end_units, int per_sm8,
+            int per_sm16) {
     rows = columns <= 8 ? 8 : 16;
     chunks = (columns + rows - 1) / rows;
     const long long segments = static_cast<long long>(num_seqs) * Hkv * chunks;
@@ -270,7 +272,7 @@ struct SplitPlan {
     if (cluster) ctas = static_cast<int>(segments * kSplitClusterCtas);
     shared = split && !cluster;
     joints = shared && segments > ctas ? ctas : 0;
-    fits = units + segments <= 0x7FFFFFFF;  // the places of units and of segments' ends
+    fits = units + end_units * segments <= 0x7FFFFFFF;  // the places of units and of segments' ends
   }
   size_t joint_bytes() const { return sizeof(SegmentJoint) * joints; }
   size_t part_bytes(int d) const { return sizeof(float) * 2 * ctas * rows * d; }
@@ -294,7 +296,8 @@ constexpr int kFp4ClusterUnits = kSplitClusterTokens / (kFp4UnitBlocks * kDecode
 
 struct Fp4Plan : SplitPlan {
   Fp4Plan(int num_seqs, int Hkv, int group, int max_blocks_per_seq)
-      : SplitPlan(num_seqs, Hkv, group, max_blocks_per_seq, kFp4UnitBlocks, fp4_decode_ctas(8), fp4_decode_ctas(16)) {}
+      : SplitPlan(num_seqs, Hkv, group, max_blocks_per_seq, kFp4UnitBlocks, 1, fp4_decode_ctas(8),
+                  fp4_decode_ctas(16)) {}
 };
 
 struct DecodeFp4Args {
@@ -316,6 +319,9 @@ cudaError_t launch_decode_fp4(const DecodeFp4Args& a, const DeviceGuard& g, cuda
 // warp, two for heads of 64.
 constexpr __host__ __device__ int fp8_unit_blocks(int d) { return d == 128 ? 4 : 8; }
 
+// Units that the end of a segment of `rows` columns counts for in the 8-bit decode.
+constexpr __host__ __device__ int fp8_end_units(int d, int rows) { return rows > 8 ? 4 : 2; }
+
 // CTAs of the 8-bit decode that share an SM, for segments of `rows` columns.
 constexpr __host__ __device__ int fp8_decode_ctas(int rows) { return rows > 8 ? 2 : 3; }
 
@@ -323,8 +329,8 @@ constexpr int kFp8MaxQueries = 16;  // query tokens of a sequence in one call
 
 struct Fp8Plan : SplitPlan {
   Fp8Plan(int num_seqs, int Hkv, int columns, int max_blocks_per_seq, int d)
-      : SplitPlan(num_seqs, Hkv, columns, max_blocks_per_seq, fp8_unit_blocks(d), fp8_decode_ctas(8),
-                  fp8_decode_ctas(16)) {}
+      : SplitPlan(num_seqs, Hkv, columns, max_blocks_per_seq, fp8_unit_blocks(d), fp8_end_units(d, columns),
+                  fp8_decode_ctas(8), fp8_decode_ctas(16)) {}
 };
 
 struct DecodeFp8Args {
