@@ -9,9 +9,8 @@
 namespace exattn {
 namespace {
 
-constexpr int kAppendThreads = 256;
-constexpr int kAppendWarps = kAppendThreads / 32;
-constexpr int kAppendCtas = 3;    // that share an SM
+constexpr int kAppendCtas = 3;    // of eight warps that share an SM
+constexpr long long kAppendLarge = 16 << 20;  // bytes of rows of a large call
 constexpr int kAppendStages = 2;  // heads of a warp on their way, and the one at hand
 constexpr int kBlk = kDecodeBlockSize;
 constexpr int kReadLanes = 4;
@@ -43,18 +42,19 @@ struct Added {
   }
 };
 
-template <int D>
+template <int D, int kWarps>
 struct AppendSmem {
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kPerTok = D / 16;              // lanes per token: 8 pairs each
   static constexpr int kSteps = kBlk * kPerTok / 32;  // rounds of a warp over 16 tokens
-  uint4 ring[kAppendWarps][kAppendStages][kSteps][2][32];  // a lane's two vectors of each round
+  uint4 ring[kWarps][kAppendStages][kSteps][2][32];  // a lane's two vectors of each round
   // Of a run: cosines and sines by token, then two pairs (float4) of each lane next to each
   // other, so that the lanes of a token read neighbouring vectors; and where each token lies.
   float4 angles[kBlk][4][kPerTok];
   int block[kBlk], place[kBlk];
-  int upto[kAppendThreads];     // runs of the sequences of this and earlier threads
-  Added added[kAppendThreads];  // where a thread has one sequence
-  int warp_sum[kAppendWarps];
+  int upto[kThreads];     // runs of the sequences of this and earlier threads
+  Added added[kThreads];  // where a thread has one sequence
+  int warp_sum[kWarps];
 };
 
 __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.4028234663852886e38f; }
@@ -88,17 +88,18 @@ __device__ __forceinline__ void rescale(uint8_t* codes, int from, int to, int fi
 }
 
 // kSingle: each sequence has one token; runs are `tile` of them.
-template <int D, bool kSingle>
-__global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
+template <int D, bool kSingle, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? kAppendCtas : 1)
     rope_cache_fp8_kernel(const RopeFp8Args a, const __grid_constant__ RopeAxesTable table, const int tile,
                           const int splits) {
   using Span = Fp8Span<D>;
-  using Smem = AppendSmem<D>;
+  using Smem = AppendSmem<D, kWarps>;
+  constexpr int kThreads = Smem::kThreads;
   constexpr int kHalf = D / 2, kApart = kHalf / 8;  // 16-byte vectors between the halves of a row
   constexpr int kPerTok = Smem::kPerTok, kSteps = Smem::kSteps;
   constexpr int kToks = 32 / kPerTok;               // tokens of a warp at once
-  constexpr int kAtOnce = kAppendThreads / kHalf;   // tokens whose angles the threads form at once
-  constexpr int kAngles = kBlk / kAtOnce;
+  constexpr int kAtOnce = kThreads / kHalf;   // tokens whose angles the threads form at once
+  constexpr int kAngles = (kBlk + kAtOnce - 1) / kAtOnce;
   extern __shared__ __align__(16) uint8_t append_smem[];
   Smem& sm = *reinterpret_cast<Smem*>(append_smem);
 
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
   cudaGridDependencySynchronize();
 
   // ---- the runs: counted from token_starts, or `tile` sequences each
-  const int per = (a.num_seqs + kAppendThreads - 1) / kAppendThreads;
+  const int per = (a.num_seqs + kThreads - 1) / kThreads;
   auto added_of = [&](int s) {
     return Added{__ldg(a.token_starts + s), __ldg(a.token_starts + s + 1), __ldg(a.ctx_lens + s)};
   };
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
     }
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kAppendWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       if (w < warp) sum += sm.warp_sum[w];
       total += sm.warp_sum[w];
     }
@@ -154,10 +155,9 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
   auto find_run = [&](int r) {
     if constexpr (kSingle) return Run{r * tile, min(tile, a.num_seqs - r * tile), r * tile, 0, 0};
     // the first thread with upto > r, by the warp: its warp's place, then its own
-    static_assert(kAppendThreads == 32 * kAppendWarps, "lanes look at every eighth entry");
-    const int eighth = min(31, __popc(__ballot_sync(0xffffffffu, sm.upto[kAppendWarps * lane + kAppendWarps - 1] <= r)));
-    const bool past = lane < kAppendWarps && sm.upto[kAppendWarps * eighth + min(lane, kAppendWarps - 1)] <= r;
-    const int lo = kAppendWarps * eighth + min(kAppendWarps - 1, __popc(__ballot_sync(0xffffffffu, past)));
+    const int eighth = min(31, __popc(__ballot_sync(0xffffffffu, sm.upto[kWarps * lane + kWarps - 1] <= r)));
+    const bool past = lane < kWarps && sm.upto[kWarps * eighth + min(lane, kWarps - 1)] <= r;
+    const int lo = kWarps * eighth + min(kWarps - 1, __popc(__ballot_sync(0xffffffffu, past)));
     r -= lo > 0 ? sm.upto[lo - 1] : 0;
     if (per == 1) return sm.added[lo].run(lo, r);
     int s = lo * per;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
         }
         row += kToks * view.token;
       }
-      to_item += splits * kAppendWarps;
+      to_item += splits * kWarps;
     }
     cp_async_commit();
   };
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
     const bool more = unit + static_cast<int>(gridDim.x) < units;
     const Run next = more ? find_run((unit + gridDim.x) / splits) : run;
     if (more) ask(next);
-    for (int item = unit % splits + splits * warp; item < items; item += splits * kAppendWarps) {
+    for (int item = unit % splits + splits * warp; item < items; item += splits * kWarps) {
       const bool value = item >= first_value, query = item >= first_query;
       const int head = item - (query ? first_query : value ? first_value : 0);
       cp_async_wait<kAppendStages - 2>();
@@ -458,29 +458,41 @@ __global__ void __launch_bounds__(kTileThreads, 8) cache_read_fp8_kernel(const R
   }
 }
 
-template <int D, bool kSingle>
-cudaError_t launch_append(const RopeFp8Args& a, const RopeAxesTable& table, int sms, cudaStream_t stream) {
-  const size_t smem = sizeof(AppendSmem<D>);
+template <int D, bool kSingle, int kWarps>
+cudaError_t launch_append(const RopeFp8Args& a, const RopeAxesTable& table, int sms, long long runs, int tile,
+                          cudaStream_t stream) {
+  using Smem = AppendSmem<D, kWarps>;
   static std::atomic<int> smem_set[64] = {};
-  const cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(rope_cache_fp8_kernel<D, kSingle>),
-                                        static_cast<int>(smem), smem_set);
+  const cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(rope_cache_fp8_kernel<D, kSingle, kWarps>),
+                                        static_cast<int>(sizeof(Smem)), smem_set);
   if (e != cudaSuccess) return e;
-  // Small calls take so few CTAs that those of two launches fit on the SMs together, one's
-  // start under the other's end.
-  const int items = a.Hq + 2 * a.Hkv, most = (items + kAppendWarps - 1) / kAppendWarps;  // most: an item for each warp
-  const int fit = sms * kAppendCtas / 2;
-  int tile = 32 / AppendSmem<D>::kPerTok;  // tokens that a warp's lanes take at once
-  int runs;
-  if (kSingle) {
-    while (tile < kBlk && (a.num_tokens + tile - 1) / tile * most > fit) tile *= 2;
-    runs = (a.num_tokens + tile - 1) / tile;
-  } else {  // about as many as the call can have
-    runs = a.num_tokens / kBlk + (a.num_seqs < a.num_tokens ? a.num_seqs : a.num_tokens);
+  // Few runs are divided among as many CTAs as fit under the end of a launch before (half of
+  // the places on the SMs), down to an item for each warp.
+  const int places = sms * (kWarps == 8 ? kAppendCtas : 1), few = kWarps == 8 ? places / 2 : places;
+  const int most = (a.Hq + 2 * a.Hkv + kWarps - 1) / kWarps;
+  const int splits = runs * most <= few ? most : runs < few ? static_cast<int>(few / runs) : 1;
+  const long long units = runs * splits;
+  return launch_overlapped(rope_cache_fp8_kernel<D, kSingle, kWarps>, static_cast<unsigned int>(units < places ? units : places),
+                           Smem::kThreads, sizeof(Smem), stream, 1, a, table, tile, splits);
+}
+
+template <int D>
+cudaError_t launch_append_d(const RopeFp8Args& a, const RopeAxesTable& table, int sms, cudaStream_t stream) {
+  const long long items = a.Hq + 2 * a.Hkv;
+  if (a.token_starts == nullptr) {
+    const long long most = (items + 7) / 8;
+    int tile = 32 / AppendSmem<D, 8>::kPerTok;  // tokens that a warp's lanes take at once
+    while (tile < kBlk && (a.num_tokens + tile - 1) / tile * most > sms * kAppendCtas / 2) tile *= 2;
+    return launch_append<D, true, 8>(a, table, sms, (a.num_tokens + tile - 1) / tile, tile, stream);
   }
-  const int splits = runs * most <= fit ? most : runs < fit ? fit / runs : 1;
-  const int units = runs * splits;
-  return launch_overlapped(rope_cache_fp8_kernel<D, kSingle>, units < sms * kAppendCtas ? units : sms * kAppendCtas,
-                           kAppendThreads, smem, stream, 1, a, table, tile, splits);
+  // About as many runs as the call can have.  Large calls whose runs fill one CTA an SM or
+  // many take CTAs of 16 warps, each run's tokens in longer stretches: 64 x 256 tokens (32 + 2 x 8
+  // heads of 128) 59.9 us, 62.0 with three of eight; 2048 tokens 9.7 and 11.1; but 2048 tokens
+  // and 63 single ones 13.7 and 11.6, and small calls lose the overlap (64 tokens 3.0 and 2.7).
+  const long long runs = a.num_tokens / kBlk + (a.num_seqs < a.num_tokens ? a.num_seqs : a.num_tokens);
+  if (a.num_tokens * items * D * 2 > kAppendLarge && (runs <= sms || runs > sms * kAppendCtas))
+    return launch_append<D, false, 16>(a, table, sms, runs, 1, stream);
+  return launch_append<D, false, 8>(a, table, sms, runs, 1, stream);
 }
 
 }  // namespace
@@ -488,9 +500,7 @@ cudaError_t launch_append(const RopeFp8Args& a, const RopeAxesTable& table, int 
 cudaError_t launch_rope_cache_write_fp8(const RopeFp8Args& a, const RopeAxesTable& table, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  if (a.token_starts == nullptr)
-    return a.d == 64 ? launch_append<64, true>(a, table, sms, stream) : launch_append<128, true>(a, table, sms, stream);
-  return a.d == 64 ? launch_append<64, false>(a, table, sms, stream) : launch_append<128, false>(a, table, sms, stream);
+  return a.d == 64 ? launch_append_d<64>(a, table, sms, stream) : launch_append_d<128>(a, table, sms, stream);
 }
 
 cudaError_t launch_cache_read_fp8(const ReadFp8Args& a, cudaStream_t stream) {

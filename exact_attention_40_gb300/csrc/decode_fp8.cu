@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
         // reference is taken from it, as it was when it gave that: in one fused
         // operation the largest itself would lie off by the rounding, which passes all
         // that fp16 holds once scores come to 2^28.
-        float x[kPer][NT][4], shift[kPer][NT][2];  // y = x + shift
+        float x[kPer][NT][4], y[kPer][NT][4];
         auto distances = [&]() {
           float most = -INFINITY;
 #pragma unroll
@@ -491,14 +491,13 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const uint64_t mm = f2_pack(m[nt][0], m[nt][1]);
+              const uint64_t nn = f2_pack(n[nt][0] - value_exp[b], n[nt][1] - value_exp[b]);
 #pragma unroll
-              for (int z = 0; z < 4; z += 2)
-                f2_unpack(f2_sub(f2_pack(c[b][nt][z], c[b][nt][z + 1]), mm), x[b][nt][z], x[b][nt][z + 1]);
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                shift[b][nt][j] = (m[nt][j] - n[nt][j]) + value_exp[b];
-                const float top = fmaxf(x[b][nt][j], x[b][nt][2 + j]);
-                most = max3f(most, top, top + shift[b][nt][j]);
+              for (int z = 0; z < 4; z += 2) {
+                const uint64_t s = f2_pack(c[b][nt][z], c[b][nt][z + 1]);
+                f2_unpack(f2_sub(s, mm), x[b][nt][z], x[b][nt][z + 1]);
+                f2_unpack(f2_sub(s, nn), y[b][nt][z], y[b][nt][z + 1]);
+                most = max3f(most, max3f(x[b][nt][z], x[b][nt][z + 1], y[b][nt][z]), y[b][nt][z + 1]);
               }
             }
           return most;
@@ -548,7 +547,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               l[nt][z & 1] += ex2_approx(x[b][nt][z]);
-              w[z] = ex2_approx(x[b][nt][z] + shift[b][nt][z & 1]);
+              w[z] = ex2_approx(y[b][nt][z]);
             }
             pb[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
             pb[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));

@@ -549,6 +549,13 @@ def test_append_many_sequences(env, S):
     run_append(env, append_case(541, held, new, 2, 1, 64), 1, 64, (32,))
 
 
+@pytest.mark.parametrize("held,new,Hq,Hkv,d", [([5, 0], [1100, 1100], 40, 4, 128), ([0] * 4, [1850] * 4, 3, 3, 128),
+                                                ([3] * 4, [2600] * 4, 7, 2, 64)])
+def test_append_large_calls(env, held, new, Hq, Hkv, d):
+    """Ones that take a CTA an SM: with fewer runs than these, and with many."""
+    run_append(env, append_case(548, held, new, Hq, Hkv, d), Hkv, d, (d // 2,))
+
+
 @pytest.mark.parametrize("S", [1, 300, 3000])
 def test_append_a_token_for_each_sequence(env, S):
     held = np.floor(synth.uniform01(545, S) * 50).astype(np.int32)
