@@ -1,6 +1,52 @@
 // One-token paged decode over the 8-bit cache (layout in fp8.cuh) for sm_103a, and the
 // decode of a few tokens of each sequence at once: split-KV partial attention plus a
 // log-sum-exp merge.
+//
+//   s_ij = scale <q_i, kc_j> ks_j,   o_i = sum_j exp(s_ij - m_i) vs_j vc_j / sum_j exp(s_ij - m_i)
+//   with kc, vc the codes and ks, vs the scales of j's block.
+//
+// decode_fp8_split_kernel: the frame of the 4-bit decode (decode_shares.cuh).  The work is
+//   units of 16.5 KB, 64 tokens of heads of 128 or 128 of heads of 64, of one (sequence, KV
+//   head, chunk of up to 8 NT columns), its segment; a column is a query head of one of the
+//   query tokens.  Each CTA takes an equal, contiguous share of all segments' units, found
+//   from ctx_lens.  One warp copies, a bulk copy for each block's span; four compute, a block
+//   of each unit for a warp (two at d = 64), transposed, so that tokens are the rows of
+//   mma.sync m16n8k16 and columns its 8 columns:
+//     S^T = K Q^T      A = keys [16 tokens x 16 columns], B = queries
+//     O^T += V^T P^T   A = values [16 columns x 16 tokens], B = weights.
+//   The scales are kept out of the products: a block's key scale, a power of two, goes into
+//   the factor of its scores, and its value scale into the exponent of the weights that the
+//   second product takes.  So a code only has to become fp16, one cvt for two, and both enter
+//   exactly.  The sum of the weights has a reference m of its own, the weighted values one (n)
+//   that follows score + value exponent: whatever the blocks' scales, the largest weight of
+//   the product lies between 2^7 and 2^15, where fp16 rounds those above 2^-21 of it by at
+//   most 2^-11 of themselves and the rest by 2^-32 of it.  The sum takes the weights unrounded
+//   in fp32.  (Two exponentials a score: with one reference for both, a block of large values
+//   and small weights would be rounded away, or pass what fp16 holds.)
+//   Query tokens before the last see fewer keys: their scores are masked in the units that
+//   reach past what the first of them sees, and a value that only some see, if it is NaN,
+//   is multiplied for each of them apart.
+//   What bounds it: HBM for up to 8 columns and long contexts (64 sequences of 8192 tokens, 32
+//   heads over 8 of 128: 164 to 168 us = 6.4 to 6.6 TB/s, 95 to 97% of a copy; 64 sequences of 512
+//   to 8192 tokens 92.3 us = 6.2 TB/s with the merge).  A unit takes a warp 1100 cycles
+//   (scores 370, distances and vote 100, products 360, the rest waits), which twelve warps an SM
+//   overlap.  For 9 to 16 columns 168 registers leave room for eight computing warps, whose
+//   units take 1390 cycles (440, 150, 485), and their latency bounds it: 32 sequences of 512 to
+//   8192 tokens, 96 heads over 8: 61 us; four queries of 32 heads over 8: 65.0 us = 4.4 TB/s.
+//   Chunks of 16 columns read the keys and values once each (64 columns, 16 sequences of 4000
+//   tokens: 101.5 us).  Short contexts pay for the ends of their segments, 1450 to 4500 cycles
+//   (4096 sequences of 200 tokens, 8 heads over 2: 91.9 us), few of them for the chain
+//   ctx_lens -> table -> copies -> merge (one of 32768 tokens 16.7 us, its bytes' time 9.9).
+//   Small calls take a cluster of 8 CTAs for each segment, which take its units in turn and
+//   merge through distributed shared memory: one launch, no workspace (six of up to 1500 tokens
+//   4.2 us).
+//   Measured and not taken: the scores of a unit beside the products of the one before (four
+//   queries 85 us, 4096 x 200 104), two chains of a score's products (68, no change for 8 columns),
+//   two blocks a warp for 16 columns (68 to 77), the queries of 16 columns in shared memory and
+//   three CTAs (77, with spills), 16 columns as two chunks of 8 (91), tcgen05 with units of 128
+//   tokens (74: a unit's hand-overs between copies, conversions, scores, softmax and products
+//   take longer than its bytes; only at 64 columns 97 against 101).
+// decode_fp8_combine_kernel: merges the partial outputs of a segment.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -159,14 +205,14 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
     x.units = max(1, units_of<kUnit>(x.ctx));
   };
   const bool copies = warp == kWarps;
-  int phys_lane = -1;  // of the copying warp: physical block of block lane % 8 of a batch's unit lane / 8; -1: none
+  int phys_lane = -1;  // of the copying warp: physical block of block lane % kUnit of a batch's unit lane / kUnit; -1: none
   auto check = [&](int ph) {
     if (ph >= 0 && ph < p.num_blocks) return ph;
     atomicOr(p.status, 2u);  // EXATTN_DEVICE_BOUNDS_BIT
     return -1;
   };
   if constexpr (kCluster) {
-    // Every 8th unit, so that the table entries and queries need not wait for the
+    // Every kStep-th unit, so that the table entries and queries need not wait for the
     // context length: the three loads are in flight together.
     static_assert(kSplitClusterTokens / kUnitTokens / kSplitClusterCtas <= 32 / kUnit, "one batch of table entries");
     const int seg = cta / kSplitClusterCtas;
@@ -220,7 +266,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
     const uint32_t blk_bytes = static_cast<uint32_t>(p.Hkv) * Span::kBytes;
     Place to = at;
     int to_load = left;  // places whose table entries are not yet asked for
-    // A batch: up to four units of one segment; lane 8 i + b has unit i's block b.
+    // A batch: as many units of one segment as lanes have blocks; lane kUnit i + b has unit i's block b.
     struct Entries {
       int units, raw;  // raw: this lane's table entry, if it has one (`mine`)
       bool mine;
@@ -348,7 +394,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
     const int n_units = kCluster ? left : min(at.units - at.k, left);
     const bool ends = at.k + n_units == at.units;
 
-    int exponent[NT][2];  // of the power of two that heads 2t, 2t + 1 were divided by
+    int exponent[NT][2];  // of the power of two that columns 2t, 2t + 1 were divided by
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float top = 0.f;
@@ -376,7 +422,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
       exponent[nt][1] = __shfl_sync(0xffffffffu, e, 8 * t + 4);
     }
 
-    // Of heads 2t, 2t + 1: m and n, the references of weights and of weighted values; l,
+    // Of columns 2t, 2t + 1: m and n, the references of weights and of weighted values; l,
     // the sum of this lane's tokens' weights.
     float m[NT][2], n[NT][2], l[NT][2];
     float acc[kMTiles][NT][4];
@@ -458,7 +504,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
         };
         scores(std::integral_constant<int, 0>());
         if constexpr (kPer == 2) scores(std::integral_constant<int, 1>());
-        // ---- online softmax: c[b][nt][j] is token tok_s, head 2t + j, c[b][nt][2 + j]
+        // ---- online softmax: c[b][nt][j] is token tok_s, column 2t + j, c[b][nt][2 + j]
         // token tok_s + 8.  Tokens that do not count are masked here and their values
         // zeroed below (the slots may hold anything).
         if (!full) {

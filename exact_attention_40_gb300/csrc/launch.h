@@ -28,8 +28,8 @@ inline int device_sm_count() {
 // Launches a kernel that may take its place on the SMs while the last CTAs of the one before
 // it on the stream end (programmatic dependent launch): about 1 us of a launch's 2
 // to 3.  Every thread of it calls cudaGridDependencySynchronize before it reads or writes
-// any tensor.  The 4-bit decode lets the next kernel (its merge, or what follows a
-// small call) in earlier, after its own wait, so that what came before both has ended
+// any tensor.  The decodes over quantised caches let the next kernel (their merge, or what
+// follows a small call) in earlier, after its own wait, so that what came before both has ended
 // by then.  The others do not: CTAs of the next call would take slots that the present
 // one's last CTAs want (rotation of 3 x 1001 tokens 5.5 us against 4.6; the same trigger
 // in the merge, decode of 9 sequences of 1000 to 4000 tokens, 15.0 against 12.4).
@@ -319,10 +319,18 @@ cudaError_t launch_decode_fp4(const DecodeFp4Args& a, const DeviceGuard& g, cuda
 // warp, two for heads of 64.
 constexpr __host__ __device__ int fp8_unit_blocks(int d) { return d == 128 ? 4 : 8; }
 
-// Units that the end of a segment of `rows` columns counts for in the 8-bit decode.
+// Units that the end of a segment of `rows` columns counts for in the 8-bit decode.  (Counted
+// for too few, the CTAs with short sequences finish last.  16 columns, four queries of 32
+// sequences of 512 to 8192 tokens: 73.5 us with one, 69.4 with two, 66.8 with three, 64.9 with
+// four; 8 columns, 128 sequences of 1 to 2000 tokens, 8 heads over 8 of 64: 28.9 with one,
+// 28.2 with two.)
 constexpr __host__ __device__ int fp8_end_units(int d, int rows) { return rows > 8 ? 4 : 2; }
 
-// CTAs of the 8-bit decode that share an SM, for segments of `rows` columns.
+// CTAs of the 8-bit decode that share an SM, for segments of `rows` columns: three of four
+// computing warps and three units of shared memory, or two with four units where 16 columns
+// take 168 registers.  (Without a copying warp, each warp copying its own blocks, four and
+// three fit and are slower: a batch of 64 sequences 98 us against 92, four queries of 32 sequences
+// 81 against 65.)
 constexpr __host__ __device__ int fp8_decode_ctas(int rows) { return rows > 8 ? 2 : 3; }
 
 constexpr int kFp8MaxQueries = 16;  // query tokens of a sequence in one call
