@@ -54,7 +54,7 @@ void check(const Tensor& t, const char* name, c10::Device device, at::IntArrayRe
     if (shape[i] >= 0 && t.size(i) != shape[i])
       fail(PyExc_ValueError, "%s: size of dimension %d must be %lld, got %lld", name, static_cast<int>(i),
            static_cast<long long>(shape[i]), static_cast<long long>(t.size(i)));
-  if (contiguous ? !t.is_contiguous() : t.stride(-1) != 1)
+  if (contiguous ? !t.is_contiguous() : t.stride(-1) != 1 && t.numel() > 0)  // (an empty one's strides mean nothing)
     fail(PyExc_ValueError, contiguous ? "%s must be contiguous" : "the last dimension of %s must be contiguous", name);
 }
 
