@@ -427,7 +427,9 @@ int attn_decode_paged_fp4(const void* q, const void* kv_cache, const int32_t* bl
  * are then brought to the larger scale (rounded once more, which changes those that
  * fall below 2^-6 of it).  A call that writes a block's place 0 starts its scales anew
  * from its own tokens, so that a block's memory can be given to another sequence: what
- * the block's other places held is void then.  Elements that are not finite are stored
+ * the block's other places held is void then.  Tokens that are taken back (drafted ones that
+ * were not kept: the next call's ctx_lens count without them) leave the scale as large as
+ * they made it.  Elements that are not finite are stored
  * and read back as NaN.  A cache starts as zeros.
  * attn_fp8_cache_bytes: its size (0 for invalid arguments).  d is 64 or 128 for
  * every call on it.

@@ -186,3 +186,19 @@ def test_layers_of_one_tensor(env):
     out, lse = ex.attn_decode_paged_fp8(to_dev(q, dev), pool[1], tbl, ctx)
     check_decode(out, lse, q, want.cpu().numpy(), c["table"], c["ctx"], d, d ** -0.5)
     assert ex.attn_get_device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_drafted_tokens_taken_back(env, d):
+    """Four drafted tokens, large ones among them, of which some are kept: the next step writes
+    over the others, in the same block, in the one before and at a block's beginning."""
+    torch, ex, dev = env
+    first = append_case(912, [5, 30, 14, 16, 0], [4, 4, 4, 4, 4], 4, 2, d, gain=64.0, room=16)
+    cache = run_append(env, first, 2, d, (d // 2,))
+    step = append_case(913, [7, 31, 15, 16, 0], [4, 1, 4, 4, 2], 4, 2, d)
+    step["table"], step["cache"] = first["table"], cache.cpu().numpy()
+    after = run_append(env, step, 2, d, (d // 2,))
+    q = synth.normal_bf16(914, 0, (5, 2, 4, d))
+    out, lse = ex.attn_decode_paged_fp8(to_dev(q, dev), after, to_dev(step["table"], dev), to_dev(step["ctx"], dev))
+    check_decode(out, lse, q, after.cpu().numpy(), step["table"], step["ctx"], d, d ** -0.5)
+    assert ex.attn_get_device_status() == 0
