@@ -36,7 +36,7 @@
 //   Chunks of 16 columns read the keys and values once each (64 columns, 16 sequences of 4000
 //   tokens: 101.5 us).  Short contexts pay for the ends of their segments, 1450 to 4500 cycles
 //   (4096 sequences of 200 tokens, 8 heads over 2: 91.9 us), few of them for the chain
-//   ctx_lens -> table -> copies -> merge (one of 32768 tokens 16.7 us, its bytes' time 9.9).
+//   ctx_lens -> table -> copies -> merge (one of 32768 tokens 16.3 us, its bytes' time 9.9).
 //   Small calls take a cluster of 8 CTAs for each segment, which take its units in turn and
 //   merge through distributed shared memory: one launch, no workspace (six of up to 1500 tokens
 //   4.2 us).
@@ -49,8 +49,8 @@
 //   e4m3 numbers (84: it is slower here than conversions and fp16), tcgen05 with units of 128
 //   tokens (74: a unit's hand-overs between copies, conversions, scores, softmax and products
 //   take longer than its bytes; only at 64 columns 97 against 101).
-// decode_fp8_combine_kernel: merges the partial outputs of a segment: 2.6 us of a call, its
-//   launch included.
+// decode_fp8_combine_kernel: merges the partial outputs of a segment: 2 to 2.6 us of a
+//   call, its launch included.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -809,9 +809,9 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
   }
 }
 
-template <int D, int NT, bool kFind>
+template <int D, int NT, bool kFind, int kCuts>
 __global__ void __launch_bounds__(kMergeThreads, kFind ? 5 : 6) decode_fp8_combine_kernel(const MergeParams p) {
-  merge_segment<D, fp8_unit_blocks(D), fp8_end_units(D, 8 * NT), kFind, true>(p);
+  merge_segment<D, fp8_unit_blocks(D), fp8_end_units(D, 8 * NT), kFind, true, kCuts>(p);
 }
 
 template <int D, int NT, bool kCluster>
@@ -874,11 +874,22 @@ cudaError_t launch_d(const DecodeFp8Args& a, const DeviceGuard& g, cudaStream_t 
   cp.ctas = plan.ctas;
   cp.rows = plan.rows;
   const int columns = a.queries * sp.group;
-  const dim3 grid(columns < plan.rows ? columns : plan.rows, plan.joints > 0 ? plan.joints : a.num_seqs * cp.segs);
-  auto merge = [&](auto kernel) { return launch_overlapped(kernel, grid, kMergeThreads, 0, stream, 1, cp); };
-  if (plan.rows == 8)
-    return plan.joints > 0 ? merge(decode_fp8_combine_kernel<D, 1, false>) : merge(decode_fp8_combine_kernel<D, 1, true>);
-  return plan.joints > 0 ? merge(decode_fp8_combine_kernel<D, 2, false>) : merge(decode_fp8_combine_kernel<D, 2, true>);
+  const int rows = columns < plan.rows ? columns : plan.rows;
+  auto merge = [&](auto kernel, int segments, int cuts) {
+    return launch_overlapped(kernel, dim3(rows, segments, cuts), kMergeThreads, 0, stream, 1, cp);
+  };
+  auto merge_of = [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    const int segments = a.num_seqs * cp.segs;
+    if (plan.joints > 0) return merge(decode_fp8_combine_kernel<D, NT, false, 1>, plan.joints, 1);
+    // Few rows are cut, so that all their partial outputs are on their way at once: one
+    // sequence of 8000 tokens (32 rows) 8.3 us with four cuts, 8.6 with two, 8.9 with none;
+    // four queries of two (256 rows) 15.1, 13.0 and 13.4; nine sequences (288) 15.8, 13.5, 13.4.
+    if (rows * segments <= 64) return merge(decode_fp8_combine_kernel<D, NT, true, 4>, segments, 4);
+    if (rows * segments <= 256) return merge(decode_fp8_combine_kernel<D, NT, true, 2>, segments, 2);
+    return merge(decode_fp8_combine_kernel<D, NT, true, 1>, segments, 1);
+  };
+  return plan.rows == 8 ? merge_of(std::integral_constant<int, 1>()) : merge_of(std::integral_constant<int, 2>());
 }
 
 }  // namespace

@@ -297,17 +297,20 @@ struct MergeParams {
 // would leave it no room beside a split kernel for 16 heads (32 sequences of 96 heads
 // 59.7 us, 55.4 with 48), and fewer slow the search (one of 8000 tokens 8.4 us with 66,
 // 8.8 with 48, 9.1 with 40).  The weights are formed once, one
-// per thread; D/4 threads take four columns each of every kTeams-th partial output,
+// per thread; kVecs threads take four columns each of every kTeams-th partial output,
 // the first ones' loads on their way before the weights are known.
 // kMany: a segment's columns are the heads of several query tokens (SegmentJoint).
-template <int D, int kUnit, int kEnd, bool kFind, bool kMany>
+// kCuts: CTAs that share a row, each a part of its d columns.
+template <int D, int kUnit, int kEnd, bool kFind, bool kMany, int kCuts = 1>
 __device__ __forceinline__ void merge_segment(const MergeParams& p) {
-  constexpr int kTeams = kMergeThreads / (D / 4);
+  constexpr int kVecs = D / 4 / kCuts;  // vectors of four columns
+  constexpr int kTeams = kMergeThreads / kVecs;
   constexpr int kMergeWarps = kMergeThreads / 32;
   constexpr int kEarly = 3;
   __shared__ float weight[kSplitMaxCtas];
   __shared__ float top[kMergeWarps], sum[kMergeWarps];
-  __shared__ float4 part[kTeams][D / 4];
+  constexpr int kSums = kCuts > 1 ? kMergeWarps : kTeams;  // (with cuts a warp's teams add up by shuffles first)
+  __shared__ float4 part[kSums][kVecs];
   __shared__ SegmentJoint found;
   const int r = blockIdx.x;
   if constexpr (kFind) {
@@ -338,7 +341,8 @@ __device__ __forceinline__ void merge_segment(const MergeParams& p) {
   if (joint.more == 0 || r >= (kMany ? joint.columns() : joint.rows)) return;
   const int used = joint.more + 1;
   auto place = [&](int i) { return static_cast<size_t>(2 * (joint.cta + i) + (i == 0 ? 1 : 0)) * p.rows + r; };
-  const int col = threadIdx.x % (D / 4), team = threadIdx.x / (D / 4);
+  const int vec = threadIdx.x % kVecs, team = threadIdx.x / kVecs;
+  const int col = kCuts == 1 ? vec : blockIdx.z * kVecs + vec;
   auto part_of = [&](int s) { return reinterpret_cast<const float4*>(p.ws_o + place(s) * D)[col]; };
   float4 early[kEarly];
 #pragma unroll
@@ -383,12 +387,24 @@ __device__ __forceinline__ void merge_segment(const MergeParams& p) {
     if (team + i * kTeams < used) add(weight[team + i * kTeams], early[i]);
 #pragma unroll 4
   for (int s = team + kEarly * kTeams; s < used; s += kTeams) add(weight[s], part_of(s));
-  part[team][col] = o;
-  __syncthreads();
-  if (threadIdx.x < D / 4) {
+  if constexpr (kCuts > 1) {
 #pragma unroll
-    for (int x = 1; x < kTeams; ++x) {
-      const float4 a = part[x][col];
+    for (int x = kVecs; x < 32; x *= 2) {
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
+      o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
+      o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
+    }
+    if ((threadIdx.x & 31) < kVecs) part[threadIdx.x >> 5][vec] = o;
+  } else {
+    part[team][vec] = o;
+  }
+  __syncthreads();
+  if (threadIdx.x < kVecs) {
+    if constexpr (kCuts > 1) o = part[0][vec];
+#pragma unroll
+    for (int x = 1; x < kSums; ++x) {
+      const float4 a = part[x][vec];
       o.x += a.x;
       o.y += a.y;
       o.z += a.z;
