@@ -463,7 +463,11 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
           most_valid = max(most_valid, n_valid[b]);
         }
       }
-      if (most_valid > 0) {
+      // Units that count whole have code of their own, without the masks: the loop over
+      // them then fits the instruction caches better (four queries of 32 sequences 64.9 us
+      // with one code for both, 62.9 with two; 96 heads over 8 60.8 and 58.7).
+      auto compute = [&](auto whole_unit) {
+        constexpr bool full = decltype(whole_unit)::value;
         // ---- S^T = K Q^T, with the score's factor and the key scale
         float c[kPer][NT][4];
         float value_exp[kPer];  // exponent of the block's value scale
@@ -669,7 +673,11 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
         };
         products(std::integral_constant<int, 0>());
         if constexpr (kPer == 2) products(std::integral_constant<int, 1>());
-      }
+      };
+      if (full)
+        compute(std::integral_constant<bool, true>());
+      else if (most_valid > 0)
+        compute(std::integral_constant<bool, false>());
       __syncwarp();  // all lanes are done with this stage
       if (lane == 0) mbar_arrive(&sm.empty[st]);
       if (++st == kStages) {
