@@ -32,15 +32,15 @@
 //   (scores 370, distances and vote 100, products 360, the rest waits), which twelve warps an SM
 //   overlap.  For 9 to 16 columns 168 registers leave room for eight computing warps, whose
 //   units take 1390 cycles (440, 150, 485), and their latency bounds it: 32 sequences of 512 to
-//   8192 tokens, 96 heads over 8: 61 us; four queries of 32 heads over 8: 65.0 us = 4.4 TB/s.
+//   8192 tokens, 96 heads over 8: 59.0 us; four queries of 32 heads over 8: 63.6 us = 4.5 TB/s.
 //   Chunks of 16 columns read the keys and values once each (64 columns, 16 sequences of 4000
-//   tokens: 101.5 us).  Short contexts pay for the ends of their segments, 1450 to 4500 cycles
-//   (4096 sequences of 200 tokens, 8 heads over 2: 91.9 us), few of them for the chain
-//   ctx_lens -> table -> copies -> merge (one of 32768 tokens 16.3 us, its bytes' time 9.9).
+//   tokens: 97.9 us).  Short contexts pay for the ends of their segments, 1450 to 4500 cycles
+//   (4096 sequences of 200 tokens, 8 heads over 2: 89.1 us), few of them for the chain
+//   ctx_lens -> table -> copies -> merge (one of 32768 tokens 15.9 us, its bytes' time 9.9).
 //   Small calls take a cluster of 8 CTAs for each segment, which take its units in turn and
 //   merge through distributed shared memory: one launch, no workspace (six of up to 1500 tokens
 //   4.2 us).
-//   Measured and not taken: the scores of a unit beside the products of the one before (four
+//   Measured and not taken (four queries 64.9 us then): the scores of a unit beside the products of the one before (four
 //   queries 85 us, 4096 x 200 104), two chains of a score's products (68, no change for 8 columns),
 //   two blocks a warp for 16 columns (68 to 77), the queries of 16 columns in shared memory and
 //   three CTAs (77, with spills), 16 columns as two chunks of 8 (91) or as two warps that read
@@ -48,11 +48,12 @@
 //   both with three CTAs), scores by mma.sync on the e4m3 keys themselves with each query as two
 //   e4m3 numbers (84: it is slower here than conversions and fp16), tcgen05 with units of 128
 //   tokens (74: a unit's hand-overs between copies, conversions, scores, softmax and products
-//   take longer than its bytes; only at 64 columns 97 against 101).
+//   take longer than its bytes; at 64 columns 97).
 // decode_fp8_combine_kernel: merges the partial outputs of a segment: 2 to 2.6 us of a
 //   call, its launch included.
 #include <cuda_bf16.h>
 
+#include <cmath>
 #include <type_traits>
 
 #include "decode_shares.cuh"
@@ -87,7 +88,8 @@ struct Fp8SplitParams {
   unsigned int* status;
   unsigned long long wait_ns;
   int num_seqs, queries, Hq, Hkv, group, n_chunks, num_blocks, max_blocks_per_seq;
-  float scale_log2;       // scale * log2 e
+  int scale_exponent;     // scale * log2 e = scale_fraction * 2^scale_exponent
+  float scale_fraction;   // in [1, 2)
 };
 
 template <int D, int NT>
@@ -390,15 +392,9 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
   int buf = 0;
 #pragma unroll 1
   while (left > 0) {  // segments of this CTA's share
-    const int rows_here = rows_of(at);
-    const int chunk0 = at.chunk * kRows;  // the segment's first column
-    const int segment_row = at.seq * p.queries * p.Hq + at.head * p.group;
-    const Place here = at;
-    const bool starts = at.k == 0;
     const int n_units = kCluster ? left : min(at.units - at.k, left);
-    const bool ends = at.k + n_units == at.units;
 
-    int exponent[NT][2];  // of the power of two that columns 2t, 2t + 1 were divided by
+    int exponent[NT][2];  // of the power of two that columns 2t, 2t + 1 were divided by, and of the scores' factor
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float top = 0.f;
@@ -422,8 +418,8 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
           const uint32_t v = qb[nt][ks][x];
           qb[nt][ks][x] = pack_f16x2(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xFFFF0000u) * down);
         }
-      exponent[nt][0] = __shfl_sync(0xffffffffu, e, 8 * t);
-      exponent[nt][1] = __shfl_sync(0xffffffffu, e, 8 * t + 4);
+      exponent[nt][0] = __shfl_sync(0xffffffffu, e + p.scale_exponent, 8 * t);
+      exponent[nt][1] = __shfl_sync(0xffffffffu, e + p.scale_exponent, 8 * t + 4);
     }
 
     // Of columns 2t, 2t + 1: m and n, the references of weights and of weighted values; l,
@@ -494,17 +490,14 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
                 mma_f16_16816(c[b][nt], h0, h1, h2, h3, qb[nt][w][0], qb[nt][w][1]);
             }
           }
-          const int key_exp = static_cast<int>(s[0] >> 23 & 255u) - 127;
+          const int key_exp = static_cast<int>(s[0] >> 23 & 255u);
           value_exp[b] = static_cast<float>(static_cast<int>(s[1] >> 23 & 255u) - 127);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float f[2];  // (kept finite and above zero: a product of 0 stays one, whatever the scales)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int e = max(-126, min(127, exponent[nt][j] + key_exp));
-              f[j] = fminf(fmaxf(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23), 1.17549435e-38f),
-                           3.0e38f);
-            }
+            for (int j = 0; j < 2; ++j)
+              f[j] = p.scale_fraction * __uint_as_float(static_cast<uint32_t>(max(1, min(254, exponent[nt][j] + key_exp))) << 23);
 #pragma unroll
             for (int y = 0; y < 4; y += 2)
               f2_unpack(f2_mul(f2_pack(c[b][nt][y], c[b][nt][y + 1]), f2_pack(f[0], f[1])), c[b][nt][y], c[b][nt][y + 1]);
@@ -686,6 +679,12 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
       }
     }
 
+    const int rows_here = rows_of(at);
+    const int chunk0 = at.chunk * kRows;  // the segment's first column
+    const int segment_row = at.seq * p.queries * p.Hq + at.head * p.group;
+    const Place here = at;
+    const bool starts = at.k == 0;
+    const bool ends = at.k + n_units == at.units;
     // ---- the warps' states merge.  The staging of the segment before may still
     // be read, unless the two take turns with halves of it.
     if (!two_halves) compute_barrier();
@@ -857,7 +856,13 @@ cudaError_t launch_d(const DecodeFp8Args& a, const DeviceGuard& g, cudaStream_t 
   sp.n_chunks = plan.chunks;
   sp.num_blocks = a.num_blocks;
   sp.max_blocks_per_seq = a.max_blocks_per_seq;
-  sp.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  // (rounded once, also where the scale itself has fewer bits)
+  sp.scale_fraction = static_cast<float>(2.0 * std::frexp(static_cast<double>(a.scale) * 1.4426950408889634, &sp.scale_exponent));
+  sp.scale_exponent -= 1;
+  if (sp.scale_fraction == 2.f) {
+    sp.scale_fraction = 1.f;
+    sp.scale_exponent += 1;
+  }
   if (plan.cluster)
     return plan.rows == 8 ? launch_split<D, 1, true>(sp, plan.ctas, stream)
                           : launch_split<D, 2, true>(sp, plan.ctas, stream);

@@ -7,7 +7,7 @@ import pytest
 import fp8_reference as ref
 from exact_attention_40_gb300 import synth
 from helpers import to_dev
-from test_fp8_gpu import check_decode, env, run_append, append_case  # noqa: F401  (env: a fixture)
+from test_fp8_gpu import append_case, check_decode, decode_case, env, run_append, run_decode  # noqa: F401  (env: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -202,3 +202,14 @@ def test_drafted_tokens_taken_back(env, d):
     out, lse = ex.attn_decode_paged_fp8(to_dev(q, dev), after, to_dev(step["table"], dev), to_dev(step["ctx"], dev))
     check_decode(out, lse, q, after.cpu().numpy(), step["table"], step["ctx"], d, d ** -0.5)
     assert ex.attn_get_device_status() == 0
+
+
+@pytest.mark.parametrize("q_exp,k_exp,scale_exp", [(78, 60, -140), (-70, -56, 124), (75, 72, -149), (-110, 40, 68),
+                                                    (120, -110, -12)])
+def test_decode_factors_far_from_one(env, q_exp, k_exp, scale_exp):
+    """Queries, keys and scale whose product is ordinary, though that of two of them may pass
+    what a float's exponent holds."""
+    d = 64
+    q, cache, table, lens = decode_case(915, [70, 300], 4, 2, d, gain=2.0 ** k_exp)
+    f = synth.bf16_bits_to_f32(q) * np.float32(2.0 ** q_exp)
+    run_decode(env, (synth.f32_to_bf16_bits(f), cache, table, lens), d, scale=2.0 ** scale_exp)
