@@ -40,15 +40,15 @@
 //   Small calls take a cluster of 8 CTAs for each segment, which take its units in turn and
 //   merge through distributed shared memory: one launch, no workspace (six of up to 1500 tokens
 //   4.2 us).
-//   Measured and not taken (four queries 64.9 us then): the scores of a unit beside the products of the one before (four
-//   queries 85 us, 4096 x 200 104), two chains of a score's products (68, no change for 8 columns),
-//   two blocks a warp for 16 columns (68 to 77), the queries of 16 columns in shared memory and
-//   three CTAs (77, with spills), 16 columns as two chunks of 8 (91) or as two warps that read
-//   the same blocks (72), two warps that share their weights and split the values' columns (73;
-//   both with three CTAs), scores by mma.sync on the e4m3 keys themselves with each query as two
-//   e4m3 numbers (84: it is slower here than conversions and fp16), tcgen05 with units of 128
-//   tokens (74: a unit's hand-overs between copies, conversions, scores, softmax and products
-//   take longer than its bytes; at 64 columns 97).
+//   Measured and not taken (four queries 64.9 us then): the scores of a unit beside the products
+//   of the one before (four queries 85 us, 4096 x 200 104), two chains of a score's products
+//   (68, no change for 8 columns), two blocks a warp for 16 columns (68 to 77), the queries of
+//   16 columns in shared memory and three CTAs (77, with spills), 16 columns as two chunks of 8
+//   (91) or as two warps that read the same blocks (72), two warps that share their weights and
+//   split the values' columns (73; both with three CTAs), scores by mma.sync on the e4m3 keys
+//   themselves with each query as two e4m3 numbers (84: it is slower here than conversions and
+//   fp16), tcgen05 with units of 128 tokens (74: a unit's hand-overs between copies,
+//   conversions, scores, softmax and products take longer than its bytes; at 64 columns 97).
 // decode_fp8_combine_kernel: merges the partial outputs of a segment: 2 to 2.6 us of a
 //   call, its launch included.
 #include <cuda_bf16.h>
