@@ -45,10 +45,11 @@
 //   (68, no change for 8 columns), two blocks a warp for 16 columns (68 to 77), the queries of
 //   16 columns in shared memory and three CTAs (77, with spills), 16 columns as two chunks of 8
 //   (91) or as two warps that read the same blocks (72), two warps that share their weights and
-//   split the values' columns (73; both with three CTAs), scores by mma.sync on the e4m3 keys
-//   themselves with each query as two e4m3 numbers (84: it is slower here than conversions and
-//   fp16), tcgen05 with units of 128 tokens (74: a unit's hand-overs between copies,
-//   conversions, scores, softmax and products take longer than its bytes; at 64 columns 97).
+//   split the values' columns (73; both with three CTAs; the latter with 32 columns, for groups
+//   of 64: 187 us, 97.9 in chunks of 16), scores by mma.sync on the e4m3 keys themselves with
+//   each query as two e4m3 numbers (84: it is slower here than conversions and fp16), tcgen05
+//   with units of 128 tokens (74: a unit's hand-overs between copies, conversions, scores,
+//   softmax and products take longer than its bytes; at 64 columns 97).
 // decode_fp8_combine_kernel: merges the partial outputs of a segment: 2 to 2.6 us of a
 //   call, its launch included.
 #include <cuda_bf16.h>

@@ -213,3 +213,13 @@ def test_decode_factors_far_from_one(env, q_exp, k_exp, scale_exp):
     q, cache, table, lens = decode_case(915, [70, 300], 4, 2, d, gain=2.0 ** k_exp)
     f = synth.bf16_bits_to_f32(q) * np.float32(2.0 ** q_exp)
     run_decode(env, (synth.f32_to_bf16_bits(f), cache, table, lens), d, scale=2.0 ** scale_exp)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("S,Hq,Hkv,queries", [(1, 8, 2, 1), (1, 12, 1, 1), (5, 16, 4, 1), (3, 6, 2, 5), (9, 16, 8, 1),
+                                               (21, 10, 1, 2), (18, 16, 8, 2)])
+def test_decode_merge_of_few_and_many_rows(env, S, Hq, Hkv, queries, d):
+    """Contexts whose segments many CTAs share, of 8 to 640 rows that are merged."""
+    lens = 4200 + np.arange(S) * 37 % 900
+    lens[0] = 9001
+    run_decode(env, decode_case(916, lens, Hq, Hkv, d, queries), d)
