@@ -17,10 +17,12 @@
 //   The scales are kept out of the products: a block's key scale, a power of two, goes into
 //   the factor of its scores, and its value scale into the exponent of the weights that the
 //   second product takes.  So a code only has to become fp16, one cvt for two, and both enter
-//   exactly.  The sum of the weights has a reference m of its own, the weighted values one (n)
+//   exactly.  The sum of the weights has a reference m of its own, the weighted values one (m + n)
 //   that follows score + value exponent: whatever the blocks' scales, the largest weight of
 //   the product lies between 2^7 and 2^15, where fp16 rounds those above 2^-21 of it by at
-//   most 2^-11 of themselves and the rest by 2^-32 of it.  The sum takes the weights unrounded
+//   most 2^-11 of themselves and the rest by 2^-32 of it.  Only n, their distance, is held: it
+//   has the size of the scales' exponents, so that a score of any size meets m alone, and what
+//   the rounding of m brings is the same in both.  The sum takes the weights unrounded
 //   in fp32.  (Two exponentials a score: with one reference for both, a block of large values
 //   and small weights would be rounded away, or pass what fp16 holds.)
 //   Query tokens before the last see fewer keys: their scores are masked in the units that
@@ -103,7 +105,7 @@ struct Fp8Smem {
   uint64_t empty[kStages];       // the four warps have used it
   int present[kStages];          // bits of its blocks that were copied, kWhole where all are and are full
   float wm[2][kWarps][8 * NT];   // per-warp references (log2 units) of the weights
-  float wn[2][kWarps][8 * NT];   // ... and of the weighted values
+  float wn[2][kWarps][8 * NT];   // ... and how far that of the weighted values lies from it
   float wl[2][kWarps][8 * NT];   // per-warp sum of the weights
 };
 
@@ -423,14 +425,14 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
       exponent[nt][1] = __shfl_sync(0xffffffffu, e + p.scale_exponent, 8 * t + 4);
     }
 
-    // Of columns 2t, 2t + 1: m and n, the references of weights and of weighted values; l,
-    // the sum of this lane's tokens' weights.
+    // Of columns 2t, 2t + 1: m, the reference of the weights, and n, what the weighted values'
+    // lies above it; l, the sum of this lane's tokens' weights.
     float m[NT][2], n[NT][2], l[NT][2];
     float acc[kMTiles][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = n[nt][0] = n[nt][1] = kNoScore;
-      l[nt][0] = l[nt][1] = 0.f;
+      m[nt][0] = m[nt][1] = kNoScore;
+      n[nt][0] = n[nt][1] = l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int mt = 0; mt < kMTiles; ++mt) acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.f;
     }
@@ -530,7 +532,8 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
         // first blocks: most blocks pay one vote.  A score is rounded before the
         // reference is taken from it, as it was when it gave that: in one fused
         // operation the largest itself would lie off by the rounding, which passes all
-        // that fp16 holds once scores come to 2^28.
+        // that fp16 holds once scores come to 2^28.  y is taken from x: a sum of the
+        // score's size and the value exponent would be rounded to the score's last place.
         float x[kPer][NT][4], y[kPer][NT][4];
         auto distances = [&]() {
           float most = -INFINITY;
@@ -539,12 +542,12 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const uint64_t mm = f2_pack(m[nt][0], m[nt][1]);
-              const uint64_t nn = f2_pack(n[nt][0] - value_exp[b], n[nt][1] - value_exp[b]);
+              const uint64_t up = f2_pack(value_exp[b] - n[nt][0], value_exp[b] - n[nt][1]);
 #pragma unroll
               for (int z = 0; z < 4; z += 2) {
-                const uint64_t s = f2_pack(c[b][nt][z], c[b][nt][z + 1]);
-                f2_unpack(f2_sub(s, mm), x[b][nt][z], x[b][nt][z + 1]);
-                f2_unpack(f2_sub(s, nn), y[b][nt][z], y[b][nt][z + 1]);
+                const uint64_t above = f2_sub(f2_pack(c[b][nt][z], c[b][nt][z + 1]), mm);
+                f2_unpack(above, x[b][nt][z], x[b][nt][z + 1]);
+                f2_unpack(f2_add(above, up), y[b][nt][z], y[b][nt][z + 1]);
                 most = max3f(most, max3f(x[b][nt][z], x[b][nt][z + 1], y[b][nt][z]), y[b][nt][z + 1]);
               }
             }
@@ -555,20 +558,18 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float top = fmaxf(c[0][nt][j], c[0][nt][2 + j]), top_value = top + value_exp[0];
-              if constexpr (kPer == 2) {
-                const float other = fmaxf(c[kPer - 1][nt][j], c[kPer - 1][nt][2 + j]);
-                top = fmaxf(top, other);
-                top_value = fmaxf(top_value, other + value_exp[kPer - 1]);
-              }
+              float top[kPer];  // of each block
 #pragma unroll
-              for (int z = 4; z < 32; z *= 2) {
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
-                top_value = fmaxf(top_value, __shfl_xor_sync(0xffffffffu, top_value, z));
+              for (int b = 0; b < kPer; ++b) {
+                top[b] = fmaxf(c[b][nt][j], c[b][nt][2 + j]);
+#pragma unroll
+                for (int z = 4; z < 32; z *= 2) top[b] = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], z));
               }
-              const float mn = fmaxf(m[nt][j], top - kLift), nn = fmaxf(n[nt][j], top_value - kLift);
-              l[nt][j] *= ex2_approx(m[nt][j] - mn);
-              const float alpha = ex2_approx(n[nt][j] - nn);
+              const float mn = fmaxf(m[nt][j], fmaxf(top[0], top[kPer - 1]) - kLift);
+              const float top_value = fmaxf(top[0] - mn + value_exp[0], top[kPer - 1] - mn + value_exp[kPer - 1]);
+              const float down = m[nt][j] - mn, kept = down + n[nt][j], nn = fmaxf(kept, top_value - kLift);
+              l[nt][j] *= ex2_approx(down);
+              const float alpha = ex2_approx(kept - nn);
               m[nt][j] = mn;
               n[nt][j] = nn;
 #pragma unroll
@@ -719,18 +720,19 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
     // back to the weights', in two steps as their distance may pass what fp32's exponents
     // hold.  A share all of whose scores are -inf, or whose blocks are all missing, sees nothing.
     const int own = lane % kRows;
-    float M = kNoScore, N = kNoScore, L = 0.f, part[kWarps];
+    float M = kNoScore, N = -INFINITY, L = 0.f, part[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.wm[buf][w][own]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      M = fmaxf(M, sm.wm[buf][w][own]);
-      N = fmaxf(N, sm.wn[buf][w][own]);
+      const float down = sm.wm[buf][w][own] - M;
+      part[w] = down + sm.wn[buf][w][own];  // of its values, the reference's distance from M
+      N = fmaxf(N, part[w]);
+      L += ex2_approx(down) * sm.wl[buf][w][own];
     }
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      part[w] = ex2_approx(sm.wn[buf][w][own] - N);
-      L += ex2_approx(sm.wm[buf][w][own] - M) * sm.wl[buf][w][own];
-    }
-    const float inv = L == 0.f ? 0.f : __fdividef(1.f, L), half_way = ex2_approx(0.5f * (N - M));
+    for (int w = 0; w < kWarps; ++w) part[w] = ex2_approx(part[w] - N);
+    const float inv = L == 0.f ? 0.f : __fdividef(1.f, L), half_way = ex2_approx(0.5f * N);
     const float own_lse = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
     const bool whole = starts && ends;
     const int own_row = whole && own < rows_here ? static_cast<int>(row_of(here, own)) : 0;

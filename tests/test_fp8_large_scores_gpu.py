@@ -1,0 +1,79 @@
+"""The 8-bit decode where scores are so large that fp32 holds them in steps of 2^-4 to 2^7
+(2^20 to 2^30 and more).  What a softmax gives does not depend on the size of its scores where
+these are equal, or so far apart that all but the largest count nothing; so neither does the
+bar, which is that of test_fp8_gpu.py without its term for the rounding of scores:
+|o - ref| <= 2^-8 |ref| + 2^-10 mean|v| + n 2^-23 part.
+
+Queries have one column that is not 0, keys one value in it for all tokens of a block: a score
+is one product, and tokens with one key have one score to the last bit."""
+import numpy as np
+import pytest
+
+import fp8_reference as ref
+from exact_attention_40_gb300 import synth
+from helpers import to_dev
+from test_fp8_gpu import env  # noqa: F401  (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+VALUE_EXPONENTS = np.array([-8, -7, 4, -12, 16, 0, -3, 9, -15, -6])
+
+
+def large_case(seed, lens, columns, d, key_of_block=None, queries=None, low=20, high=31):
+    """Scores of magnitudes 2^low to 2^high, of both signs, one for each column; value scales
+    that differ from block to block.  key_of_block(b): the key's value in a sequence's block b."""
+    lens = np.asarray(lens, np.int32)
+    S = len(lens)
+    table, nb = synth.paged_layout(lens, 16, seed)
+    cache = ref.random_cache(seed, nb, 1, d)
+    codes, scales = ref.split(cache, d)
+    scales[:, 0, 1] = 2.0 ** VALUE_EXPONENTS[np.arange(nb) * 7 % 10]
+    codes[:, :, 0] = 0
+    scales[:, :, 0] = 1.0
+    at = ref.place(d)[:, 5]
+    for s in range(S):
+        for b in range((int(lens[s]) + 15) // 16):
+            value = 1.0 if key_of_block is None else key_of_block(b)
+            codes[table[s, b], 0, 0, at] = ref.codes_of(np.full(16, value), 0)
+    N = 1 if queries is None else queries
+    u = synth.uniform01(seed + 3, 3 * S * N * columns).reshape(3, S, N, columns)
+    size = 2.0 ** np.floor(low + u[0] * (high - low)) * (1 + np.floor(u[1] * 128) / 128)  # bf16 numbers
+    q = np.zeros((S, N, columns, d), np.float32)
+    q[..., 5] = np.where(u[2] < 0.5, -size, size)
+    q = synth.f32_to_bf16_bits(q)
+    return q if queries is not None else q[:, 0], cache, table, lens
+
+
+def check(env, case, d, label=""):
+    torch, ex, dev = env
+    q, cache, table, lens = case
+    out, lse = ex.attn_decode_paged_fp8(*(to_dev(x, dev) for x in case), scale=1.0)
+    torch.cuda.synchronize()
+    assert ex.attn_get_device_status() == 0
+    q4 = q if q.ndim == 4 else q[:, None]
+    want, wl, big, mean, part = ref.decode(q4, cache, table, lens, d, 1.0)
+    got, gl = out.double().cpu().numpy().reshape(want.shape), lse.double().cpu().numpy().reshape(wl.shape)
+    assert np.isfinite(got).all(), label
+    n = np.asarray(lens, np.float64)[:, None, None, None]
+    bar = 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * mean + n * 2.0 ** -23 * part[..., None]
+    err = np.abs(got - want)
+    assert (err <= bar).all(), "%s: out off by %.3e over the bar" % (label, (err - bar).max())
+    seen = np.isfinite(wl)
+    assert np.array_equal(np.isneginf(gl), ~seen) and (got[~seen] == 0).all(), label
+    bar = 2.0 ** -16 * big[seen] + 2.0 ** -19 * (1 + np.abs(wl[seen]))
+    assert (np.abs(gl[seen] - wl[seen]) <= bar).all(), label
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("S,columns", [(5, 3), (600, 2), (300, 12)])
+def test_one_token_is_its_value(env, d, S, columns):
+    """Whatever the score and the value's scale."""
+    check(env, large_case(930, np.ones(S, np.int32), columns, d), d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("S,columns,queries", [(3, 4, None), (500, 2, None), (200, 16, None), (40, 4, 4)])
+def test_equal_scores_give_the_mean_of_the_values(env, d, S, columns, queries):
+    """Contexts of one unit of work, whose blocks have scales of their own."""
+    lens = 1 + np.arange(S) * 11 % (64 if d == 128 else 128)
+    check(env, large_case(931, lens, columns, d, queries=queries), d)
