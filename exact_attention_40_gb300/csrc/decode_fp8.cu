@@ -1,6 +1,6 @@
 // One-token paged decode over the 8-bit cache (layout in fp8.cuh) for sm_103a, and the
 // decode of a few tokens of each sequence at once: split-KV partial attention plus a
-// log-sum-exp merge.
+// merge of the parts by the references and the sums of their weights.
 //
 //   s_ij = scale <q_i, kc_j> ks_j,   o_i = sum_j exp(s_ij - m_i) vs_j vc_j / sum_j exp(s_ij - m_i)
 //   with kc, vc the codes and ks, vs the scales of j's block.
@@ -85,7 +85,7 @@ struct Fp8SplitParams {
   const int32_t* ctx_lens;
   SegmentJoint* joints;  // one per CTA: its last segment, where others go on with it; or NULL
   float* ws_o;    // [2 * ctas][rows][d]
-  float* ws_lse;  // [2 * ctas][rows]
+  float2* ws_sum;  // [2 * ctas][rows]: reference (log2 units) and sum of the weights
   __nv_bfloat16* out;
   float* lse;
   unsigned int* status;
@@ -381,14 +381,19 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
   int st = 0;      // stage of the next unit
   uint32_t parity = 0;
 
-  // In a cluster: this CTA's outcome, in the ring, which every copy has left by then.
+  // In a cluster: this CTA's outcome, its weights' references and their sums, in the ring,
+  // which every copy has left by then.
   float* const cluster_o = reinterpret_cast<float*>(&sm.ring[0][0][0]);
-  float* const cluster_lse = cluster_o + kRows * D;
+  float* const cluster_ref = cluster_o + kRows * D;
+  float* const cluster_sum = cluster_ref + kRows;
   if constexpr (kCluster)
     if (left == 0)
       for (int idx = threadIdx.x; idx < kRows * D; idx += kThreads) {
         cluster_o[idx] = 0.f;
-        if (idx < kRows) cluster_lse[idx] = -INFINITY;
+        if (idx < kRows) {
+          cluster_ref[idx] = kNoScore;
+          cluster_sum[idx] = 0.f;
+        }
       }
 
   const bool two_halves = columns <= 4 * NT;  // staging rows for two segments
@@ -733,8 +738,9 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) part[w] = ex2_approx(part[w] - N);
     const float inv = L == 0.f ? 0.f : __fdividef(1.f, L), half_way = ex2_approx(0.5f * N);
-    const float own_lse = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
     const bool whole = starts && ends;
+    // the log-sum-exp, or the reference, which goes with the sum to where the parts merge
+    const float own_ref = kCluster || !whole ? M : L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
     const int own_row = whole && own < rows_here ? static_cast<int>(row_of(here, own)) : 0;
     constexpr int kRowLanes = D / 4, kAtOnce = 32 / kRowLanes;  // lanes of a row, rows of a warp
 #pragma unroll 1
@@ -751,22 +757,25 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
         o.w += wt * a.w;
       }
       const float by = __shfl_sync(0xffffffffu, inv, r), h = __shfl_sync(0xffffffffu, half_way, r);
-      const float ls = __shfl_sync(0xffffffffu, own_lse, r);
+      const float from = __shfl_sync(0xffffffffu, own_ref, r), sum = __shfl_sync(0xffffffffu, L, r);
       const int row_out = __shfl_sync(0xffffffffu, own_row, r);
       if (r >= rows_here) continue;
       auto scaled = [&](float x) { return x * by * h * h; };
       o = make_float4(scaled(o.x), scaled(o.y), scaled(o.z), scaled(o.w));
       if constexpr (kCluster) {
         *reinterpret_cast<float4*>(cluster_o + r * D + col) = o;
-        if (col == 0) cluster_lse[r] = ls;
+        if (col == 0) {
+          cluster_ref[r] = from;
+          cluster_sum[r] = sum;
+        }
       } else if (whole) {
         const size_t row = row_out;
         *reinterpret_cast<uint2*>(p.out + row * D + col) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-        if (p.lse != nullptr && col == 0) p.lse[row] = ls;
+        if (p.lse != nullptr && col == 0) p.lse[row] = from;
       } else {
         const size_t row = static_cast<size_t>(2 * cta + (starts ? 1 : 0)) * kRows + r;
         *reinterpret_cast<float4*>(p.ws_o + row * D + col) = o;
-        if (col == 0) p.ws_lse[row] = ls;
+        if (col == 0) p.ws_sum[row] = make_float2(from, sum);
       }
     }
     __syncwarp();
@@ -780,27 +789,27 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
   }
   __syncwarp();
   if constexpr (kCluster) {
-    // ---- the cluster's CTAs merge: L = log sum_i exp(lse_i), o = sum_i exp(lse_i - L) O_i
+    // ---- the cluster's CTAs merge: W = sum_i 2^(m_i - M) l_i, o = sum_i 2^(m_i - M) l_i O_i / W
     const int rows_here = rows_of(at);
     cluster_barrier();
     for (int idx = threadIdx.x * kSplitClusterCtas + rank; idx < rows_here * (D / 4); idx += kThreads * kSplitClusterCtas) {
       const int r = idx / (D / 4), col = idx % (D / 4) * 4;
-      float ls[kSplitClusterCtas];
+      float from[kSplitClusterCtas], sum[kSplitClusterCtas];
       float4 part[kSplitClusterCtas];
 #pragma unroll
       for (int i = 0; i < kSplitClusterCtas; ++i) {
-        ls[i] = cluster_load(cluster_lse + r, i);
+        from[i] = cluster_load(cluster_ref + r, i);
+        sum[i] = cluster_load(cluster_sum + r, i);
         part[i] = cluster_load4(cluster_o + r * D + col, i);
       }
-      float M = ls[0];
+      float M = from[0];
 #pragma unroll
-      for (int i = 1; i < kSplitClusterCtas; ++i) M = max_nan(M, ls[i]);
-      const float ref = M == -INFINITY ? 0.f : M;
+      for (int i = 1; i < kSplitClusterCtas; ++i) M = fmaxf(M, from[i]);
       float W = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < kSplitClusterCtas; ++i) {
-        const float w = ex2_approx((ls[i] - ref) * kLog2e);
+        const float w = ex2_approx(from[i] - M) * sum[i];
         W += w;
         o.x = fmaf(w, part[i].x, o.x);
         o.y = fmaf(w, part[i].y, o.y);
@@ -811,7 +820,7 @@ __global__ void __launch_bounds__(kCtaThreads, fp8_decode_ctas(8 * NT)) decode_f
       const size_t row = row_of(at, r);
       *reinterpret_cast<uint2*>(p.out + row * D + col) =
           make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-      if (p.lse != nullptr && col == 0) p.lse[row] = W == 0.f ? -INFINITY : M + __logf(W);
+      if (p.lse != nullptr && col == 0) p.lse[row] = W == 0.f ? -INFINITY : (M + __log2f(W)) * kLn2;
     }
     cluster_barrier();  // nobody's shared memory goes away before the others have read it
   } else {
@@ -846,7 +855,7 @@ cudaError_t launch_d(const DecodeFp8Args& a, const DeviceGuard& g, cudaStream_t 
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   sp.joints = plan.joints > 0 ? reinterpret_cast<SegmentJoint*>(ws) : nullptr;
   sp.ws_o = reinterpret_cast<float*>(ws + plan.joint_bytes());
-  sp.ws_lse = reinterpret_cast<float*>(ws + plan.joint_bytes() + plan.part_bytes(D));
+  sp.ws_sum = reinterpret_cast<float2*>(ws + plan.joint_bytes() + plan.part_bytes(D));
   sp.out = static_cast<__nv_bfloat16*>(a.out);
   sp.lse = a.lse;
   sp.status = g.status;
@@ -877,7 +886,7 @@ cudaError_t launch_d(const DecodeFp8Args& a, const DeviceGuard& g, cudaStream_t 
   cp.joints = sp.joints;
   cp.ctx_lens = a.ctx_lens;
   cp.ws_o = sp.ws_o;
-  cp.ws_lse = sp.ws_lse;
+  cp.ws_sum = sp.ws_sum;
   cp.out = sp.out;
   cp.lse = a.lse;
   cp.num_seqs = a.num_seqs;

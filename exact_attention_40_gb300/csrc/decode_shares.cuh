@@ -281,6 +281,7 @@ struct MergeParams {
   const int32_t* ctx_lens;
   const float* ws_o;
   const float* ws_lse;
+  const float2* ws_sum;  // in place of it (kMany)
   __nv_bfloat16* out;
   float* lse;
   int num_seqs, Hq, segs, n_chunks, group, max_blocks_per_seq, ctas;
@@ -299,7 +300,11 @@ struct MergeParams {
 // 8.8 with 48, 9.1 with 40).  The weights are formed once, one
 // per thread; kVecs threads take four columns each of every kTeams-th partial output,
 // the first ones' loads on their way before the weights are known.
-// kMany: a segment's columns are the heads of several query tokens (SegmentJoint).
+// kMany: a segment's columns are the heads of several query tokens (SegmentJoint), and its
+// parts come with the reference m_i (log2 units) and the sum l_i of their weights instead of
+// their lse: o = sum_i 2^(m_i - M) l_i O_i / sum_i 2^(m_i - M) l_i.  (An lse of 2^24 has no room
+// for the logarithm of the sum: parts with equal scores would weigh by a power of e, not
+// by their tokens.)
 // kCuts: CTAs that share a row, each a part of its d columns.
 template <int D, int kUnit, int kEnd, bool kFind, bool kMany, int kCuts = 1>
 __device__ __forceinline__ void merge_segment(const MergeParams& p) {
@@ -308,6 +313,7 @@ __device__ __forceinline__ void merge_segment(const MergeParams& p) {
   constexpr int kMergeWarps = kMergeThreads / 32;
   constexpr int kEarly = 3;
   __shared__ float weight[kSplitMaxCtas];
+  __shared__ float amount[kMany ? kSplitMaxCtas : 1];
   __shared__ float top[kMergeWarps], sum[kMergeWarps];
   constexpr int kSums = kCuts > 1 ? kMergeWarps : kTeams;  // (with cuts a warp's teams add up by shuffles first)
   __shared__ float4 part[kSums][kVecs];
@@ -350,9 +356,16 @@ __device__ __forceinline__ void merge_segment(const MergeParams& p) {
     early[i] = team + i * kTeams < used ? part_of(team + i * kTeams) : make_float4(0.f, 0.f, 0.f, 0.f);
   float M = -INFINITY;
   for (int s = threadIdx.x; s < used; s += kMergeThreads) {
-    const float ls = p.ws_lse[place(s)];
-    weight[s] = ls;
-    M = max_nan(M, ls);
+    if constexpr (kMany) {
+      const float2 x = p.ws_sum[place(s)];
+      weight[s] = x.x;
+      amount[s] = x.y;
+      M = fmaxf(M, x.x);
+    } else {
+      const float ls = p.ws_lse[place(s)];
+      weight[s] = ls;
+      M = max_nan(M, ls);
+    }
   }
 #pragma unroll
   for (int x = 1; x < 32; x *= 2) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, x));
@@ -364,7 +377,7 @@ __device__ __forceinline__ void merge_segment(const MergeParams& p) {
   const float ref = M == -INFINITY ? 0.f : M;  // all weights 0 where no part sees anything
   float W = 0.f;
   for (int s = threadIdx.x; s < used; s += kMergeThreads) {
-    const float w = ex2_approx((weight[s] - ref) * kLog2e);
+    const float w = kMany ? ex2_approx(weight[s] - M) * amount[s] : ex2_approx((weight[s] - ref) * kLog2e);
     weight[s] = w;
     W += w;
   }
@@ -415,7 +428,8 @@ __device__ __forceinline__ void merge_segment(const MergeParams& p) {
     const size_t row = static_cast<size_t>(joint.row) + (kMany ? at / p.group * p.Hq + at % p.group : r);
     reinterpret_cast<uint2*>(p.out + row * D)[col] =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (p.lse != nullptr && col == 0) p.lse[row] = W == 0.f ? -INFINITY : M + __logf(W);
+    if (p.lse != nullptr && col == 0)
+      p.lse[row] = W == 0.f ? -INFINITY : kMany ? (M + __log2f(W)) * kLn2 : M + __logf(W);
   }
 }
 

@@ -276,9 +276,9 @@ struct SplitPlan {
   }
   size_t joint_bytes() const { return sizeof(SegmentJoint) * joints; }
   size_t part_bytes(int d) const { return sizeof(float) * 2 * ctas * rows * d; }
-  // of the workspace: joints, partial outputs, their log-sum-exp
-  size_t bytes(int d) const {
-    return shared ? joint_bytes() + part_bytes(d) + sizeof(float) * 2 * ctas * rows : 0;
+  // of the workspace: joints, partial outputs, `floats` numbers for each of their rows
+  size_t bytes(int d, int floats) const {
+    return shared ? joint_bytes() + part_bytes(d) + sizeof(float) * floats * 2 * ctas * rows : 0;
   }
 };
 
@@ -298,6 +298,7 @@ struct Fp4Plan : SplitPlan {
   Fp4Plan(int num_seqs, int Hkv, int group, int max_blocks_per_seq)
       : SplitPlan(num_seqs, Hkv, group, max_blocks_per_seq, kFp4UnitBlocks, 1, fp4_decode_ctas(8),
                   fp4_decode_ctas(16)) {}
+  size_t bytes(int d) const { return SplitPlan::bytes(d, 1); }  // a row's log-sum-exp
 };
 
 struct DecodeFp4Args {
@@ -339,6 +340,7 @@ struct Fp8Plan : SplitPlan {
   Fp8Plan(int num_seqs, int Hkv, int columns, int max_blocks_per_seq, int d)
       : SplitPlan(num_seqs, Hkv, columns, max_blocks_per_seq, fp8_unit_blocks(d), fp8_end_units(d, columns),
                   fp8_decode_ctas(8), fp8_decode_ctas(16)) {}
+  size_t bytes(int d) const { return SplitPlan::bytes(d, 2); }  // a row's reference and sum of weights
 };
 
 struct DecodeFp8Args {
@@ -348,7 +350,7 @@ struct DecodeFp8Args {
   const int32_t* ctx_lens;
   void* out;
   float* lse;
-  void* workspace;  // joints, then partial outputs [2 ctas][rows][d] and their lse
+  void* workspace;  // joints, then partial outputs [2 ctas][rows][d], then a reference and a sum for each
   Fp8Plan plan;
   int num_seqs, queries, Hq, Hkv, d, num_blocks, max_blocks_per_seq;
   float scale;

@@ -77,3 +77,23 @@ def test_equal_scores_give_the_mean_of_the_values(env, d, S, columns, queries):
     """Contexts of one unit of work, whose blocks have scales of their own."""
     lens = 1 + np.arange(S) * 11 % (64 if d == 128 else 128)
     check(env, large_case(931, lens, columns, d, queries=queries), d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("columns", [3, 14])
+@pytest.mark.parametrize("key", ["rising", "falling", "mixed"])
+def test_scores_far_apart_give_the_largest_ones_values(env, d, columns, key):
+    """Blocks whose scores differ by a 32nd of their size and more."""
+    key_of_block = {"rising": lambda b: 1.0 + b % 8 / 8 + 8.0 * (b // 8), "falling": lambda b: 2.0 ** -(b % 9),
+                    "mixed": lambda b: 1.0 + b * 5 % 8 / 8}[key]
+    check(env, large_case(932, [60, 100, 1, 250, 33, 1000], columns, d, key_of_block), d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,columns,queries", [([1000, 77, 300], 4, None), ([1500, 90], 10, None), ([20000, 130], 4, None),
+                                                  ([9000, 2, 4500], 12, None), ([3000] * 30, 3, 2), ([400, 700, 33] * 200, 2, None)],
+                         ids=["cluster", "cluster 10", "two long", "long 12", "queries", "many"])
+def test_equal_scores_in_several_ctas_give_the_mean_of_the_values(env, d, lens, columns, queries):
+    """Their parts merge in a cluster, in a grid that finds the segments and in one that reads
+    the list of shared ones."""
+    check(env, large_case(933, lens, columns, d, queries=queries), d)
