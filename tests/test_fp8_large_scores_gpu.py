@@ -97,3 +97,26 @@ def test_equal_scores_in_several_ctas_give_the_mean_of_the_values(env, d, lens, 
     """Their parts merge in a cluster, in a grid that finds the segments and in one that reads
     the list of shared ones."""
     check(env, large_case(933, lens, columns, d, queries=queries), d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,queries", [(2, None), (12, None), (2, 3)])
+@pytest.mark.parametrize("n", [40, 300, 9000])
+def test_factors_past_what_fp32_holds(env, d, Hq, queries, n):
+    """The largest element of a query meets keys of 0, the second is 2^-20 of it: the query's
+    size, the key's scale and the scale together are 2^136 to 2^140, the scores 2^110 and 2^111.
+    The first block has the larger scale and the smaller codes, and the larger scores."""
+    shape = (1, Hq, d) if queries is None else (1, queries, Hq, d)
+    table, nb = synth.paged_layout(np.array([n], np.int32), 16, 934)
+    cache = ref.random_cache(934, nb, 1, d)
+    codes, scales = ref.split(cache, d)
+    codes[:, :, 0] = 0
+    scales[:, 0, 0] = 2.0 ** 36
+    codes[:, 0, 0, ref.place(d)[:, 9]] = 0x08  # 2^-6
+    first = table[0, 0]
+    scales[first, 0, 0] = 2.0 ** 40
+    codes[first, 0, 0, ref.place(d)[:, 9]] = 0x01  # 2^-9
+    q = np.zeros(shape, np.float32)
+    q[..., 3], q[..., 9] = 2.0 ** 100, 2.0 ** 80
+    case = synth.f32_to_bf16_bits(q), cache, table, np.array([n], np.int32)
+    check(env, case, d)
