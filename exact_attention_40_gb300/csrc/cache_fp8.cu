@@ -26,9 +26,9 @@
 namespace exattn {
 namespace {
 
-// CTAs of eight warps that share an SM.  (Calls on 64 x 256 tokens, on 2048 + 63 tokens: three
-// with a ring of two stages 62.0 and 11.6 us; two with three stages 66.7; five of four
-// warps 16.6 for the second; one with three stages, and room for no launch ahead, 76 for the first.)
+// CTAs of eight warps that share an SM: 72 registers, 73 KB each at d = 128.  (200 sequences of 16
+// more tokens, 4000 + 63 tokens: 19.1 and 16.9 us; with 76 KB, so that only two of three
+// fitted, 22.3 and 19.2; 2048 + 63 tokens 11.5 with both, 16.6 with five CTAs of four warps.)
 constexpr int kAppendCtas = 3;
 constexpr long long kAppendLarge = 16 << 20;  // bytes of rows of a large call
 constexpr int kAppendStages = 2;  // heads of a warp on their way, and the one at hand
@@ -72,10 +72,10 @@ struct AppendSmem {
   // other, so that the lanes of a token read neighbouring vectors; and where each token lies.
   float4 angles[kBlk][4][kPerTok];
   int block[kBlk], place[kBlk];
-  int upto[kThreads];     // runs of the sequences of this and earlier threads
-  Added added[kThreads];  // where a thread has one sequence
+  int upto[kThreads];  // runs of the sequences of this and earlier threads
   int warp_sum[kWarps];
 };
+static_assert(kAppendCtas * (sizeof(AppendSmem<128, 8>) + 1024) <= 228 * 1024, "CTAs of an SM by shared memory");
 
 __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.4028234663852886e38f; }
 
@@ -142,15 +142,13 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? kAppendCtas : 1)
   if constexpr (!kSingle) {
     int mine = 0;
     bool bad = false;
-    Added x = {0, 0, 0};
     for (int i = 0; i < per; ++i) {
       const int s = threadIdx.x * per + i;
       if (s >= a.num_seqs) break;
-      x = added_of(s);
+      const Added x = added_of(s);
       bad |= x.begin < 0 || x.end < x.begin || x.end > a.num_tokens;
       mine += bad ? 0 : x.runs();
     }
-    sm.added[threadIdx.x] = x;
     int sum = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -179,7 +177,6 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? kAppendCtas : 1)
     const bool past = lane < kWarps && sm.upto[kWarps * eighth + min(lane, kWarps - 1)] <= r;
     const int lo = kWarps * eighth + min(kWarps - 1, __popc(__ballot_sync(0xffffffffu, past)));
     r -= lo > 0 ? sm.upto[lo - 1] : 0;
-    if (per == 1) return sm.added[lo].run(lo, r);
     int s = lo * per;
     Added x = added_of(s);
     while (r >= x.runs() && s + 1 < a.num_seqs) {
