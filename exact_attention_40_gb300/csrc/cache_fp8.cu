@@ -31,6 +31,7 @@ namespace {
 // fitted, 22.3 and 19.2; 2048 + 63 tokens 11.5 with both, 16.6 with five CTAs of four warps.)
 constexpr int kAppendCtas = 3;
 constexpr long long kAppendLarge = 16 << 20;  // bytes of rows of a large call
+constexpr long long kAppendWide = 192 << 10;  // ... and of a run of 16 tokens with many heads
 constexpr int kAppendStages = 2;  // heads of a warp on their way, and the one at hand
 constexpr int kBlk = kDecodeBlockSize;
 constexpr int kReadLanes = 4;
@@ -505,12 +506,17 @@ cudaError_t launch_append_d(const RopeFp8Args& a, const RopeAxesTable& table, in
     while (tile < kBlk && (a.num_tokens + tile - 1) / tile * most > sms * kAppendCtas / 2) tile *= 2;
     return launch_append<D, true, 8>(a, table, sms, (a.num_tokens + tile - 1) / tile, tile, stream);
   }
-  // About as many runs as the call can have.  Large calls whose runs fill one CTA an SM or
-  // many take CTAs of 16 warps, each run's tokens in longer stretches: 64 x 256 tokens (32 + 2 x 8
-  // heads of 128) 59.9 us, 62.0 with three of eight; 2048 tokens 9.7 and 11.1; but 2048 tokens
-  // and 63 single ones 13.7 and 11.6, and small calls lose the overlap (64 tokens 3.0 and 2.7).
+  // About as many runs as the call can have.  Large calls whose runs fill one CTA an SM, or
+  // many where the runs are wide, take CTAs of 16 warps, each run's tokens in longer stretches:
+  // 64 x 256 tokens (32 + 2 x 8 heads of 128) 60.1 us, 65.6 with three of eight; 2048 tokens 9.7
+  // and 11.0; but 2048 tokens and 63 single ones 13.7 and 11.5, and small calls lose the overlap
+  // (64 tokens 3.0 and 2.7).  Beside the borders, 16 warps and eight: 80 runs of 192 KB 8.4 both, 100
+  // 9.4 and 9.1, 128 9.2 and 10.0, 190 16.9 and 15.5, 456 28.7 and 27.9, 500 34.7 and 32.9, 608
+  // 37.0 and 37.9; 1024 of 160 KB (64 + 2 x 8 heads of 64) 62.4 and 57.3, of 72 KB 36.4 and 26.4,
+  // of 320 KB 107 both.
   const long long runs = a.num_tokens / kBlk + (a.num_seqs < a.num_tokens ? a.num_seqs : a.num_tokens);
-  if (a.num_tokens * items * D * 2 > kAppendLarge && (runs <= sms || runs > sms * kAppendCtas))
+  if (a.num_tokens * items * D * 2 > kAppendLarge &&
+      (runs <= sms || (runs > sms * kAppendCtas && kBlk * items * D * 2 >= kAppendWide)))
     return launch_append<D, false, 16>(a, table, sms, runs, 1, stream);
   return launch_append<D, false, 8>(a, table, sms, runs, 1, stream);
 }
