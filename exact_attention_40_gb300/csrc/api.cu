@@ -911,6 +911,8 @@ int attn_rope_cache_write_fp8(const void* q, const void* k, const void* v, void*
   int rc = quantised_sizes(Hkv, d, num_blocks, num_seqs, max_blocks_per_seq);
   if (rc != EXATTN_OK) return rc;
   if (Hq > 65535 || Hkv > 65535 || num_seqs > 65535) return EXATTN_ERR_UNSUPPORTED;
+  // (a sequence's tokens, the places before them in its first block and what rounds up to blocks)
+  if (num_tokens > kMaxTokens - 2 * exattn::kDecodeBlockSize) return EXATTN_ERR_UNSUPPORTED;
   exattn::RopeAxesTable table;
   if ((rc = rope_table(sections, num_axes, d, base, per_axis, &table)) != EXATTN_OK) return rc;
   if (token_starts == nullptr && num_tokens != num_seqs) return EXATTN_ERR_INVALID_ARG;

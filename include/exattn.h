@@ -460,7 +460,7 @@ size_t attn_fp8_cache_bytes(int num_blocks, int Hkv, int d);
  * new tokens in one block.  Tokens whose places or table entries lie outside the table or
  * the cache are rotated in q_out but store nothing, and set EXATTN_DEVICE_BOUNDS_BIT.
  * token_starts that decrease or leave 0 .. num_tokens set it too, and nothing is written.
- * num_seqs <= 65535; num_tokens >= 0 (0 launches nothing).  One launch on `stream`,
+ * num_seqs <= 65535; 0 <= num_tokens < 2^31 - 32 (0 launches nothing).  One launch on `stream`,
  * asynchronous, deterministic; the call can be captured into a CUDA graph, whose replays
  * follow the contents of token_starts and ctx_lens.
  */
