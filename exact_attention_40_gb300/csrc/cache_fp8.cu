@@ -179,10 +179,17 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? kAppendCtas : 1)
     const int lo = kWarps * eighth + min(kWarps - 1, __popc(__ballot_sync(0xffffffffu, past)));
     r -= lo > 0 ? sm.upto[lo - 1] : 0;
     int s = lo * per;
-    Added x = added_of(s);
+    // (the numbers are read a second time: if another stream changes them meanwhile the result is
+    // undefined, but every row that comes out is one of the call)
+    auto within = [&] {
+      const Added x = added_of(s);
+      return Added{max(0, x.begin), min(a.num_tokens, x.end), x.ctx};
+    };
+    Added x = within();
     while (r >= x.runs() && s + 1 < a.num_seqs) {
       r -= x.runs();
-      x = added_of(++s);
+      ++s;
+      x = within();
     }
     return x.run(s, r);
   };
