@@ -457,9 +457,11 @@ size_t attn_fp8_cache_bytes(int num_blocks, int Hkv, int d);
  * Rows of the call that belong to no sequence (before token_starts[0], from
  * token_starts[num_seqs] on) are neither read nor written; a batch that is padded to a
  * captured size gives its unused sequences no tokens (equal starts).  Two sequences must not have
- * new tokens in one block.  token_starts and ctx_lens keep their values while the call runs.
- * Tokens whose places or table entries lie outside the table or the cache are rotated in
- * q_out but store nothing, and set EXATTN_DEVICE_BOUNDS_BIT.
+ * new tokens in one block, and a block that is shared for a common prefix and not yet full has to
+ * be copied before one of its sequences appends to it: the append may bring all of it to a
+ * larger scale, for whoever reads it.  token_starts and ctx_lens keep their values while the
+ * call runs.  Tokens whose places or table entries lie outside the table or the cache are
+ * rotated in q_out but store nothing, and set EXATTN_DEVICE_BOUNDS_BIT.
  * token_starts that decrease or leave 0 .. num_tokens set it too, and nothing is written.
  * num_seqs <= 65535; 0 <= num_tokens < 2^31 - 32 (0 launches nothing).  One launch on `stream`,
  * asynchronous, deterministic; the call can be captured into a CUDA graph, whose replays
