@@ -9,12 +9,15 @@
 //   each lane's own (cp.async), one head ahead, through all runs of the CTA.  Keys are turned
 //   twice, for their magnitude and for their codes, which costs less than registers that would
 //   keep them.
-//   Bound by HBM: 64 x 256 tokens (32 + 2 x 8 heads of 128; 202 MB read, 168 written): 59.9 us =
+//   Bound by HBM: 64 x 256 tokens (32 + 2 x 8 heads of 128; 202 MB read, 168 written): 60.1 us =
 //   6.2 TB/s, 91% of a copy.  Long stretches of a token's row at once are worth more than
 //   balance: with the heads of each run divided among CTAs 68 us and more, with those of the
 //   last round of runs 69.  Small calls are one round of dependent loads (64 tokens of 64
 //   sequences 2.7 us, one token 2.5; five chunks of 1 to 333 tokens, 14 + 2 x 2 heads of 64, whose
-//   runs are counted first, 3.9).
+//   runs are counted first, 3.9).  Where a block's scale grows, its other codes are read and
+//   written too, by the eight lanes of a token (four at d = 64) or by the warp of a run: 64 tokens
+//   that all let both scales of their blocks grow 9.3 us, 3.1 without (512 of them 31 and 6.6; four
+//   new tokens of each of 64 sequences 5.8 and 4.8).
 // cache_read_fp8_kernel: below.
 #include <cuda_bf16.h>
 

@@ -32,16 +32,18 @@
 //   heads over 8 of 128: 164 to 168 us = 6.4 to 6.6 TB/s, 95 to 97% of a copy; 64 sequences of 512
 //   to 8192 tokens 92.3 us = 6.2 TB/s with the merge).  A unit takes a warp 1100 cycles
 //   (scores 370, distances and vote 100, products 360, the rest waits), which twelve warps an SM
-//   overlap.  For 9 to 16 columns 168 registers leave room for eight computing warps, whose
-//   units take 1390 cycles (440, 150, 485), and their latency bounds it: 32 sequences of 512 to
-//   8192 tokens, 96 heads over 8: 59.0 us; four queries of 32 heads over 8: 63.6 us = 4.5 TB/s.
-//   Chunks of 16 columns read the keys and values once each (64 columns, 16 sequences of 4000
-//   tokens: 97.9 us).  Short contexts pay for the ends of their segments, 1450 to 4500 cycles
-//   (4096 sequences of 200 tokens, 8 heads over 2: 89.1 us), few of them for the chain
-//   ctx_lens -> table -> copies -> merge (one of 32768 tokens 15.9 us, its bytes' time 9.9).
+//   overlap.  For 9 to 16 columns 168 registers (and, at d = 128, 88 bytes of spills a thread; 28
+//   in a cluster) leave room for eight computing warps, whose units take 1390 cycles (440, 150,
+//   485), and their latency bounds it: 32 sequences of 512 to 8192 tokens, 96 heads over 8:
+//   59.3 us; four queries of 32 heads over 8: 63.6 us = 4.5 TB/s.  More than 16 columns are
+//   chunks of 16, each of which reads, converts and multiplies all keys and values again
+//   (64 columns, 16 sequences of 4000 tokens: 97.9 us, their bytes' time 20).  Short contexts pay
+//   for the ends of their segments, 1450 to 4500 cycles (4096 sequences of 200 tokens, 8 heads
+//   over 2: 90.2 us), few of them for the chain ctx_lens -> table -> copies -> merge (one of
+//   32768 tokens 16.1 us, its bytes' time 9.9).
 //   Small calls take a cluster of 8 CTAs for each segment, which take its units in turn and
 //   merge through distributed shared memory: one launch, no workspace (six of up to 1500 tokens
-//   4.2 us).
+//   4.3 us).
 //   Measured and not taken (four queries 64.9 us then): the scores of a unit beside the products
 //   of the one before (four queries 85 us, 4096 x 200 104), two chains of a score's products
 //   (68, no change for 8 columns), two blocks a warp for 16 columns (68 to 77), the queries of

@@ -329,7 +329,7 @@ constexpr __host__ __device__ int fp8_end_units(int d, int rows) { return rows >
 
 // CTAs of the 8-bit decode that share an SM, for segments of `rows` columns: three of four
 // computing warps and three units of shared memory, or two with four units where 16 columns
-// take 168 registers.  (Without a copying warp, each warp copying its own blocks, four and
+// take 168 registers and, at d = 128, spill 88 bytes.  (Without a copying warp, each warp copying its own blocks, four and
 // three fit and are slower: a batch of 64 sequences 98 us against 92, four queries of 32 sequences
 // 81 against 65.)
 constexpr __host__ __device__ int fp8_decode_ctas(int rows) { return rows > 8 ? 2 : 3; }

@@ -501,7 +501,8 @@ def attn_rope_cache_write_fp8(q, k, v, token_starts, ctx_lens, positions, block_
     [S,max_blocks]; sections, base, per_axis as attn_rope_axes.  q_out may be q.
 
     Returns q_out, the rotated queries (contiguous where not given).  Rows that
-    belong to no sequence are left as they are."""
+    belong to no sequence are left as they are.  A part-filled block that sequences
+    share has to be copied before one of them appends to it."""
     return (_native or _load_native()).rope_cache_write_fp8(q, k, v, token_starts, ctx_lens, positions, block_table,
                                                             kv_cache, sections, base, per_axis, q_out, stream)
 
