@@ -60,7 +60,7 @@ struct Added {
     x.seq = seq;
     x.token = begin + from;
     x.place = r == 0 ? phase() : 0;
-    x.count = min(kBlk - x.place, end - x.token);
+    x.count = max(0, min(kBlk - x.place, end - x.token));  // (0 only where the numbers changed meanwhile)
     x.slot = static_cast<long long>(ctx) - (end - begin) + from;
     return x;
   }
