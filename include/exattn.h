@@ -491,7 +491,8 @@ int attn_cache_read_fp8(const void* kv_cache, const int32_t* seq_ids, const int3
  * Keys and values enter exactly; a weight is rounded by at most 2^-11 of itself or
  * 2^-32 of the largest product of a weight and its block's value scale, whichever is
  * more.  A query that sees no token gets out = 0, lse = -inf.  What a query does not see
- * has no part in its output, NaN included.  out overlaps no input, and
+ * has no part in its output, NaN included.  Scores are held in fp32: a head of a query one of
+ * whose scores is past its largest number gets NaN.  out overlaps no input, and
  * ctx_lens keep their values while the call runs.  scale and 2 scale are finite and > 0;
  * 1 <= num_queries <= 16.
  *   workspace: attn_decode_fp8_workspace_bytes(...) bytes, 16-byte aligned, its

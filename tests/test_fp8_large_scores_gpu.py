@@ -120,3 +120,21 @@ def test_factors_past_what_fp32_holds(env, d, Hq, queries, n):
     q[..., 3], q[..., 9] = 2.0 ** 100, 2.0 ** 80
     case = synth.f32_to_bf16_bits(q), cache, table, np.array([n], np.int32)
     check(env, case, d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [40, 300, 9000])
+def test_scores_past_fp32_are_nan_in_their_head_alone(env, d, n):
+    torch, ex, dev = env
+    q, cache, table, lens = large_case(935, [n], 3, d, low=20, high=24)
+    huge = synth.bf16_bits_to_f32(q)
+    huge[0, 1, 5] = 2.0 ** 100
+    scales = ref.split(cache, d)[1]
+    scales[table[0, 0], 0, 0] = 2.0 ** 40  # the first block's score: 2^140
+    args = [to_dev(x, dev) for x in (cache, table, lens)]
+    want, want_lse = ex.attn_decode_paged_fp8(to_dev(q, dev), *args, scale=1.0)
+    out, lse = ex.attn_decode_paged_fp8(to_dev(synth.f32_to_bf16_bits(huge), dev), *args, scale=1.0)
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
+    for h in (0, 2):
+        assert torch.equal(out[0, h], want[0, h]) and torch.equal(lse[0, h], want_lse[0, h])
+    assert torch.isfinite(want[0, [0, 2]]).all() and ex.attn_get_device_status() == 0
